@@ -407,6 +407,213 @@ CSGMV_API int extra_token_embedding(const int32_t *input_ids, void *output, int6
                                     const void *extra_embeddings, int64_t num_extra_tokens, int64_t vocab_size,
                                     const csgmv_batch_info *bi, csgmv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The serving step around the adapters: a paged K/V cache, attention of a
+ * tree of drafted tokens over it, verification of the drafts, and the cache's
+ * page bookkeeping (additions of this library; the pages stop at the
+ * projections).  The conventions above hold: device pointers, the given
+ * stream, nothing allocated, nothing synchronized.
+ * ------------------------------------------------------------------------ */
+
+/* csgmv_kv_cache.dtype also takes IEEE half. */
+enum { CSGMV_DTYPE_F16 = 2 };
+
+/* Bits of csgmv_kv_cache.status and of the status words below.  Device-side
+ * problems are OR-ed in and the offending request is left out; a status word
+ * is never reset by the library. */
+enum {
+    CSGMV_KV_STATUS_BAD_SEQ = 1,   /* sequence slot out of range, used twice, or (fork) not empty */
+    CSGMV_KV_STATUS_BAD_PAGE = 2,  /* page number out of range, or a reference count that would go below zero */
+    CSGMV_KV_STATUS_CAPACITY = 4,  /* no free pages left, or a row of the page table is full */
+    CSGMV_KV_STATUS_BAD_LENS = 8,  /* negative or inconsistent lengths */
+    CSGMV_KV_STATUS_BAD_TREE = 16, /* a parent that does not come before its child, or a bad node number */
+    CSGMV_KV_STATUS_BAD_TOKEN = 32 /* a drafted token outside the vocabulary, or a distribution without mass */
+};
+
+/*
+ * A paged K/V cache: num_pages pages of page_size tokens for every layer,
+ * handed out to at most max_seqs sequences.  Element (layer l, page p, head
+ * h, token slot t, d) of k_pages and of v_pages is at
+ *     l * layer_stride + p * page_stride + h * head_stride + t * token_stride + d
+ * (strides in elements, multiples of 8).  Token i of sequence s is in slot
+ * i % page_size of page page_table[s * max_pages_per_seq + i / page_size].
+ * page_refs[p] counts the sequences that hold page p; a page is free when it
+ * is 0, and pages are given out lowest first.  The caller allocates every
+ * buffer; an empty cache has seq_lens = 0, page_refs = 0 and page_table = -1.
+ */
+typedef struct csgmv_kv_cache {
+    void *k_pages, *v_pages;
+    int32_t *page_table; /* [max_seqs][max_pages_per_seq]; -1 past a sequence's pages */
+    int32_t *seq_lens;   /* [max_seqs] tokens held */
+    int32_t *page_refs;  /* [num_pages] */
+    int32_t *scratch;    /* [csgmv_kv_scratch_ints()]; contents do not matter between calls */
+    int32_t *status;     /* [1] CSGMV_KV_STATUS_* bits */
+    int64_t layer_stride, page_stride, head_stride, token_stride;
+    int32_t dtype;       /* CSGMV_DTYPE_BF16 or CSGMV_DTYPE_F16 */
+    int32_t num_layers, num_pages, page_size, num_kv_heads, head_dim, max_seqs, max_pages_per_seq;
+} csgmv_kv_cache;
+
+/* int32 entries of csgmv_kv_cache.scratch.  Host only; 0 for negative sizes. */
+CSGMV_API int64_t csgmv_kv_scratch_ints(int num_pages, int max_seqs);
+
+/*
+ * Appends tokens to sequences, in every layer.  Request b appends
+ * accept_len[b] tokens to sequence seq_slots[b] (b itself when seq_slots is
+ * NULL): its j-th is row tree_indptr[b] + accept_index[b * accept_width + j]
+ * of k_new and v_new.  Pages are taken as needed; a partly filled last page
+ * that another sequence holds too is first replaced by a copy of its own.
+ *   k_new, v_new   dtype of the cache; element (layer l, row t, head h, d) at
+ *                  l * new_layer_stride + t * new_token_stride + h * new_head_stride + d
+ *                  (strides in elements, multiples of 8); num_tokens rows
+ *   accept_index   [bs][accept_width]; node numbers inside the request, each
+ *                  in [0, tree_indptr[b+1] - tree_indptr[b]); NULL for 0, 1, 2, ...
+ *                  (accept_width is then ignored)
+ *   accept_len     [bs]
+ * A request with a bad slot, length or node number, or without room in its
+ * row of the page table, is left out; when the free pages do not suffice for
+ * the whole batch nothing is appended at all (CSGMV_KV_STATUS_CAPACITY).
+ * A sequence may appear once in a batch.  bs <= max_seqs.
+ */
+CSGMV_API int csgmv_kv_commit(const csgmv_kv_cache *kv, const void *k_new, const void *v_new, int64_t new_layer_stride,
+                              int64_t new_token_stride, int64_t new_head_stride, int64_t num_tokens,
+                              const int32_t *accept_index, int accept_width, const int32_t *accept_len,
+                              const int32_t *tree_indptr, const int32_t *seq_slots, int bs, csgmv_stream_t stream);
+
+/*
+ * children[i] becomes a copy of sequence parents[i], for i < n: whole pages
+ * are shared (their count goes up), a partly filled last page is copied into
+ * a fresh one in every layer.  A child must be empty, may appear once, and
+ * may not be a parent in the same call; an entry that breaks this is left out
+ * (CSGMV_KV_STATUS_BAD_SEQ).  Without enough free pages nothing is forked.
+ * n <= max_seqs.
+ */
+CSGMV_API int csgmv_kv_fork(const csgmv_kv_cache *kv, const int32_t *parents, const int32_t *children, int n,
+                            csgmv_stream_t stream);
+
+/*
+ * Cuts sequence seqs[i] back to keep_lens[i] tokens (to none when keep_lens
+ * is NULL) and gives up its pages past them: their counts go down, their
+ * page-table entries become -1.  A sequence no longer than that is left as it
+ * is.  A page that stays partly used by it may then be shared; appending to the
+ * sequence copies such a page first (csgmv_kv_commit).  A sequence listed
+ * twice is cut to the smaller length.  n <= max_seqs.
+ */
+CSGMV_API int csgmv_kv_free(const csgmv_kv_cache *kv, const int32_t *seqs, const int32_t *keep_lens, int n,
+                            csgmv_stream_t stream);
+
+/*
+ * Moves every live page whose number is at least the count of live pages into
+ * a hole below it (k-th such page into the k-th hole), in every layer, and
+ * rewrites page_refs and the page tables: afterwards the live pages are
+ * 0 .. live - 1.
+ */
+CSGMV_API int csgmv_kv_compact(const csgmv_kv_cache *kv, csgmv_stream_t stream);
+
+/*
+ * Copies the contents of page src[i] to page dst[i] in every layer, i < n.
+ * No page may be both a source and a destination or a destination twice;
+ * pairs with a page out of range are left out (CSGMV_KV_STATUS_BAD_PAGE).
+ */
+CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, const int32_t *dst, int n,
+                                  csgmv_stream_t stream);
+
+/*
+ * Attention of the drafted tokens of each request over its sequence and its
+ * own tree.  Request b owns rows [tree_indptr[b], tree_indptr[b+1]) of q,
+ * k_new, v_new and out, and sequence s = seq_slots[b] (b when NULL) of the
+ * cache.  For row t of the request, query head h and kv head
+ * g = h / (num_q_heads / num_kv_heads),
+ *     a_i = scale * q[t][h] . K_i,   out[t][h] = sum_i softmax(a)_i V_i,
+ *     lse[t][h] = log sum_i exp(a_i)
+ * over the tokens i of sequence s in layer `layer` of the cache, and over the
+ * request's own rows j whose bit is set in row t of `mask`.  A row that sees
+ * no token gives out = 0 and lse = -inf.  What is masked has no influence,
+ * whatever it holds (infinities and NaN too, and slots past a sequence's end).
+ *   q, out         dtype of the cache; element (t, h, d) at t * q_token_stride
+ *                  + h * q_head_stride + d (out_* for out; multiples of 8)
+ *   k_new, v_new   element (t, g, d) at t * new_token_stride + g * new_head_stride + d
+ *   lse            f32 [num_tokens][num_q_heads], or NULL
+ *   mask           int32 [num_tokens][mask_words]: bit j % 32 of word j / 32 of
+ *                  row t lets t see row j of its request; a request has at most
+ *                  32 * mask_words rows.  NULL: row t sees rows 0 .. t (any
+ *                  number of rows: plain decoding and prompts)
+ * head_dim 64 or 128; num_q_heads a multiple of num_kv_heads, at most 128
+ * times it; page_size a power of two >= 8.  One row for each request is plain
+ * decoding.  The products have the inputs' type, sums are fp32; the softmax
+ * weights are rounded to the inputs' type before they meet V, as the tensor
+ * cores take them.  Results do not depend on timing.
+ *   workspace      csgmv_tree_attention_workspace_bytes(); contents do not matter
+ */
+CSGMV_API int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads,
+                                   const void *k_new, const void *v_new, int64_t new_token_stride,
+                                   int64_t new_head_stride, const csgmv_kv_cache *kv, int layer,
+                                   const int32_t *tree_indptr, const int32_t *seq_slots, int bs, int64_t num_tokens,
+                                   const int32_t *mask, int mask_words, float scale, void *out,
+                                   int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                                   size_t workspace_bytes, csgmv_stream_t stream);
+
+/* Workspace bytes of csgmv_tree_attention: independent of the batch. */
+CSGMV_API size_t csgmv_tree_attention_workspace_bytes(const csgmv_kv_cache *kv, int num_q_heads);
+
+/*
+ * Derived fields of a batch of draft trees.  Node i of request b is row
+ * tree_indptr[b] + i; parents[row] is its parent's number inside the request,
+ * smaller than i, and -1 for node 0 (the root: the last accepted token) only.
+ *   mask          [num_nodes][mask_words]: the node itself and its ancestors
+ *                 (csgmv_tree_attention's mask)
+ *   depth         [num_nodes]: 0 at the root (a token's position is its
+ *                 sequence's length plus its depth)
+ *   first_child, next_sibling   [num_nodes]: node numbers in increasing order
+ *                 of siblings, -1 for none
+ * A request with a bad parent or more than 32 * mask_words nodes gets an empty
+ * mask, depth 0 and no children (CSGMV_KV_STATUS_BAD_TREE).  mask_words <= 8.
+ */
+CSGMV_API int csgmv_build_draft_tree(const int32_t *parents, const int32_t *tree_indptr, int bs, int64_t num_nodes,
+                                     int mask_words, int32_t *mask, int32_t *depth, int32_t *first_child,
+                                     int32_t *next_sibling, int32_t *status, csgmv_stream_t stream);
+
+/*
+ * Verification of drafted tokens: a walk from the root of each tree that
+ * keeps a prefix of accepted tokens and draws one more, so that every token is
+ * distributed as the target says.  At node c with target distribution
+ * p = target_probs[c] and children x_1, x_2, ... in order:
+ *   - with draft_probs (children drawn independently from q = draft_probs[c]):
+ *     r = p, z = 1; child k is accepted if (u_k * q(x_k)) * z < r(x_k), with
+ *     u_k = accept_uniforms of the child; otherwise r = max(r - z * q, 0),
+ *     z = sum r, and the next child is tried while z > 0;
+ *   - without (children chosen by the drafter, distinct tokens): child k is
+ *     accepted if u < p(x_1) + ... + p(x_k), with u = accept_uniforms of c;
+ *     otherwise r = p without the children's tokens (a token that an earlier
+ *     sibling has already is passed over).
+ * The walk goes on at an accepted child.  When no child is accepted, next_token
+ * is the first token whose running sum of r exceeds sample_uniforms[b] times
+ * the total (of p where r is empty).
+ * Sums and the comparisons of sums are exact: a probability, clamped to
+ * [0, 1], counts in whole steps of 2^-44 (rounded down), a uniform number in
+ * steps of 2^-44 against a sum of p and of 2^-31 for the draw; r, u * q * z
+ * are fp32, each operation rounded.  So results do not depend on the order of
+ * summation.
+ *   target_probs, draft_probs   f32, row of a node at target_stride / draft_stride
+ *                  elements; draft_probs may be NULL
+ *   draft_tokens   [num_nodes] (the root's is not used)
+ *   first_child, next_sibling   from csgmv_build_draft_tree
+ *   accept_uniforms [num_nodes], sample_uniforms [bs]   in [0, 1)
+ *   accept_index   [bs][accept_width]: node numbers of the accepted path, the
+ *                  root first, then -1
+ *   accept_len     [bs]: nodes on the path (1 when no draft was accepted)
+ *   next_token     [bs]
+ * A request without nodes, or whose path is longer than accept_width
+ * (CSGMV_KV_STATUS_CAPACITY), gets accept_len = 0 and next_token = -1, as does
+ * one whose last distribution has no mass (BAD_TOKEN: next_token = -1 only).
+ * 1 <= vocab_size <= 2^18.
+ */
+CSGMV_API int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const float *draft_probs,
+                                  int64_t draft_stride, const int32_t *draft_tokens, const int32_t *tree_indptr,
+                                  const int32_t *first_child, const int32_t *next_sibling,
+                                  const float *accept_uniforms, const float *sample_uniforms, int bs,
+                                  int64_t num_nodes, int vocab_size, int32_t *accept_index, int accept_width,
+                                  int32_t *accept_len, int32_t *next_token, int32_t *status, csgmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,16 +16,26 @@ LIB_PATH = os.path.join(_HERE, "libcsgmv.so")
 
 CSGMV_DTYPE_BF16 = 0
 CSGMV_DTYPE_F32 = 1
+CSGMV_DTYPE_F16 = 2
 
 STATUS_BITS = {
     1: "BAD_ADAPTER", 2: "BAD_RANK", 4: "BAD_TOKEN_ID", 8: "BAD_PERMUTATION", 16: "CAPACITY", 32: "BAD_LENS",
+}
+
+# bits of KvCache.status and DraftTree.status (CSGMV_KV_STATUS_*; 1 << 30: a
+# bounded wait inside a kernel ran out)
+KV_STATUS_BITS = {
+    1: "BAD_SEQ", 2: "BAD_PAGE", 4: "CAPACITY", 8: "BAD_LENS", 16: "BAD_TREE", 32: "BAD_TOKEN", 1 << 30: "TIMEOUT",
 }
 
 EXPORTED = ["csgmv_last_error", "csgmv_version", "csgmv_chunk_size", "csgmv_batch_info_capacity",
             "csgmv_build_batch_info", "csgmv_build_lm_head_batch_info", "csgmv_shrink", "csgmv_expand", "csgmv_qkv", "csgmv_qkv_workspace_bytes",
             "csgmv_qkv_static_scratch", "embedding_lora_a", "embedding_lora_a_extra", "extra_token_embedding",
             "csgmv_expand_sliced", "csgmv_qkv_sliced", "csgmv_qkv_path", "csgmv_tile_table_ints",
-            "embedding_lora_a_transposed", "csgmv_transpose_embedding"]
+            "embedding_lora_a_transposed", "csgmv_transpose_embedding",
+            "csgmv_kv_scratch_ints", "csgmv_kv_commit", "csgmv_kv_fork", "csgmv_kv_free", "csgmv_kv_compact",
+            "csgmv_kv_copy_pages", "csgmv_tree_attention", "csgmv_tree_attention_workspace_bytes",
+            "csgmv_build_draft_tree", "csgmv_verify_drafts"]
 
 # csgmv_qkv_path results (CSGMV_PATH_*)
 PATHS = {0: "fused", 1: "decode", 2: "small_split", 3: "stream"}
@@ -47,6 +57,15 @@ class _BatchInfoC(ctypes.Structure):
         ("tile_table", ctypes.c_void_p)]
 
 
+class _KvCacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_pages", "v_pages", "page_table", "seq_lens", "page_refs", "scratch", "status")] + [
+        (n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "head_stride", "token_stride")] + [
+        (n, ctypes.c_int32) for n in (
+            "dtype", "num_layers", "num_pages", "page_size", "num_kv_heads", "head_dim", "max_seqs",
+            "max_pages_per_seq")]
+
+
 _lib = None
 
 
@@ -62,6 +81,8 @@ def lib():
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     i32p = ctypes.POINTER(ctypes.c_int32)
     bip = ctypes.POINTER(_BatchInfoC)
+    kvp = ctypes.POINTER(_KvCacheC)
+    f32, size_t = ctypes.c_float, ctypes.c_size_t
     sig = {
         "csgmv_last_error": (ctypes.c_char_p, []),
         "csgmv_version": (ctypes.c_char_p, []),
@@ -84,6 +105,18 @@ def lib():
         "csgmv_tile_table_ints": (i64, [i32, i32]),
         "embedding_lora_a_transposed": (i32, [vp, vp, i64, i32, vp, i64, vp, bip, vp]),
         "csgmv_transpose_embedding": (i32, [vp, i64, i32, i64, vp, vp]),
+        "csgmv_kv_scratch_ints": (i64, [i32, i32]),
+        "csgmv_kv_commit": (i32, [kvp, vp, vp, i64, i64, i64, i64, vp, i32, vp, vp, vp, i32, vp]),
+        "csgmv_kv_fork": (i32, [kvp, vp, vp, i32, vp]),
+        "csgmv_kv_free": (i32, [kvp, vp, vp, i32, vp]),
+        "csgmv_kv_compact": (i32, [kvp, vp]),
+        "csgmv_kv_copy_pages": (i32, [kvp, vp, vp, i32, vp]),
+        "csgmv_tree_attention": (i32, [vp, i64, i64, i32, vp, vp, i64, i64, kvp, i32, vp, vp, i32, i64, vp, i32, f32,
+                                       vp, i64, i64, vp, vp, size_t, vp]),
+        "csgmv_tree_attention_workspace_bytes": (size_t, [kvp, i32]),
+        "csgmv_build_draft_tree": (i32, [vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp]),
+        "csgmv_verify_drafts": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, vp, i32, vp, vp, vp,
+                                      vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -348,3 +381,272 @@ def csgmv_qkv_sliced(x: torch.Tensor, A: torch.Tensor, B_slices, slice_offsets, 
                                   _offsets(slice_offsets), int(num_slices), int(max_slice_size), _ptr(base_output),
                                   _ptr(workspace), ws_bytes, ctypes.byref(bi.c), _stream(stream)))
     return base_output
+
+
+# ---------------------------------------------------------------------------
+# The serving step around the adapters: paged K/V cache, attention of draft
+# trees, draft verification (include/csgmv.h has each call's contract).
+
+_KV_DTYPES = {torch.bfloat16: CSGMV_DTYPE_BF16, torch.float16: CSGMV_DTYPE_F16}
+
+
+def _need(ok: bool, msg: str):
+    """Checks that only the binding can make (a tensor's type and shape, which
+    the C ABI does not see) fail as the library's own argument checks do."""
+    if not ok:
+        raise CsgmvError(-1, msg)
+
+
+def _need_i32(name: str, t: torch.Tensor | None, *shape):
+    """t is a dense int32 tensor on a GPU of that shape (None: any extent)."""
+    if t is None:
+        return
+    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous int32 CUDA tensor")
+    _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)),
+          f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _need_f32(name: str, t: torch.Tensor, *shape):
+    _need(t.dtype == torch.float32 and t.is_cuda, f"{name} must be a float32 CUDA tensor")
+    _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)),
+          f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _alike(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Same shape and the same strides where they matter."""
+    return a.shape == b.shape and (a.numel() == 0 or all(
+        n <= 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride())))
+
+
+class KvCache:
+    """A paged K/V cache over caller-owned tensors, and the C struct that
+    points at them.
+
+      k_pages, v_pages   bf16 or f16, (layers, pages, kv_heads, page_size, head_dim)
+                         ("HND") or (layers, pages, page_size, kv_heads, head_dim)
+                         ("NHD"); any strides that are multiples of 8, the last 1
+      page_table         int32 (max_seqs, max_pages_per_seq), -1 where empty
+      seq_lens           int32 (max_seqs,)
+      page_refs          int32 (pages,)
+
+    KvCache.allocate() makes an empty cache with its own tensors."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                 page_refs: torch.Tensor, layout: str = "HND"):
+        _need(layout in ("HND", "NHD"), f"layout {layout!r} must be HND or NHD")
+        _need(k_pages.dtype in _KV_DTYPES and v_pages.dtype == k_pages.dtype, "k_pages / v_pages must be bf16 or f16, both alike")
+        _need(k_pages.dim() == 5 and _alike(k_pages, v_pages),
+              "k_pages / v_pages must have five dimensions and the same shape and strides")
+        _need(k_pages.is_cuda and v_pages.is_cuda, "k_pages / v_pages must be CUDA tensors")
+        _need(k_pages.stride(4) == 1, "the last dimension of k_pages / v_pages must be dense")
+        h, t = (2, 3) if layout == "HND" else (3, 2)
+        layers, pages, heads, ps, d = (int(k_pages.shape[i]) for i in (0, 1, h, t, 4))
+        _need(page_table.dim() == 2, "page_table must have two dimensions")
+        seqs, max_pages = (int(n) for n in page_table.shape)
+        _need_i32("page_table", page_table, seqs, max_pages)
+        _need_i32("seq_lens", seq_lens, seqs)
+        _need_i32("page_refs", page_refs, pages)
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.page_table, self.seq_lens, self.page_refs = page_table, seq_lens, page_refs
+        self.layout = layout
+        dev = k_pages.device
+        self.scratch = torch.empty(csgmv_kv_scratch_ints(pages, seqs), dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        c = _KvCacheC()
+        for n in ("k_pages", "v_pages", "page_table", "seq_lens", "page_refs", "scratch", "status"):
+            setattr(c, n, getattr(self, n).data_ptr())
+        c.token_stride, c.head_stride = int(k_pages.stride(t)), int(k_pages.stride(h))
+        c.page_stride, c.layer_stride = int(k_pages.stride(1)), int(k_pages.stride(0))
+        c.dtype, c.num_layers, c.num_pages, c.page_size = _KV_DTYPES[k_pages.dtype], layers, pages, ps
+        c.num_kv_heads, c.head_dim, c.max_seqs, c.max_pages_per_seq = heads, d, seqs, max_pages
+        self.c = c
+        self._ref = ctypes.byref(c)
+
+    @classmethod
+    def allocate(cls, num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                 max_seqs: int, max_pages_per_seq: int, dtype=torch.bfloat16, layout: str = "HND", device="cuda"):
+        """An empty cache with tensors of its own."""
+        shape = ((num_layers, num_pages, num_kv_heads, page_size, head_dim) if layout == "HND" else
+                 (num_layers, num_pages, page_size, num_kv_heads, head_dim))
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
+                   torch.full((max_seqs, max_pages_per_seq), -1, **i32), torch.zeros(max_seqs, **i32),
+                   torch.zeros(num_pages, **i32), layout=layout)
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return self.k_pages.dtype
+
+    def device_status(self) -> int:
+        return int(self.status.item())
+
+
+def csgmv_kv_scratch_ints(num_pages: int, max_seqs: int) -> int:
+    return int(lib().csgmv_kv_scratch_ints(int(num_pages), int(max_seqs)))
+
+
+def _new_rows(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, dims: int):
+    _need(k_new.dim() == dims and _alike(k_new, v_new),
+          f"k_new / v_new must have {dims} dimensions and the same shape and strides")
+    _need(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.is_cuda and v_new.is_cuda,
+          "k_new / v_new must be CUDA tensors of the cache's type")
+    _need(k_new.shape[-1] == cache.c.head_dim and k_new.shape[-2] == cache.c.num_kv_heads and k_new.stride(-1) == 1,
+          "k_new / v_new must end in (kv_heads, head_dim), the last dimension dense")
+
+
+def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, accept_index: torch.Tensor | None,
+                    accept_len: torch.Tensor, tree_indptr: torch.Tensor, seq_slots: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Appends accept_len[b] of request b's rows of k_new / v_new (layers,
+    tokens, kv_heads, head_dim) to its sequence: rows tree_indptr[b] +
+    accept_index[b, j], or its first rows without an accept_index."""
+    _new_rows(cache, k_new, v_new, 4)
+    _need(int(k_new.shape[0]) == cache.c.num_layers, "k_new / v_new must have the cache's layers")
+    bs = int(accept_len.numel())
+    width = 0 if accept_index is None else int(accept_index.shape[-1])
+    _need_i32("accept_len", accept_len, bs)
+    _need_i32("accept_index", accept_index, bs, width)
+    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need_i32("seq_slots", seq_slots, bs)
+    _check(lib().csgmv_kv_commit(cache._ref, _ptr(k_new), _ptr(v_new), int(k_new.stride(0)), int(k_new.stride(1)),
+                                 int(k_new.stride(2)), int(k_new.shape[1]), _ptr(accept_index), width,
+                                 _ptr(accept_len), _ptr(tree_indptr), _ptr(seq_slots), bs, _stream(stream)))
+
+
+def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
+    """Sequence children[i] becomes a copy of sequence parents[i]."""
+    n = int(parents.numel())
+    _need_i32("parents", parents, n)
+    _need_i32("children", children, n)
+    _check(lib().csgmv_kv_fork(cache._ref, _ptr(parents), _ptr(children), n, _stream(stream)))
+
+
+def csgmv_kv_free(cache: KvCache, seqs: torch.Tensor, keep_lens: torch.Tensor | None = None, stream=None) -> None:
+    """Cuts sequence seqs[i] back to keep_lens[i] tokens (None: to nothing)."""
+    n = int(seqs.numel())
+    _need_i32("seqs", seqs, n)
+    _need_i32("keep_lens", keep_lens, n)
+    _check(lib().csgmv_kv_free(cache._ref, _ptr(seqs), _ptr(keep_lens), n, _stream(stream)))
+
+
+def csgmv_kv_compact(cache: KvCache, stream=None) -> None:
+    """Moves live pages into the holes below them; live pages end up first."""
+    _check(lib().csgmv_kv_compact(cache._ref, _stream(stream)))
+
+
+def csgmv_kv_copy_pages(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Copies the contents of pages src[i] to pages dst[i] in every layer."""
+    n = int(src.numel())
+    _need_i32("src", src, n)
+    _need_i32("dst", dst, n)
+    _check(lib().csgmv_kv_copy_pages(cache._ref, _ptr(src), _ptr(dst), n, _stream(stream)))
+
+
+def csgmv_tree_attention_workspace_bytes(cache: KvCache, num_q_heads: int) -> int:
+    return int(lib().csgmv_tree_attention_workspace_bytes(cache._ref, int(num_q_heads)))
+
+
+def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: KvCache, layer: int,
+                         tree_indptr: torch.Tensor, out: torch.Tensor, mask: torch.Tensor | None = None,
+                         seq_slots: torch.Tensor | None = None, scale: float | None = None,
+                         lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of request b's rows of q (tokens, heads, head_dim) over its
+    cached sequence and over its own rows of k_new / v_new that `mask` (int32
+    bits, (tokens, words); None: causal) lets each row see.  scale defaults to
+    head_dim ** -0.5; lse (tokens, heads) f32 is optional."""
+    _need(q.dim() == 3 and out.shape == q.shape, "q and out must be (tokens, heads, head_dim)")
+    _need(q.dtype == cache.dtype and out.dtype == cache.dtype and q.is_cuda and out.is_cuda,
+          "q and out must be CUDA tensors of the cache's type")
+    n, hq, d = (int(x) for x in q.shape)
+    _need(d == cache.c.head_dim and (n == 0 or q.stride(2) == 1 and out.stride(2) == 1),
+          "q and out must have the cache's head_dim, dense")
+    _new_rows(cache, k_new, v_new, 3)
+    _need(int(k_new.shape[0]) == n, "k_new / v_new must have q's tokens")
+    bs = int(tree_indptr.numel()) - 1
+    words = 0 if mask is None else int(mask.shape[-1])
+    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need_i32("mask", mask, n, words)
+    _need_i32("seq_slots", seq_slots, bs)
+    if lse is not None:
+        _need_f32("lse", lse, n, hq)
+        _need(lse.is_contiguous(), "lse must be contiguous")
+    if workspace is None:
+        workspace = torch.empty(csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
+    _check(lib().csgmv_tree_attention(
+        _ptr(q), int(q.stride(0)), int(q.stride(1)), hq, _ptr(k_new), _ptr(v_new), int(k_new.stride(0)),
+        int(k_new.stride(1)), cache._ref, int(layer), _ptr(tree_indptr), _ptr(seq_slots), bs, n, _ptr(mask), words,
+        float(d ** -0.5 if scale is None else scale), _ptr(out), int(out.stride(0)), int(out.stride(1)), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+class DraftTree:
+    """Device buffers of csgmv_build_draft_tree for up to max_nodes drafted
+    tokens, with at most max_draft of them in one request."""
+
+    def __init__(self, max_nodes: int, max_draft: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.words = max(1, (int(max_draft) + 31) // 32)
+        self.max_draft = int(max_draft)
+        self.mask = torch.zeros((max_nodes, self.words), **i32)
+        self.depth = torch.zeros(max_nodes, **i32)
+        self.first_child = torch.full((max_nodes,), -1, **i32)
+        self.next_sibling = torch.full((max_nodes,), -1, **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
+
+
+def csgmv_build_draft_tree(tree: DraftTree, parents: torch.Tensor, tree_indptr: torch.Tensor, stream=None) -> None:
+    """Fills tree.mask, depth, first_child and next_sibling from the nodes'
+    parents (numbers inside their request, -1 at its node 0)."""
+    n, bs = int(parents.numel()), int(tree_indptr.numel()) - 1
+    _need_i32("parents", parents, n)
+    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need(n <= int(tree.depth.numel()), f"{n} nodes exceed the tree's {tree.depth.numel()}")
+    _check(lib().csgmv_build_draft_tree(_ptr(parents), _ptr(tree_indptr), bs, n, tree.words, _ptr(tree.mask),
+                                        _ptr(tree.depth), _ptr(tree.first_child), _ptr(tree.next_sibling),
+                                        _ptr(tree.status), _stream(stream)))
+
+
+def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, tree_indptr: torch.Tensor,
+                        tree: DraftTree, accept_uniforms: torch.Tensor, sample_uniforms: torch.Tensor,
+                        draft_probs: torch.Tensor | None = None, accept_index: torch.Tensor | None = None,
+                        accept_len: torch.Tensor | None = None, next_token: torch.Tensor | None = None, stream=None):
+    """Walks each tree: (accept_index (bs, width), accept_len (bs,), next_token
+    (bs,)), allocated unless given; width defaults to tree.max_draft.
+    draft_probs None: the drafts were chosen, not sampled."""
+    n, bs = int(draft_tokens.numel()), int(tree_indptr.numel()) - 1
+    _need_f32("target_probs", target_probs, n, None)
+    _need(n == 0 or target_probs.stride(1) == 1, "target_probs must have dense rows")
+    vocab = int(target_probs.shape[1])
+    if draft_probs is not None:
+        _need_f32("draft_probs", draft_probs, n, vocab)
+        _need(n == 0 or draft_probs.stride(1) == 1, "draft_probs must have dense rows")
+    _need_i32("draft_tokens", draft_tokens, n)
+    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need_f32("accept_uniforms", accept_uniforms, n)
+    _need_f32("sample_uniforms", sample_uniforms, bs)
+    _need(accept_uniforms.is_contiguous() and sample_uniforms.is_contiguous(), "the uniform numbers must be contiguous")
+    _need(n <= int(tree.depth.numel()), f"{n} nodes exceed the tree's {tree.depth.numel()}")
+    dev = target_probs.device
+    if accept_index is None:
+        accept_index = torch.empty((bs, tree.max_draft), dtype=torch.int32, device=dev)
+    if accept_len is None:
+        accept_len = torch.empty(bs, dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(bs, dtype=torch.int32, device=dev)
+    _need_i32("accept_index", accept_index, bs, None)
+    _need_i32("accept_len", accept_len, bs)
+    _need_i32("next_token", next_token, bs)
+    # the row stride of a single row says nothing
+    ts = int(target_probs.stride(0)) if n > 1 else vocab
+    ds = 0 if draft_probs is None else int(draft_probs.stride(0)) if n > 1 else vocab
+    _check(lib().csgmv_verify_drafts(
+        _ptr(target_probs), ts, _ptr(draft_probs), ds, _ptr(draft_tokens), _ptr(tree_indptr),
+        _ptr(tree.first_child), _ptr(tree.next_sibling), _ptr(accept_uniforms), _ptr(sample_uniforms), bs, n, vocab,
+        _ptr(accept_index), int(accept_index.shape[1]), _ptr(accept_len), _ptr(next_token), _ptr(tree.status),
+        _stream(stream)))
+    return accept_index, accept_len, next_token
