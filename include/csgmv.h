@@ -539,9 +539,11 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  *                  number of rows: plain decoding and prompts)
  * head_dim 64 or 128; num_q_heads a multiple of num_kv_heads, at most 128
  * times it; page_size a power of two >= 8.  One row for each request is plain
- * decoding.  The products have the inputs' type, sums are fp32; the softmax
- * weights are rounded to the inputs' type before they meet V, as the tensor
- * cores take them.  Results do not depend on timing.
+ * decoding.  Sums are fp32; before they meet V the softmax weights are
+ * rounded to half, or to a bfloat16 pair of 16 bits.  Results do not depend on
+ * timing.  A page number out of range sets CSGMV_KV_STATUS_BAD_PAGE and makes
+ * its request's rows meaningless; other bad requests are left out (their rows
+ * of out and lse stay as they are).  bs <= 16384.
  *   workspace      csgmv_tree_attention_workspace_bytes(); contents do not matter
  */
 CSGMV_API int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads,

@@ -49,6 +49,7 @@ struct AttnParams {
     int f16;  // 1: IEEE half, 0: bfloat16
 };
 size_t attn_workspace_bytes(int head_dim);
+int attn_max_requests();
 cudaError_t launch_tree_attention(const AttnParams &p, void *workspace, cudaStream_t stream);
 
 struct TreeParams {

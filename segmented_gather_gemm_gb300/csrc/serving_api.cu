@@ -80,8 +80,8 @@ int check_kv(const csgmv_kv_cache *kv) {
 int check_new(const void *k, const void *v, int64_t ts, int64_t hs) {
     if (!k || !v) return fail(CSGMV_ERR_INVALID_ARG, "k_new / v_new is NULL");
     if (!aligned16(k) || !aligned16(v)) return fail(CSGMV_ERR_INVALID_ARG, "k_new / v_new must be 16-byte aligned");
-    if (ts % 8 || hs % 8 || ts < 0 || hs < 0)
-        return fail(CSGMV_ERR_INVALID_ARG, "k_new / v_new strides must be non-negative multiples of 8");
+    if (ts % 8 || hs % 8 || ts <= 0 || hs <= 0)
+        return fail(CSGMV_ERR_INVALID_ARG, "k_new / v_new strides must be positive multiples of 8");
     return CSGMV_OK;
 }
 
@@ -190,6 +190,8 @@ int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
         return fail(CSGMV_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, kv->num_layers);
     if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
     if (num_tokens > INT32_MAX / 128) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds 2^24");
+    if (bs > csgmv::attn_max_requests())
+        return fail(CSGMV_ERR_UNSUPPORTED, "bs %d exceeds %d", bs, csgmv::attn_max_requests());
     if (bs == 0 || num_tokens == 0) return CSGMV_OK;
     if (!q || !out || !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "NULL tensor");
     if (!aligned16(q) || !aligned16(out)) return fail(CSGMV_ERR_INVALID_ARG, "q / out must be 16-byte aligned");

@@ -1,112 +1,785 @@
 // Attention of draft trees over the paged cache (include/csgmv.h,
 // csgmv_tree_attention).
 //
-// The plain kernel: a block a query row and head, a thread a token for the
-// scores and a thread an element for the sums, with the running maximum and
-// sum of a softmax over tiles of 128 tokens.
+// Mathematics.  For the rows of one request and kv head (its drafted tokens
+// times the query heads of the group, cut into tiles of 128) and tiles of 128
+// tokens: S = Q K^T, a running maximum m and sum l of the softmax in base 2,
+// O <- 2^(m - m') O + P V with P = 2^(scale log2(e) S - m').  m' moves only
+// when it would grow by more than 2^8 (P stays below 2^8, so fp32 sums lose
+// nothing), which keeps O in tensor memory untouched on almost every tile.
+//
+// What bounds it.  A tile of K and V (64 KB at head_dim 128) takes an SM's
+// share of HBM 1.47 us; its two products at 128 rows take the tensor core
+// 0.7 us and the exponentials of 128 x 128 scores about 0.6 us, whatever part
+// of the 128 rows is real.  So up to 128 rows one tile shape serves: bytes
+// bound it, and an MMA of fewer rows would save nothing.
+//
+// Split.  The tiles of all (request, kv head, row tile) items form one axis
+// that is cut into equal parts, one a CTA (one CTA an SM), so a batch of
+// ragged lengths and a single long sequence both fill the GPU.  An item cut
+// by the ends of a part leaves fp32 partial sums in the workspace (at most two
+// a CTA), which a second kernel joins in order of the axis: results do not
+// depend on timing.
+//
+// Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
+// keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
+// rounding, so there P goes in as a high and a low part (16 bits) in two
+// products, which the tensor core has time for.
+//
+// One CTA: a TMA warp fills a ring of K and V tiles, an MMA warp issues
+// S = Q K^T one tile ahead of O += P V, four warps of one row a thread do the
+// softmax from tensor memory and put P back there.
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
+
+#include <map>
+#include <mutex>
 
 #include "serving.cuh"
 
 namespace csgmv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128;         // rows of a row tile, tokens of a token tile
+constexpr int kGroups = kTile / 8; // 8-row groups: the unit of the shared-memory layout
+constexpr int kAttnCtas = 152;     // one CTA an SM
+constexpr int kSoftWarps = 4;
+constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
+constexpr int kMaxRequests = 16384;
+constexpr int kCombineThreads = 128;
+constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float to_f32(uint16_t x, int f16) {
-    return f16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
-}
-__device__ __forceinline__ uint16_t from_f32(float x, int f16) {
-    return f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+template <int D>
+struct Shape {
+    static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
+    static constexpr int kGroupBytes = kHalves * 1024; // 8 rows
+    static constexpr int kTileBytes = kGroups * kGroupBytes;
+    static constexpr int kSlots = D == 128 ? 6 : 12;
+    static constexpr int kRing = kSlots * kTileBytes;
+    static constexpr int kBars = 2 * kSlots + 8;
+    static constexpr int kSmem = 1024 + kTileBytes + kRing + kBars * 8 + 64;
+};
+
+struct alignas(64) AttnMaps {
+    CUtensorMap k, v;    // whole boxes of a page
+    CUtensorMap k8, v8;  // 8 rows of a page
+    CUtensorMap kn, vn;  // 8 rows of the drafted tokens
+};
+enum { kPagesGeneral = 0, kPagesHeadsOut = 1, kPagesHeadsIn = 2 };
+
+struct AttnKernelParams {
+    AttnParams p;
+    AttnMaps maps;
+    float *part;      // [2 * kAttnCtas][D / 4][kTile] float4: unscaled O
+    float *ml;        // [2 * kAttnCtas][2][kTile]: m, l
+    int4 *starters;   // [2 * kAttnCtas]: item a CTA begins and does not end: {b, h, row tile, rows}, {last CTA, ..}
+    int form;         // kPages*
+    int box_groups;   // 8-row groups of a whole box
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];\n" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) attend(AttnParams p) {
-    __shared__ float q[128], e[kThreads], red[kThreads / 32];
-    const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // the request that owns row t
-    int b = 0;
+// Shared-memory matrix descriptor, 128-byte swizzle: `lbo` the distance of
+// 64-element blocks along the contiguous dimension (used when that is not K),
+// `sbo` the distance of 8-row groups.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor of kind::f16, fp32 accumulation; `b_mn`: B is stored
+// with its N dimension contiguous.
+__device__ __forceinline__ uint32_t idesc16(bool f16, int M, int N, bool b_mn) {
+    const uint32_t fmt = f16 ? 0u : 1u;
+    return (1u << 4) | fmt << 7 | fmt << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return pack_bf16x2(lo, hi);
+}
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t x) {
+    const uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+    return (x & e) == e;
+}
+template <bool F16>
+__device__ __forceinline__ float widen(uint16_t x) {
+    return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+}
+
+// One request's part of the work.  Tokens lie on a virtual axis: the cached
+// ones, padded to whole 8-row groups, then the drafted ones.
+struct Req {
+    int lo, T, L, slot;
+    __device__ __forceinline__ int ctx_groups() const { return (L + 7) >> 3; }
+    __device__ __forceinline__ int groups() const { return ctx_groups() + ((T + 7) >> 3); }
+    __device__ __forceinline__ int token_tiles() const { return (groups() + kGroups - 1) / kGroups; }
+    __device__ __forceinline__ int row_tiles(int group) const { return (T * group + kTile - 1) / kTile; }
+    __device__ __forceinline__ long long tiles(int group, int hkv) const {
+        return (long long)row_tiles(group) * hkv * token_tiles();
+    }
+};
+
+// Request b, with T = 0 (no work) when it is not sound; the status bit why.
+__device__ __forceinline__ Req load_req(const AttnParams &p, int b, int *bad) {
+    Req r;
+    r.lo = p.indptr[b];
+    const int hi = p.indptr[b + 1];
+    r.slot = p.slots ? p.slots[b] : b;
+    r.T = hi - r.lo;
+    r.L = 0;
+    *bad = 0;
+    if (r.lo < 0 || hi < r.lo || hi > p.num_tokens || (p.mask && r.T > 32 * p.mask_words)) *bad = CSGMV_KV_STATUS_BAD_LENS;
+    else if (r.slot < 0 || r.slot >= p.max_seqs) *bad = CSGMV_KV_STATUS_BAD_SEQ;
+    else {
+        r.L = p.seq_lens[r.slot];
+        if (r.L < 0 || r.L > p.max_pages * p.page_size) *bad = CSGMV_KV_STATUS_BAD_LENS;
+    }
+    if (*bad) r.T = r.L = 0;
+    return r;
+}
+
+// A CTA's part of the axis, walked item by item.
+struct Walk {
+    Req r;
+    int b, h, m, t0;   // request, kv head, row tile, first token tile of the segment
+    int n, nt;         // token tiles of the segment, of the item
+    long long left;    // tiles of the part, this segment's included
+    __device__ __forceinline__ void cut() { n = (int)min((long long)(nt - t0), left); }
+    __device__ __forceinline__ bool next(const AttnParams &p) {
+        left -= n;
+        if (left <= 0 || (m + 1 == r.row_tiles(p.group) && h + 1 == p.hkv && b + 1 >= p.bs)) return false;
+        t0 = 0;
+        if (++m == r.row_tiles(p.group)) {
+            m = 0;
+            if (++h == p.hkv) {
+                h = 0;
+                int bad;
+                do {
+                    r = load_req(p, ++b, &bad);
+                } while (r.T == 0 && b + 1 < p.bs);
+                nt = r.token_tiles();
+            }
+        }
+        cut();
+        return true;
+    }
+    __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kTile, r.T * p.group - m * kTile); }
+};
+
+// 32 bits of row t's mask from drafted token j0 (which may be negative: lower
+// bits are then 0), cut at T.
+__device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r, int t, int j0) {
+    if (j0 <= -32 || j0 >= r.T) return 0;
+    uint32_t x;
+    const int a = max(j0, 0);
+    if (p.mask) {
+        const int32_t *row = p.mask + (int64_t)(r.lo + t) * p.mask_words;
+        const int w = a >> 5;
+        const uint32_t w0 = (uint32_t)row[w], w1 = w + 1 < p.mask_words ? (uint32_t)row[w + 1] : 0u;
+        x = __funnelshift_r(w0, w1, a & 31);
+    } else {
+        const int n = t + 1 - a;
+        x = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    if (j0 < 0) x <<= -j0;
+    const int lim = r.T - j0;
+    return lim >= 32 ? x : x & ((1u << lim) - 1u);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant__ AttnKernelParams k) {
+    using S = Shape<D>;
+    const AttnParams &p = k.p;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *q_s = smem, *ring = smem + S::kTileBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + S::kRing);
+    uint64_t *full = bars, *empty = bars + S::kSlots, *s_full = bars + 2 * S::kSlots, *p_ready = s_full + 2,
+             *pv_done = s_full + 4, *q_ready = s_full + 6;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars);
+    volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    griddep_launch_dependents();
+    if (warp == kSoftWarps + 1) {
+        tmem_alloc(misc, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], kSoftWarps);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_ready, kSoftWarps);
+        fence_mbar_init();
+        *odd_item = -1;
+    }
+    // The axis: tiles ahead of each request, in the ring's memory.
+    long long *ahead = reinterpret_cast<long long *>(ring);
+    long long W = 0;
     {
-        int lo = 0, hi = p.bs;
+        long long *ws = reinterpret_cast<long long *>(q_s);
+        for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
+            const int b = b0 + tid;
+            long long n = 0, tot;
+            if (b < p.bs) {
+                int bad;
+                n = load_req(p, b, &bad).tiles(p.group, p.hkv);
+                if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
+            }
+            const long long pre = block_scan_ex(n, ws, &tot);
+            if (b < p.bs) ahead[b] = W + pre;
+            W += tot;
+        }
+    }
+    __syncthreads();
+    const long long nct = min((long long)gridDim.x, W);
+    const long long first = nct ? (long long)blockIdx.x * W / nct : 0;
+    const long long last = nct ? ((long long)blockIdx.x + 1) * W / nct : 0;
+    const bool idle = blockIdx.x >= nct;
+    if (tid == 0) k.starters[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    Walk w0 = {};
+    if (!idle) {
+        int lo = 0, hi = p.bs;  // the last request with ahead <= first and work of its own
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p.indptr[mid] <= t) lo = mid; else hi = mid;
+            if (ahead[mid] <= first) lo = mid; else hi = mid;
         }
-        b = lo;
+        int bad;
+        w0.b = lo;
+        w0.r = load_req(p, lo, &bad);
+        w0.nt = w0.r.token_tiles();
+        const long long in = first - ahead[lo];
+        const int item = (int)(in / w0.nt);
+        w0.t0 = (int)(in - (long long)item * w0.nt);
+        const int rt = w0.r.row_tiles(p.group);
+        w0.h = item / rt;
+        w0.m = item - w0.h * rt;
+        w0.left = last - first;
+        w0.cut();
     }
-    const int r0 = p.indptr[b], r1 = p.indptr[b + 1], n = r1 - r0;
-    if (t < r0 || t >= r1) return;  // a row of no request
-    const int slot = p.slots ? p.slots[b] : b;
-    int bad = 0, len = 0;
-    if (slot < 0 || slot >= p.max_seqs) bad = CSGMV_KV_STATUS_BAD_SEQ;
-    else if ((len = p.seq_lens[slot]) < 0 || len > p.max_pages * p.page_size || r0 < 0 || r1 > p.num_tokens ||
-             (p.mask && n > 32 * p.mask_words))
-        bad = CSGMV_KV_STATUS_BAD_LENS;
-    if (bad) {
-        if (tid == 0) atomicOr(p.status, bad);
-        return;
-    }
-    const int g = h / p.group;
-    if (tid < p.d) q[tid] = to_f32(p.q[t * p.q_ts + h * p.q_hs + tid], p.f16);
+    fence_proxy_async_smem();  // the ring's memory goes over to TMA
+    tc_fence_before();
     __syncthreads();
-    const int32_t *table = p.page_table + (int64_t)slot * p.max_pages;
-    auto place = [&](int i, const uint16_t *pages, const uint16_t *fresh) -> const uint16_t * {
-        if (i >= len) return fresh + (int64_t)(r0 + i - len) * p.n_ts + g * p.n_hs;
-        const int page = table[i / p.page_size];
-        if (page < 0 || page >= p.num_pages) return nullptr;
-        return pages + page * p.page_stride + g * p.head_stride + (int64_t)(i % p.page_size) * p.token_stride;
-    };
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int i0 = 0; i0 < len + n; i0 += kThreads) {
-        const int i = i0 + tid;
-        bool sees = i < len;
-        if (i >= len && i < len + n) {
-            const int j = i - len;
-            sees = p.mask ? (p.mask[(int64_t)t * p.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= t - r0;
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const uint32_t t_o = tmem + 256;
+
+    if (idle) {
+        // nothing
+    } else if (warp == kSoftWarps) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            prefetch_tmap(&k.maps.k);
+            prefetch_tmap(&k.maps.v);
+            prefetch_tmap(&k.maps.kn);
+            prefetch_tmap(&k.maps.vn);
         }
-        float s = -INFINITY;
-        if (sees) {
-            const uint16_t *k = place(i, p.k_pages, p.k_new);
-            if (k) {
-                s = 0.0f;
-                for (int x = 0; x < p.d; ++x) s += q[x] * to_f32(k[x], p.f16);
-                s *= p.scale;
-            } else {
-                atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
-                sees = false;
+        const int gpp_shift = __ffs(p.page_size >> 3) - 1;  // log2 of the 8-row groups of a page
+        const int bg = k.box_groups;
+        int it = 0;  // slots filled
+        Walk w = w0;
+        do {
+            const int gctx = w.r.ctx_groups(), gall = w.r.groups();
+            const int whole = (w.r.L >> 3) & ~(bg - 1);  // groups in boxes that are full of tokens
+            const int32_t *table = p.page_table + (int64_t)w.r.slot * p.max_pages;
+            for (int t = w.t0; t < w.t0 + w.n; ++t) {
+                const int g = t * kGroups + lane, ng = min(kGroups, gall - t * kGroups);
+                int page = 0;
+                const bool in = lane < ng, ctx = in && g < gctx;
+                const bool box = ctx && g < whole, lead = box && !(lane & (bg - 1));
+                if (lead || (ctx && !box)) {
+                    page = table[g >> gpp_shift];
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
+                        page = p.num_pages;  // past the pool: zeros
+                    }
+                }
+                const int rg = g & ((1 << gpp_shift) - 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int s = it % S::kSlots;
+                    mbar_wait(&empty[s], ((it / S::kSlots) & 1) ^ 1, p.status, kKvStatusTimeout);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
+                    __syncwarp();
+                    const uint32_t dst = smem_u32(ring) + s * S::kTileBytes + lane * S::kGroupBytes;
+                    if (lead) {
+                        const void *map = kv ? &k.maps.v : &k.maps.k;
+                        if (k.form == kPagesHeadsOut) tma_load_5d(dst, map, 0, 0, 0, rg, page * p.hkv + w.h, &full[s]);
+                        else if (k.form == kPagesHeadsIn) tma_load_5d(dst, map, 0, 0, 0, w.h, (page << gpp_shift) + rg, &full[s]);
+                        else tma_load_5d(dst, map, 0, rg * 8, 0, w.h, page, &full[s]);
+                    } else if (ctx && !box) {
+                        tma_load_5d(dst, kv ? &k.maps.v8 : &k.maps.k8, 0, rg * 8, 0, w.h, page, &full[s]);
+                    } else if (in && !ctx) {
+                        tma_load_5d(dst, kv ? &k.maps.vn : &k.maps.kn, 0, w.r.lo + (g - gctx) * 8, 0, w.h, 0, &full[s]);
+                    }
+                }
             }
+        } while (w.next(p));
+    } else if (warp == kSoftWarps + 1) {
+        // --------------------------------------------------------- products
+        if (lane == 0) {
+            const uint32_t ids = idesc16(F16, kTile, D, true);
+            const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(q_s);
+            int it = 0, item = 0;
+            Walk w = w0;
+            do {
+                const int gall = w.r.groups();
+                auto keys = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) / 2 * 16; };
+                auto scores = [&](int t, int i) {
+                    const int s = (2 * i) % S::kSlots;
+                    mbar_wait(&full[s], ((2 * i) / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    tc_fence_after();
+                    const uint32_t id = idesc16(F16, kTile, keys(t), false);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = (x / 4) * 1024 + (x % 4) * 32;
+                        tc_mma_bf16(tmem + (i & 1) * 128, smem_desc(q_a + off, 16, S::kGroupBytes),
+                                    smem_desc(ring_a + s * S::kTileBytes + off, 16, S::kGroupBytes), id, x > 0);
+                    }
+                    tc_commit(&empty[s]);
+                    tc_commit(&s_full[i & 1]);
+                };
+                mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
+                tc_fence_after();
+                scores(w.t0, it);
+                for (int j = 0; j < w.n; ++j, ++it) {
+                    if (j + 1 < w.n) {
+                        // the next scores take the columns that P of the tile before lies in
+                        if (j > 0) mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
+                        scores(w.t0 + j + 1, it + 1);
+                    }
+                    mbar_wait(&p_ready[it & 1], (it >> 1) & 1, p.status, kKvStatusTimeout);
+                    const int s = (2 * it + 1) % S::kSlots;
+                    mbar_wait(&full[s], ((2 * it + 1) / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    tc_fence_after();
+                    const int steps = keys(w.t0 + j) / 16;
+                    for (int x = 0; x < steps; ++x) {
+                        const uint64_t v = smem_desc(ring_a + s * S::kTileBytes + x * 2 * S::kGroupBytes, 1024, S::kGroupBytes);
+                        const uint32_t w = tmem + (it & 1) * 128 + x * 8;
+                        tc_mma_bf16_tmem_a(t_o, w, v, ids, j > 0 || x > 0);
+                        if (!F16) tc_mma_bf16_tmem_a(t_o, w + 64, v, ids, true);
+                    }
+                    tc_commit(&empty[s]);
+                    tc_commit(&pv_done[it & 1]);
+                }
+                ++item;
+            } while (w.next(p));
         }
-        float top = s;
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
-        if (lane == 0) red[warp] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-        const float w = sees ? expf(s - base) : 0.0f, f = expf(m - base);
-        e[tid] = sees ? w : -1.0f;
-        float sum = warp_sum(w);
-        __syncthreads();
-        if (lane == 0) red[warp] = sum;
-        __syncthreads();
-        l = l * f + red[0] + red[1] + red[2] + red[3];
-        o *= f;
-        m = mn;
-        if (tid < p.d)
-            for (int y = 0; y < kThreads && i0 + y < len + n; ++y) {
-                if (e[y] == -1.0f) continue;  // not seen: no influence whatever it holds
-                o += e[y] * to_f32(place(i0 + y, p.v_pages, p.v_new)[tid], p.f16);
+    } else {
+        // ---------------------------------------------------------- softmax
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const float c = p.scale * kLog2e;
+        constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
+        int it = 0, item = 0;
+        Walk w = w0;
+        do {
+            const int rows = w.rows(p);
+            const bool live = tid < rows, warp_live = warp * 32 < rows;
+            const int at = w.m * kTile + tid, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
+            // Q: a thread a row, into the swizzled tile
+            if (live) {
+                const uint16_t *src = p.q + (int64_t)(w.r.lo + t_row) * p.q_ts + head * p.q_hs;
+                const uint32_t dst = smem_u32(q_s) + (tid >> 3) * S::kGroupBytes + (tid & 7) * 128;
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    const uint4 v = ldg16(src + x * 8);
+                    const uint32_t a = dst + (x >> 3) * 1024 + (((x & 7) ^ (tid & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
             }
-        __syncthreads();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+
+            float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m
+            const int gctx = w.r.ctx_groups(), gall = w.r.groups();
+            for (int j = 0; j < w.n; ++j, ++it) {
+                const int t = w.t0 + j, buf = it & 1;
+                const int nkeys = (min(kGroups, gall - t * kGroups) + 1) / 2 * 16;
+                const bool edge = (t + 1) * kTile > w.r.L;  // holds more than cached tokens
+                const uint32_t t_s = tmem + buf * 128 + lane_base;
+                mbar_wait(&s_full[buf], (it >> 1) & 1, p.status, kKvStatusTimeout);
+                __syncwarp();
+                tc_fence_after();
+                if (warp_live) {
+                    float s[128];
+                    {
+                        float(&a)[64] = *reinterpret_cast<float(*)[64]>(&s[0]);
+                        float(&b)[64] = *reinterpret_cast<float(*)[64]>(&s[64]);
+                        tmem_ld64(t_s, a);
+                        if (nkeys > 64) tmem_ld64(t_s + 64, b);
+                        else {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) b[i] = -INFINITY;
+                        }
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int k0 = t * kTile + x * 32, n = w.r.L - k0;
+                            uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+                            if (live) bits |= tree_word(p, w.r, t_row, k0 - gctx * 8);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[x * 32 + i] = (bits >> i) & 1 ? s[x * 32 + i] : -INFINITY;
+                        }
+                    }
+                    __syncwarp();
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    const bool grow = live && (top > m + kLazy || (m == -INFINITY && top > m));
+                    if (__any_sync(kFullMask, grow)) {
+                        const float mn = grow ? top : m;
+                        if (j > 0) {  // O so far, in units of 2^m
+                            const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
+                            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
+                            __syncwarp();
+                            tc_fence_after();
+#pragma unroll
+                            for (int x = 0; x < D / 32; ++x) {
+                                float o[32];
+                                uint32_t u[32];
+                                tmem_ld32(t_o + lane_base + x * 32, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+                                tmem_st32(t_o + lane_base + x * 32, u);
+                            }
+                            l *= f;
+                        }
+                        m = mn;
+                    }
+                    const float base = m == -INFINITY ? 0.0f : kShift - m;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t u[16], low[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e0 = ex2(fmaf(s[x * 32 + 2 * i], c, base)), e1 = ex2(fmaf(s[x * 32 + 2 * i + 1], c, base));
+                            sum[i & 3] += e0 + e1;
+                            u[i] = pack2<F16>(e0, e1);
+                            if (!F16) {
+                                const float2 h = unpack_bf16x2(u[i]);
+                                low[i] = pack_bf16x2(e0 - h.x, e1 - h.y);
+                            }
+                        }
+                        tmem_st16(t_s + x * 16, u);
+                        if (!F16) tmem_st16(t_s + 64 + x * 16, low);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                if (edge) {
+                    // V: a thread a token.  Rows that are no token are cleared (a weight of 0
+                    // would not silence a NaN there); what is not finite in a drafted row is
+                    // taken out, and added at the end to the rows that see it.
+                    const int sv = (2 * it + 1) % S::kSlots;
+                    mbar_wait(&full[sv], ((2 * it + 1) / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    const int vk = t * kTile + tid, jt = vk - gctx * 8;
+                    if (tid < nkeys) {
+                        unsigned char *row = ring + sv * S::kTileBytes + (tid >> 3) * S::kGroupBytes + (tid & 7) * 128;
+                        const bool drafted = jt >= 0 && jt < w.r.T;
+                        if (drafted || vk >= w.r.L) {
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x) {
+                                uint4 *a = reinterpret_cast<uint4 *>(row + (x >> 3) * 1024 + (x & 7) * 16);
+                                uint4 v = make_uint4(0, 0, 0, 0);
+                                if (drafted) {
+                                    v = *a;
+                                    uint32_t *e = reinterpret_cast<uint32_t *>(&v);
+                                    bool odd = false;
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        if (nonfinite16<F16>(e[y])) odd = true, e[y] &= 0xffff0000u;
+                                        if (nonfinite16<F16>(e[y] >> 16)) odd = true, e[y] &= 0x0000ffffu;
+                                    }
+                                    if (!odd) continue;
+                                    *odd_item = item;
+                                }
+                                *a = v;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[buf]);
+            }
+            // the segment's sums.  (A warp may be here before another has P of the tile
+            // before last ready: pv_done is two barriers, so that the parity waited for
+            // cannot be that of an older product.)
+            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
+            __syncwarp();
+            tc_fence_after();
+            if (warp_live) {
+                const bool whole = w.n == w.nt, odd = *odd_item == item;
+                const int cell = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
+                const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays
+                uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs;
+                float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + tid;
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    float o[32];
+                    tmem_ld32(t_o + lane_base + x * 32, o);
+                    if (live) {
+                        if (odd) {
+                            for (int j = 0; j < w.r.T; ++j) {
+                                const int vt = (gctx * 8 + j) / kTile;
+                                if (vt < w.t0 || vt >= w.t0 + w.n || !(tree_word(p, w.r, t_row, j) & 1)) continue;
+                                const uint16_t *v = p.v_new + (int64_t)(w.r.lo + j) * p.n_ts + w.h * p.n_hs + x * 32;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (nonfinite16<F16>(v[i])) o[i] += widen<F16>(v[i]);
+                            }
+                        }
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint4 v;
+                                v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                                v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                                v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                                v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                                *reinterpret_cast<uint4 *>(dst + x * 32 + i * 8) = v;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                part[(x * 8 + i) * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                    __syncwarp();  // the next load is the whole warp's
+                }
+                if (live) {
+                    if (!whole) {
+                        k.ml[cell * 2 * kTile + tid] = m;
+                        k.ml[cell * 2 * kTile + kTile + tid] = l;
+                    } else if (p.lse) {
+                        p.lse[(int64_t)(w.r.lo + t_row) * p.hq + head] =
+                            l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+                    }
+                }
+                if (tid == 0 && !whole && w.t0 == 0) {
+                    // the CTA that holds the item's last tile
+                    const long long end = last - w.left + w.nt;  // first tile past the item
+                    k.starters[2 * blockIdx.x + 1] = make_int4((int)((end * nct - 1) / W), 0, 0, 0);
+                    k.starters[2 * blockIdx.x] = make_int4(w.b, w.h, w.m, rows);
+                }
+            }
+            tc_fence_before();
+            ++item;
+        } while (w.next(p));
     }
-    if (tid < p.d) p.out[t * p.o_ts + h * p.o_hs + tid] = from_f32(l == 0.0f ? 0.0f : o / l, p.f16);
-    if (tid == 0 && p.lse) p.lse[(int64_t)t * p.hq + h] = l == 0.0f ? -INFINITY : m + logf(l);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    __syncwarp();
+    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, 512);
 }
+
+// Joins the parts of the items that the axis' cuts went through: block (c, y)
+// the item that CTA c began, in order of the axis.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant__ AttnKernelParams k) {
+    griddep_wait();
+    const AttnParams &p = k.p;
+    const int c0 = blockIdx.x;
+    const int4 head4 = k.starters[2 * c0];
+    if (head4.x < 0) return;
+    const int c1 = k.starters[2 * c0 + 1].x, rows = head4.w, n = rows * (D / 4);
+    constexpr float kShift = F16 ? 4.0f : 0.0f;
+    const int lo = p.indptr[head4.x];
+    for (int e = blockIdx.y * kCombineThreads + threadIdx.x; e < n; e += gridDim.y * kCombineThreads) {
+        const int d4 = e / rows, row = e - d4 * rows;
+        auto cell = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
+        float m = -INFINITY;
+        for (int c = c0; c <= c1; ++c) m = fmaxf(m, k.ml[cell(c) * 2 * kTile + row]);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float f = ex2(k.ml[cell(c) * 2 * kTile + row] - base);
+            l += k.ml[cell(c) * 2 * kTile + kTile + row] * f;
+            const float4 v = reinterpret_cast<const float4 *>(k.part)[((int64_t)cell(c) * (D / 4) + d4) * kTile + row];
+            // a part of all-masked tiles counts for nothing (its m is -inf, its O is 0)
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+        }
+        const int at = head4.z * kTile + row, t = at / p.group, head = head4.y * p.group + (at - t * p.group);
+        const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        uint2 u;
+        u.x = pack2<F16>(o.x * inv, o.y * inv);
+        u.y = pack2<F16>(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(p.out + (int64_t)(lo + t) * p.o_ts + head * p.o_hs + d4 * 4) = u;
+        if (d4 == 0 && p.lse)
+            p.lse[(int64_t)(lo + t) * p.hq + head] =
+                l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::mutex g_mu;
+std::map<int, int> g_ready;  // device -> CTAs to launch
+
+cudaError_t prepare(int *ctas) {
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto found = g_ready.find(dev);
+    if (found != g_ready.end()) {
+        *ctas = found->second;
+        return cudaSuccess;
+    }
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    int sms = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const struct { const void *fn; int smem; } all[] = {
+        {reinterpret_cast<const void *>(attend<64, false>), Shape<64>::kSmem},
+        {reinterpret_cast<const void *>(attend<64, true>), Shape<64>::kSmem},
+        {reinterpret_cast<const void *>(attend<128, false>), Shape<128>::kSmem},
+        {reinterpret_cast<const void *>(attend<128, true>), Shape<128>::kSmem}};
+    for (const auto &f : all)
+        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
+    *ctas = g_ready[dev] = sms < kAttnCtas ? sms : kAttnCtas;
+    return cudaSuccess;
+}
+
+// A 5-D map of 16-bit elements with 128-byte rows: dims and box from the
+// innermost, strides in elements of dims 1 .. 4.
+bool encode(CUtensorMap *map, const void *base, bool f16, const int64_t (&dim)[5], const int64_t (&stride)[4],
+            const int (&box)[5]) {
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 5; ++i) {
+        d[i] = (cuuint64_t)dim[i];
+        b[i] = (cuuint32_t)box[i];
+    }
+    // the stride of a dimension of one element is never used
+    for (int i = 0; i < 4; ++i) s[i] = dim[i + 1] > 1 ? (cuuint64_t)stride[i] * 2 : 128;
+    return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                    const_cast<void *>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F16>
+cudaError_t launch(const AttnKernelParams &k, int ctas, cudaStream_t stream) {
+    cudaError_t e = launch_kernel(attend<D, F16>, dim3((unsigned)ctas), kAttnThreads, Shape<D>::kSmem, stream, 0, false, k);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(combine<D, F16>, dim3((unsigned)ctas, 8), kCombineThreads, 0, stream, 0, true, k);
+}
+
+constexpr size_t kStarterBytes = 2 * kAttnCtas * sizeof(int4);
+constexpr size_t kMlBytes = 2 * (size_t)kAttnCtas * 2 * kTile * sizeof(float);
 
 }  // namespace
 
-size_t attn_workspace_bytes(int head_dim) { return 0; }
+size_t attn_workspace_bytes(int head_dim) {
+    return kStarterBytes + kMlBytes + 2 * (size_t)kAttnCtas * kTile * (size_t)head_dim * sizeof(float);
+}
+
+int attn_max_requests() { return kMaxRequests; }
 
 cudaError_t launch_tree_attention(const AttnParams &p, void *workspace, cudaStream_t stream) {
-    return launch_kernel(attend, dim3((unsigned)p.num_tokens, (unsigned)p.hq), kThreads, 0, stream, 0, false, p);
+    int ctas;
+    const cudaError_t e = prepare(&ctas);
+    if (e != cudaSuccess) return e;
+    AttnKernelParams k;
+    k.p = p;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    k.starters = reinterpret_cast<int4 *>(ws);
+    k.ml = reinterpret_cast<float *>(ws + kStarterBytes);
+    k.part = reinterpret_cast<float *>(ws + kStarterBytes + kMlBytes);
+
+    // Pages.  A box of several 8-row groups must land as the tile holds them
+    // (both 64-column halves of a group side by side), which takes the page
+    // axis and the head axis (or the group axis) as one dimension: possible
+    // when pages follow one another without gaps.  Other strides take 8 rows a
+    // box.
+    const int64_t D = p.d, H = p.hkv, ps = p.page_size, P = p.num_pages, halves = D / 64;
+    const int br = (int)(ps < kTile ? ps : kTile);
+    const bool small = P * H <= INT32_MAX / 2 && P * (ps / 8) <= INT32_MAX / 2;
+    bool ok = true;
+    const uint16_t *pools[2] = {p.k_pages, p.v_pages};
+    CUtensorMap *whole[2] = {&k.maps.k, &k.maps.v}, *eight[2] = {&k.maps.k8, &k.maps.v8}, *fresh[2] = {&k.maps.kn, &k.maps.vn};
+    const uint16_t *rows[2] = {p.k_new, p.v_new};
+    if (small && p.page_stride == H * p.head_stride) k.form = kPagesHeadsOut;
+    else if (small && p.page_stride == ps * p.token_stride) k.form = kPagesHeadsIn;
+    else k.form = kPagesGeneral;
+    k.box_groups = k.form == kPagesGeneral ? 1 : br / 8;
+    for (int i = 0; i < 2; ++i) {
+        ok = ok && encode(eight[i], pools[i], p.f16, {64, ps, halves, H, P},
+                          {p.token_stride, 64, p.head_stride, p.page_stride}, {64, 8, (int)halves, 1, 1});
+        if (k.form == kPagesHeadsOut)
+            ok = ok && encode(whole[i], pools[i], p.f16, {64, 8, halves, ps / 8, P * H},
+                              {p.token_stride, 64, 8 * p.token_stride, p.head_stride}, {64, 8, (int)halves, br / 8, 1});
+        else if (k.form == kPagesHeadsIn)
+            ok = ok && encode(whole[i], pools[i], p.f16, {64, 8, halves, H, P * (ps / 8)},
+                              {p.token_stride, 64, p.head_stride, 8 * p.token_stride}, {64, 8, (int)halves, 1, br / 8});
+        else
+            *whole[i] = *eight[i];
+        ok = ok && encode(fresh[i], rows[i], p.f16, {64, p.num_tokens, halves, H, 1}, {p.n_ts, 64, p.n_hs, 64},
+                          {64, 8, (int)halves, 1, 1});
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    if (D == 64) return p.f16 ? launch<64, true>(k, ctas, stream) : launch<64, false>(k, ctas, stream);
+    return p.f16 ? launch<128, true>(k, ctas, stream) : launch<128, false>(k, ctas, stream);
 }
 
 }  // namespace csgmv
