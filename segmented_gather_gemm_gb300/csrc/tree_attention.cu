@@ -26,9 +26,10 @@
 // rounding, so there P goes in as a high and a low part (16 bits) in two
 // products, which the tensor core has time for.
 //
-// One CTA: a TMA warp fills a ring of K and V tiles, an MMA warp issues
-// S = Q K^T one tile ahead of O += P V, four warps of one row a thread do the
-// softmax from tensor memory and put P back there.
+// One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, an
+// MMA warp issues S = Q K^T two tiles ahead of O += P V (three S buffers, each
+// P in its S's place), eight warps do the softmax from tensor memory, two for
+// 32 rows: a thread has half a row's tokens.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
@@ -43,8 +44,10 @@ namespace {
 constexpr int kTile = 128;         // rows of a row tile, tokens of a token tile
 constexpr int kGroups = kTile / 8; // 8-row groups: the unit of the shared-memory layout
 constexpr int kAttnCtas = 152;     // one CTA an SM
-constexpr int kSoftWarps = 4;
-constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
+constexpr int kSoftWarps = 8;
+constexpr int kWarpK = kSoftWarps, kWarpV = kSoftWarps + 1, kWarpMma = kSoftWarps + 2;
+constexpr int kAttnThreads = 32 * (kSoftWarps + 3);
+constexpr int kBufs = 3;           // S buffers in tensor memory
 constexpr int kMaxRequests = 16384;
 constexpr int kCombineThreads = 128;
 constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
@@ -55,10 +58,12 @@ struct Shape {
     static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
     static constexpr int kGroupBytes = kHalves * 1024; // 8 rows
     static constexpr int kTileBytes = kGroups * kGroupBytes;
-    static constexpr int kSlots = D == 128 ? 6 : 12;
-    static constexpr int kRing = kSlots * kTileBytes;
-    static constexpr int kBars = 2 * kSlots + 8;
-    static constexpr int kSmem = 1024 + kTileBytes + kRing + kBars * 8 + 64;
+    static constexpr int kSlots = D == 128 ? 3 : 6;    // of each ring
+    static constexpr int kRing = 2 * kSlots * kTileBytes;
+    static constexpr int kBars = 4 * kSlots + 3 * kBufs + 1;
+    static constexpr int kPairBytes = 2 * 2 * kTile * 4;
+    static constexpr int kSmem = kTileBytes + kRing + kPairBytes + (kBars + 1) * 8 + 64;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct alignas(64) AttnMaps {
@@ -179,8 +184,8 @@ struct Walk {
     Req r;
     int b, h, m, t0;   // request, kv head, row tile, first token tile of the segment
     int n, nt;         // token tiles of the segment, of the item
-    long long left;    // tiles of the part, this segment's included
-    __device__ __forceinline__ void cut() { n = (int)min((long long)(nt - t0), left); }
+    int left;          // tiles of the part, this segment's included
+    __device__ __forceinline__ void cut() { n = min(nt - t0, left); }
     __device__ __forceinline__ bool next(const AttnParams &p) {
         left -= n;
         if (left <= 0 || (m + 1 == r.row_tiles(p.group) && h + 1 == p.hkv && b + 1 >= p.bs)) return false;
@@ -222,31 +227,53 @@ __device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r,
     return lim >= 32 ? x : x & ((1u << lim) - 1u);
 }
 
+// The even cut of W tiles into n parts: the first W % n have one tile more.
+struct Cut {
+    int q, r;
+    __device__ __forceinline__ Cut(int W, int n) : q(W / n), r(W - W / n * n) {}
+    __device__ __forceinline__ int first(int c) const { return c * q + min(c, r); }
+    // The part that holds tile x.
+    __device__ __forceinline__ int part(int x) const {
+        const int big = r * (q + 1);
+        return x < big ? x / (q + 1) : r + (x - big) / q;
+    }
+};
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant__ AttnKernelParams k) {
     using S = Shape<D>;
     const AttnParams &p = k.p;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char *q_s = smem, *ring = smem + S::kTileBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + S::kRing);
-    uint64_t *full = bars, *empty = bars + S::kSlots, *s_full = bars + 2 * S::kSlots, *p_ready = s_full + 2,
-             *pv_done = s_full + 4, *q_ready = s_full + 6;
-    uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *q_s = smem, *k_ring = smem + S::kTileBytes, *v_ring = k_ring + S::kSlots * S::kTileBytes;
+    float(*pair_s)[2][kTile] = reinterpret_cast<float(*)[2][kTile]>(k_ring + S::kRing);  // a row's two halves, by turns
+    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kPairBytes);
+    uint64_t *k_full = bars, *k_empty = k_full + S::kSlots, *v_full = k_empty + S::kSlots, *v_empty = v_full + S::kSlots,
+             *s_full = v_empty + S::kSlots, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
+             *q_ready = pv_done + kBufs;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     griddep_launch_dependents();
-    if (warp == kSoftWarps + 1) {
+    if (smem_u32(smem) & 1023) {  // the swizzled tiles count on it
+        if (tid == 0) {
+            atomicOr(p.status, kKvStatusTimeout);
+            k.starters[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+        }
+        return;
+    }
+    if (warp == kWarpMma) {
         tmem_alloc(misc, 512);
         tmem_relinquish();
     }
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], kSoftWarps);
             mbar_init(&pv_done[i], 1);
@@ -255,9 +282,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         fence_mbar_init();
         *odd_item = -1;
     }
-    // The axis: tiles ahead of each request, in the ring's memory.
-    long long *ahead = reinterpret_cast<long long *>(ring);
-    long long W = 0;
+    // The axis: tiles ahead of each request, in the rings' memory.
+    int *ahead = reinterpret_cast<int *>(k_ring);
+    long long all = 0;
     {
         long long *ws = reinterpret_cast<long long *>(q_s);
         for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
@@ -269,19 +296,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
             }
             const long long pre = block_scan_ex(n, ws, &tot);
-            if (b < p.bs) ahead[b] = W + pre;
-            W += tot;
+            if (b < p.bs) ahead[b] = (int)min(all + pre, (long long)INT32_MAX);
+            all += tot;
         }
     }
+    if (all > INT32_MAX / 2) {  // more work than 32-bit counts hold: refused
+        if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_CAPACITY);
+        all = 0;
+    }
     __syncthreads();
-    const long long nct = min((long long)gridDim.x, W);
-    const long long first = nct ? (long long)blockIdx.x * W / nct : 0;
-    const long long last = nct ? ((long long)blockIdx.x + 1) * W / nct : 0;
-    const bool idle = blockIdx.x >= nct;
+    const int W = (int)all, nct = min((int)gridDim.x, W);
+    const bool idle = (int)blockIdx.x >= nct;
+    const Cut cut(W, max(nct, 1));
+    const int first = cut.first(blockIdx.x), last = cut.first(blockIdx.x + 1);
     if (tid == 0) k.starters[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     Walk w0 = {};
     if (!idle) {
-        int lo = 0, hi = p.bs;  // the last request with ahead <= first and work of its own
+        int lo = 0, hi = p.bs;  // the last request with ahead <= first: it has work of its own
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (ahead[mid] <= first) lo = mid; else hi = mid;
@@ -289,144 +320,160 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         int bad;
         w0.b = lo;
         w0.r = load_req(p, lo, &bad);
-        w0.nt = w0.r.token_tiles();
-        const long long in = first - ahead[lo];
-        const int item = (int)(in / w0.nt);
-        w0.t0 = (int)(in - (long long)item * w0.nt);
-        const int rt = w0.r.row_tiles(p.group);
+        w0.nt = max(w0.r.token_tiles(), 1);
+        const int in = first - ahead[lo], item = in / w0.nt;
+        w0.t0 = in - item * w0.nt;
+        const int rt = max(w0.r.row_tiles(p.group), 1);
         w0.h = item / rt;
         w0.m = item - w0.h * rt;
         w0.left = last - first;
         w0.cut();
     }
-    fence_proxy_async_smem();  // the ring's memory goes over to TMA
+    fence_proxy_async_smem();  // the rings' memory goes over to TMA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    const uint32_t t_o = tmem + 256;
+    const uint32_t t_o = tmem + kBufs * 128;
 
     if (idle) {
         // nothing
-    } else if (warp == kSoftWarps) {
+    } else if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------------------ loads
+        const bool v = warp == kWarpV;
+        const void *map_page = v ? &k.maps.v : &k.maps.k, *map_8 = v ? &k.maps.v8 : &k.maps.k8,
+                   *map_new = v ? &k.maps.vn : &k.maps.kn;
+        uint64_t *full = v ? v_full : k_full, *empty = v ? v_empty : k_empty;
+        const uint32_t ring = smem_u32(v ? v_ring : k_ring);
         if (lane == 0) {
-            prefetch_tmap(&k.maps.k);
-            prefetch_tmap(&k.maps.v);
-            prefetch_tmap(&k.maps.kn);
-            prefetch_tmap(&k.maps.vn);
+            prefetch_tmap(map_page);
+            prefetch_tmap(map_8);
+            prefetch_tmap(map_new);
         }
         const int gpp_shift = __ffs(p.page_size >> 3) - 1;  // log2 of the 8-row groups of a page
         const int bg = k.box_groups;
-        int it = 0;  // slots filled
+        int it = 0;
         Walk w = w0;
         do {
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             const int whole = (w.r.L >> 3) & ~(bg - 1);  // groups in boxes that are full of tokens
             const int32_t *table = p.page_table + (int64_t)w.r.slot * p.max_pages;
-            for (int t = w.t0; t < w.t0 + w.n; ++t) {
+            // the page a lane's load of token tile t needs (0 where it needs none)
+            auto page_of = [&](int t) {
+                const int g = t * kGroups + lane;
+                const bool ctx = lane < kGroups && g < gctx;
+                return ctx && (g >= whole || !(lane & (bg - 1))) ? table[g >> gpp_shift] : 0;
+            };
+            int page = page_of(w.t0);
+            for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
+                const int ahead_page = t + 1 < w.t0 + w.n ? page_of(t + 1) : 0;
                 const int g = t * kGroups + lane, ng = min(kGroups, gall - t * kGroups);
-                int page = 0;
                 const bool in = lane < ng, ctx = in && g < gctx;
                 const bool box = ctx && g < whole, lead = box && !(lane & (bg - 1));
-                if (lead || (ctx && !box)) {
-                    page = table[g >> gpp_shift];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
-                        page = p.num_pages;  // past the pool: zeros
-                    }
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
+                    page = p.num_pages;  // past the pool: zeros
                 }
                 const int rg = g & ((1 << gpp_shift) - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int s = it % S::kSlots;
-                    mbar_wait(&empty[s], ((it / S::kSlots) & 1) ^ 1, p.status, kKvStatusTimeout);
-                    if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
-                    __syncwarp();
-                    const uint32_t dst = smem_u32(ring) + s * S::kTileBytes + lane * S::kGroupBytes;
-                    if (lead) {
-                        const void *map = kv ? &k.maps.v : &k.maps.k;
-                        if (k.form == kPagesHeadsOut) tma_load_5d(dst, map, 0, 0, 0, rg, page * p.hkv + w.h, &full[s]);
-                        else if (k.form == kPagesHeadsIn) tma_load_5d(dst, map, 0, 0, 0, w.h, (page << gpp_shift) + rg, &full[s]);
-                        else tma_load_5d(dst, map, 0, rg * 8, 0, w.h, page, &full[s]);
-                    } else if (ctx && !box) {
-                        tma_load_5d(dst, kv ? &k.maps.v8 : &k.maps.k8, 0, rg * 8, 0, w.h, page, &full[s]);
-                    } else if (in && !ctx) {
-                        tma_load_5d(dst, kv ? &k.maps.vn : &k.maps.kn, 0, w.r.lo + (g - gctx) * 8, 0, w.h, 0, &full[s]);
-                    }
+                const int s = it % S::kSlots;
+                mbar_wait(&empty[s], ((it / S::kSlots) & 1) ^ 1, p.status, kKvStatusTimeout);
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
+                __syncwarp();
+                const uint32_t dst = ring + s * S::kTileBytes + lane * S::kGroupBytes;
+                if (lead) {
+                    if (k.form == kPagesHeadsOut) tma_load_5d(dst, map_page, 0, 0, 0, rg, page * p.hkv + w.h, &full[s]);
+                    else if (k.form == kPagesHeadsIn) tma_load_5d(dst, map_page, 0, 0, 0, w.h, (page << gpp_shift) + rg, &full[s]);
+                    else tma_load_5d(dst, map_page, 0, rg * 8, 0, w.h, page, &full[s]);
+                } else if (ctx && !box) {
+                    tma_load_5d(dst, map_8, 0, rg * 8, 0, w.h, page, &full[s]);
+                } else if (in && !ctx) {
+                    tma_load_5d(dst, map_new, 0, w.r.lo + (g - gctx) * 8, 0, w.h, 0, &full[s]);
                 }
+                page = ahead_page;
             }
         } while (w.next(p));
-    } else if (warp == kSoftWarps + 1) {
+    } else if (warp == kWarpMma) {
         // --------------------------------------------------------- products
         if (lane == 0) {
             const uint32_t ids = idesc16(F16, kTile, D, true);
-            const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(q_s);
+            const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes),
+                           v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes);
             int it = 0, item = 0;
             Walk w = w0;
             do {
                 const int gall = w.r.groups();
-                auto keys = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) / 2 * 16; };
+                auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
                 auto scores = [&](int t, int i) {
-                    const int s = (2 * i) % S::kSlots;
-                    mbar_wait(&full[s], ((2 * i) / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    const int s = i % S::kSlots, buf = i % kBufs;
+                    mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
                     tc_fence_after();
-                    const uint32_t id = idesc16(F16, kTile, keys(t), false);
+                    const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false), dst = tmem + buf * 128;
+                    const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t off = (x / 4) * 1024 + (x % 4) * 32;
-                        tc_mma_bf16(tmem + (i & 1) * 128, smem_desc(q_a + off, 16, S::kGroupBytes),
-                                    smem_desc(ring_a + s * S::kTileBytes + off, 16, S::kGroupBytes), id, x > 0);
+                        const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
+                        tc_mma_bf16(dst, q_d + off, kd + off, id, x > 0);
                     }
-                    tc_commit(&empty[s]);
-                    tc_commit(&s_full[i & 1]);
+                    tc_commit(&k_empty[s]);
+                    tc_commit(&s_full[buf]);
                 };
                 mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
                 tc_fence_after();
                 scores(w.t0, it);
+                if (w.n > 1) scores(w.t0 + 1, it + 1);
                 for (int j = 0; j < w.n; ++j, ++it) {
-                    if (j + 1 < w.n) {
-                        // the next scores take the columns that P of the tile before lies in
-                        if (j > 0) mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
-                        scores(w.t0 + j + 1, it + 1);
+                    if (j + 2 < w.n) {
+                        // those scores take the columns that P of the tile before lies in
+                        if (j > 0)
+                            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
+                        scores(w.t0 + j + 2, it + 2);
                     }
-                    mbar_wait(&p_ready[it & 1], (it >> 1) & 1, p.status, kKvStatusTimeout);
-                    const int s = (2 * it + 1) % S::kSlots;
-                    mbar_wait(&full[s], ((2 * it + 1) / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    const int s = it % S::kSlots, buf = it % kBufs;
+                    mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                     tc_fence_after();
-                    const int steps = keys(w.t0 + j) / 16;
-                    for (int x = 0; x < steps; ++x) {
-                        const uint64_t v = smem_desc(ring_a + s * S::kTileBytes + x * 2 * S::kGroupBytes, 1024, S::kGroupBytes);
-                        const uint32_t w = tmem + (it & 1) * 128 + x * 8;
-                        tc_mma_bf16_tmem_a(t_o, w, v, ids, j > 0 || x > 0);
-                        if (!F16) tc_mma_bf16_tmem_a(t_o, w + 64, v, ids, true);
+                    const int steps = steps_of(w.t0 + j);
+                    const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4);
+                    const uint32_t pt = tmem + buf * 128;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        if (x < steps) {
+                            const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
+                            tc_mma_bf16_tmem_a(t_o, pt + x * 8, d, ids, j > 0 || x > 0);
+                            if (!F16) tc_mma_bf16_tmem_a(t_o, pt + 64 + x * 8, d, ids, true);
+                        }
                     }
-                    tc_commit(&empty[s]);
-                    tc_commit(&pv_done[it & 1]);
+                    tc_commit(&v_empty[s]);
+                    tc_commit(&pv_done[buf]);
                 }
                 ++item;
             } while (w.next(p));
         }
     } else {
         // ---------------------------------------------------------- softmax
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        // warps w and w + 4 share 32 rows: tokens (or elements) 0 .. 63 and 64 .. 127 (the two halves of D)
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const float c = p.scale * kLog2e;
         constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
         int it = 0, item = 0;
         Walk w = w0;
         do {
             const int rows = w.rows(p);
-            const bool live = tid < rows, warp_live = warp * 32 < rows;
-            const int at = w.m * kTile + tid, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
-            // Q: a thread a row, into the swizzled tile
+            const bool live = row < rows, warp_live = quad * 32 < rows;
+            const int at = w.m * kTile + row, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
+            // Q: a thread half a row, into the swizzled tile
             if (live) {
-                const uint16_t *src = p.q + (int64_t)(w.r.lo + t_row) * p.q_ts + head * p.q_hs;
-                const uint32_t dst = smem_u32(q_s) + (tid >> 3) * S::kGroupBytes + (tid & 7) * 128;
+                const uint16_t *src = p.q + (int64_t)(w.r.lo + t_row) * p.q_ts + head * p.q_hs + half * (D / 2);
+                const uint32_t dst = smem_u32(q_s) + (row >> 3) * S::kGroupBytes + (row & 7) * 128;
+                uint4 v[D / 16];
 #pragma unroll
-                for (int x = 0; x < D / 8; ++x) {
-                    const uint4 v = ldg16(src + x * 8);
-                    const uint32_t a = dst + (x >> 3) * 1024 + (((x & 7) ^ (tid & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                for (int x = 0; x < D / 16; ++x) v[x] = ldg16(src + x * 8);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const int y = half * (D / 16) + x;
+                    const uint32_t a = dst + (y >> 3) * 1024 + (((y & 7) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v[x].x), "r"(v[x].y), "r"(v[x].z), "r"(v[x].w)
                                  : "memory");
                 }
             }
@@ -434,59 +481,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
 
-            float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m
+            float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this half
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             for (int j = 0; j < w.n; ++j, ++it) {
-                const int t = w.t0 + j, buf = it & 1;
-                const int nkeys = (min(kGroups, gall - t * kGroups) + 1) / 2 * 16;
+                const int t = w.t0 + j, buf = it % kBufs;
+                const int nkeys = ((min(kGroups, gall - t * kGroups) + 1) >> 1) * 16;
                 const bool edge = (t + 1) * kTile > w.r.L;  // holds more than cached tokens
                 const uint32_t t_s = tmem + buf * 128 + lane_base;
-                mbar_wait(&s_full[buf], (it >> 1) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&s_full[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
                 if (warp_live) {
-                    float s[128];
-                    {
-                        float(&a)[64] = *reinterpret_cast<float(*)[64]>(&s[0]);
-                        float(&b)[64] = *reinterpret_cast<float(*)[64]>(&s[64]);
-                        tmem_ld64(t_s, a);
-                        if (nkeys > 64) tmem_ld64(t_s + 64, b);
-                        else {
+                    float s[64];
+                    if (nkeys > half * 64) {
+                        tmem_ld64(t_s + half * 64, s);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 64; ++i) b[i] = -INFINITY;
-                        }
+                        for (int i = 0; i < 64; ++i) s[i] = -INFINITY;
                     }
                     if (edge) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int k0 = t * kTile + x * 32, n = w.r.L - k0;
+                        for (int x = 0; x < 2; ++x) {
+                            const int k0 = t * kTile + half * 64 + x * 32, n = w.r.L - k0;
                             uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
                             if (live) bits |= tree_word(p, w.r, t_row, k0 - gctx * 8);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) s[x * 32 + i] = (bits >> i) & 1 ? s[x * 32 + i] : -INFINITY;
                         }
                     }
-                    __syncwarp();
                     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    // the row's other half; both have read S once the barrier is passed, so P may
+                    // take its place
+                    pair_s[it & 1][half][row] = top;
+                    tc_fence_before();
+                    named_bar_sync(1 + quad, 64);
+                    tc_fence_after();
+                    top = fmaxf(top, pair_s[it & 1][half ^ 1][row]);
                     const bool grow = live && (top > m + kLazy || (m == -INFINITY && top > m));
                     if (__any_sync(kFullMask, grow)) {
                         const float mn = grow ? top : m;
-                        if (j > 0) {  // O so far, in units of 2^m
+                        if (j > 0) {  // O so far, in units of 2^m: this warp's half of its columns
                             const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
-                            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
+                            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
                             __syncwarp();
                             tc_fence_after();
 #pragma unroll
-                            for (int x = 0; x < D / 32; ++x) {
+                            for (int x = 0; x < D / 64; ++x) {
                                 float o[32];
                                 uint32_t u[32];
-                                tmem_ld32(t_o + lane_base + x * 32, o);
+                                const uint32_t a = t_o + lane_base + half * (D / 2) + x * 32;
+                                tmem_ld32(a, o);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                                tmem_st32(t_o + lane_base + x * 32, u);
+                                tmem_st32(a, u);
                             }
                             l *= f;
                         }
@@ -495,7 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     const float base = m == -INFINITY ? 0.0f : kShift - m;
                     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         uint32_t u[16], low[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -507,41 +557,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                 low[i] = pack_bf16x2(e0 - h.x, e1 - h.y);
                             }
                         }
-                        tmem_st16(t_s + x * 16, u);
-                        if (!F16) tmem_st16(t_s + 64 + x * 16, low);
+                        tmem_st16(t_s + half * 32 + x * 16, u);
+                        if (!F16) tmem_st16(t_s + 64 + half * 32 + x * 16, low);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
                 }
                 if (edge) {
-                    // V: a thread a token.  Rows that are no token are cleared (a weight of 0
-                    // would not silence a NaN there); what is not finite in a drafted row is
-                    // taken out, and added at the end to the rows that see it.
-                    const int sv = (2 * it + 1) % S::kSlots;
-                    mbar_wait(&full[sv], ((2 * it + 1) / S::kSlots) & 1, p.status, kKvStatusTimeout);
-                    const int vk = t * kTile + tid, jt = vk - gctx * 8;
-                    if (tid < nkeys) {
-                        unsigned char *row = ring + sv * S::kTileBytes + (tid >> 3) * S::kGroupBytes + (tid & 7) * 128;
-                        const bool drafted = jt >= 0 && jt < w.r.T;
-                        if (drafted || vk >= w.r.L) {
+                    // V: a thread half a token's row.  Rows that are no token are cleared (a weight of
+                    // 0 would not silence a NaN there); what is not finite in a drafted row is taken
+                    // out, and added at the end to the rows that see it.
+                    const int sv = it % S::kSlots;
+                    mbar_wait(&v_full[sv], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                    const int vk = t * kTile + row, jt = vk - gctx * 8;
+                    const bool drafted = jt >= 0 && jt < w.r.T;
+                    if (row < nkeys && (drafted || vk >= w.r.L)) {
+                        unsigned char *line = v_ring + sv * S::kTileBytes + (row >> 3) * S::kGroupBytes + (row & 7) * 128;
 #pragma unroll
-                            for (int x = 0; x < D / 8; ++x) {
-                                uint4 *a = reinterpret_cast<uint4 *>(row + (x >> 3) * 1024 + (x & 7) * 16);
-                                uint4 v = make_uint4(0, 0, 0, 0);
-                                if (drafted) {
-                                    v = *a;
-                                    uint32_t *e = reinterpret_cast<uint32_t *>(&v);
-                                    bool odd = false;
+                        for (int x = 0; x < D / 16; ++x) {
+                            const int y = half * (D / 16) + x;
+                            uint4 *a = reinterpret_cast<uint4 *>(line + (y >> 3) * 1024 + (y & 7) * 16);
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            bool odd = true;
+                            if (drafted) {
+                                v = *a;
+                                uint32_t *e = reinterpret_cast<uint32_t *>(&v);
+                                odd = false;
 #pragma unroll
-                                    for (int y = 0; y < 4; ++y) {
-                                        if (nonfinite16<F16>(e[y])) odd = true, e[y] &= 0xffff0000u;
-                                        if (nonfinite16<F16>(e[y] >> 16)) odd = true, e[y] &= 0x0000ffffu;
-                                    }
-                                    if (!odd) continue;
-                                    *odd_item = item;
+                                for (int z = 0; z < 4; ++z) {
+                                    if (nonfinite16<F16>(e[z])) odd = true, e[z] &= 0xffff0000u;
+                                    if (nonfinite16<F16>(e[z] >> 16)) odd = true, e[z] &= 0x0000ffffu;
                                 }
-                                *a = v;
+                                if (odd) *odd_item = item;
                             }
+                            if (odd) *a = v;
                         }
                     }
                     fence_proxy_async_smem();
@@ -551,9 +600,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (lane == 0) mbar_arrive(&p_ready[buf]);
             }
             // the segment's sums.  (A warp may be here before another has P of the tile
-            // before last ready: pv_done is two barriers, so that the parity waited for
-            // cannot be that of an older product.)
-            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, kKvStatusTimeout);
+            // before last ready: pv_done has a barrier a buffer, so that the parity waited
+            // for cannot be that of an older product.)
+            if (warp_live) {
+                pair_s[it & 1][half][row] = l;
+                named_bar_sync(1 + quad, 64);
+                l += pair_s[it & 1][half ^ 1][row];
+                // the next tile's exchange uses the other turn, but a one-tile item after it this one
+                named_bar_sync(1 + quad, 64);
+            }
+            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
             __syncwarp();
             tc_fence_after();
             if (warp_live) {
@@ -561,9 +617,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 const int cell = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
                 const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays
                 uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs;
-                float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + tid;
+                float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + row;
 #pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
+                for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
                     float o[32];
                     tmem_ld32(t_o + lane_base + x * 32, o);
                     if (live) {
@@ -595,19 +651,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     }
                     __syncwarp();  // the next load is the whole warp's
                 }
-                if (live) {
+                if (live && half == 0) {
                     if (!whole) {
-                        k.ml[cell * 2 * kTile + tid] = m;
-                        k.ml[cell * 2 * kTile + kTile + tid] = l;
+                        k.ml[cell * 2 * kTile + row] = m;
+                        k.ml[cell * 2 * kTile + kTile + row] = l;
                     } else if (p.lse) {
                         p.lse[(int64_t)(w.r.lo + t_row) * p.hq + head] =
                             l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
                     }
                 }
                 if (tid == 0 && !whole && w.t0 == 0) {
-                    // the CTA that holds the item's last tile
-                    const long long end = last - w.left + w.nt;  // first tile past the item
-                    k.starters[2 * blockIdx.x + 1] = make_int4((int)((end * nct - 1) / W), 0, 0, 0);
+                    // and the CTA that holds the item's last tile
+                    k.starters[2 * blockIdx.x + 1] = make_int4(cut.part(last - w.left + w.nt - 1), 0, 0, 0);
                     k.starters[2 * blockIdx.x] = make_int4(w.b, w.h, w.m, rows);
                 }
             }
@@ -619,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     __syncwarp();
-    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, 512);
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of the items that the axis' cuts went through: block (c, y)
