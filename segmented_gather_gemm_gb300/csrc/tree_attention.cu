@@ -105,6 +105,36 @@ __device__ __forceinline__ uint32_t idesc16(bool f16, int M, int N, bool b_mn) {
     const uint32_t fmt = f16 ? 0u : 1u;
     return (1u << 4) | fmt << 7 | fmt << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
+// MMAs and commits that every lane of a warp reaches and the one with `lead`
+// issues: the warp's control flow stays uniform, so descriptors live in
+// uniform registers and an MMA costs few issue slots, which it shares with
+// the softmax warps of its scheduler.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lead() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -394,61 +424,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         } while (w.next(p));
     } else if (warp == kWarpMma) {
         // --------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t ids = idesc16(F16, kTile, D, true);
-            const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes),
-                           v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes);
-            int it = 0, item = 0;
-            Walk w = w0;
-            do {
-                const int gall = w.r.groups();
-                auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
-                auto scores = [&](int t, int i) {
-                    const int s = i % S::kSlots, buf = i % kBufs;
-                    mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
-                    tc_fence_after();
-                    const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false), dst = tmem + buf * 128;
-                    const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
-                        tc_mma_bf16(dst, q_d + off, kd + off, id, x > 0);
-                    }
-                    tc_commit(&k_empty[s]);
-                    tc_commit(&s_full[buf]);
-                };
-                mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
+        const uint32_t lead = elect_lead();
+        const uint32_t ids = idesc16(F16, kTile, D, true);
+        const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes),
+                       v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes);
+        int it = 0, item = 0;
+        Walk w = w0;
+        do {
+            const int gall = w.r.groups();
+            auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
+            auto scores = [&](int t, int i) {
+                const int s = i % S::kSlots, buf = i % kBufs;
+                mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                __syncwarp();
                 tc_fence_after();
-                scores(w.t0, it);
-                if (w.n > 1) scores(w.t0 + 1, it + 1);
-                for (int j = 0; j < w.n; ++j, ++it) {
-                    if (j + 2 < w.n) {
-                        // those scores take the columns that P of the tile before lies in
-                        if (j > 0)
-                            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
-                        scores(w.t0 + j + 2, it + 2);
-                    }
-                    const int s = it % S::kSlots, buf = it % kBufs;
-                    mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
-                    mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
-                    tc_fence_after();
-                    const int steps = steps_of(w.t0 + j);
-                    const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4);
-                    const uint32_t pt = tmem + buf * 128;
+                const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false), dst = tmem + buf * 128;
+                const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        if (x < steps) {
-                            const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
-                            tc_mma_bf16_tmem_a(t_o, pt + x * 8, d, ids, j > 0 || x > 0);
-                            if (!F16) tc_mma_bf16_tmem_a(t_o, pt + 64 + x * 8, d, ids, true);
-                        }
-                    }
-                    tc_commit(&v_empty[s]);
-                    tc_commit(&pv_done[buf]);
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
+                    mma_ss(lead, dst, q_d + off, kd + off, id, x > 0);
                 }
-                ++item;
-            } while (w.next(p));
-        }
+                commit_one(lead, &k_empty[s]);
+                commit_one(lead, &s_full[buf]);
+            };
+            mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
+            __syncwarp();
+            tc_fence_after();
+            scores(w.t0, it);
+            if (w.n > 1) scores(w.t0 + 1, it + 1);
+            for (int j = 0; j < w.n; ++j, ++it) {
+                if (j + 2 < w.n) {
+                    // those scores take the columns that P of the tile before lies in
+                    if (j > 0)
+                        mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
+                    scores(w.t0 + j + 2, it + 2);
+                }
+                const int s = it % S::kSlots, buf = it % kBufs;
+                mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
+                __syncwarp();
+                tc_fence_after();
+                const int steps = steps_of(w.t0 + j);
+                const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4);
+                const uint32_t pt = tmem + buf * 128;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    if (x < steps) {
+                        const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
+                        mma_ts(lead, t_o, pt + x * 8, d, ids, j > 0 || x > 0);
+                        if (!F16) mma_ts(lead, t_o, pt + 64 + x * 8, d, ids, true);
+                    }
+                }
+                commit_one(lead, &v_empty[s]);
+                commit_one(lead, &pv_done[buf]);
+            }
+            ++item;
+        } while (w.next(p));
     } else {
         // ---------------------------------------------------------- softmax
         // warps w and w + 4 share 32 rows: tokens (or elements) 0 .. 63 and 64 .. 127 (the two halves of D)
