@@ -10,9 +10,17 @@
 //
 // What bounds it.  A tile of K and V (64 KB at head_dim 128) takes an SM's
 // share of HBM 1.47 us; its two products at 128 rows take the tensor core
-// 0.7 us and the exponentials of 128 x 128 scores about 0.6 us, whatever part
-// of the 128 rows is real.  So up to 128 rows one tile shape serves: bytes
-// bound it, and an MMA of fewer rows would save nothing.
+// 0.7 us and the exponentials of 128 x 128 scores 0.6 us.  So bytes bound it up
+// to about 128 rows for each kv head.
+//
+// Few rows.  Up to 16 rows (plain decoding) the products are turned over: S^T =
+// K Q^T and O^T = V^T P^T with the tokens (the elements of V) down the 128
+// lanes and 16 columns of rows, P^T in shared memory.  The tensor core then does
+// an eighth of the work, and that counts although it has time for all of it:
+// with 128-row products the power limit lowers the clock (1.3 to 1.6 GHz).
+// Up to 64 rows the rows are repeated in the upper 64 lanes; each copy
+// keeps its own maximum and sum over its half of every tile's tokens (its
+// weights for the other half are 0), and the copies are joined once an item.
 //
 // Split.  The tiles of all (request, kv head, row tile) items form one axis
 // that is cut into equal parts, one a CTA (one CTA an SM), so a batch of
@@ -35,6 +43,7 @@
 
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "serving.cuh"
 
@@ -61,8 +70,10 @@ struct Shape {
     static constexpr int kSlots = D == 128 ? 3 : 6;    // of each ring
     static constexpr int kRing = 2 * kSlots * kTileBytes;
     static constexpr int kBars = 4 * kSlots + 3 * kBufs + 1;
+    static constexpr int kQBytes = 32768;               // Q, or 16 rows of it and P^T
     static constexpr int kPairBytes = 2 * 2 * kTile * 4;
-    static constexpr int kSmem = kTileBytes + kRing + kPairBytes + (kBars + 1) * 8 + 64;
+    static constexpr int kTurnBytes = 64 + 2 * 256;     // flags, maxima, sums
+    static constexpr int kSmem = kQBytes + kRing + kPairBytes + kTurnBytes + (kBars + 1) * 8 + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -92,18 +103,19 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle: `lbo` the distance of
-// 64-element blocks along the contiguous dimension (used when that is not K),
-// `sbo` the distance of 8-row groups.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+// Shared-memory matrix descriptor, 128-byte (or 64-byte) swizzle: `lbo` the
+// distance of whole swizzle widths along the contiguous dimension (used when
+// that is not K), `sbo` the distance of 8-row groups.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, bool swizzle64 = false) {
     return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)(swizzle64 ? 4 : 2) << 61;
 }
-// Instruction descriptor of kind::f16, fp32 accumulation; `b_mn`: B is stored
-// with its N dimension contiguous.
-__device__ __forceinline__ uint32_t idesc16(bool f16, int M, int N, bool b_mn) {
+// Instruction descriptor of kind::f16, fp32 accumulation; `a_mn` / `b_mn`: A /
+// B is stored with its M / N dimension contiguous.
+__device__ __forceinline__ uint32_t idesc16(bool f16, int M, int N, bool a_mn, bool b_mn) {
     const uint32_t fmt = f16 ? 0u : 1u;
-    return (1u << 4) | fmt << 7 | fmt << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+    return (1u << 4) | fmt << 7 | fmt << 10 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 // MMAs and commits that every lane of a warp reaches and the one with `lead`
 // issues: the warp's control flow stays uniform, so descriptors live in
@@ -159,6 +171,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 64) tmem_ld64(taddr, v);
+    else tmem_ld32(taddr, v);
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if (F16) {
@@ -166,6 +195,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         return *reinterpret_cast<const uint32_t *>(&v);
     }
     return pack_bf16x2(lo, hi);
+}
+// What packing two numbers to 16 bits left of them, packed.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2_rest(uint32_t packed, float lo, float hi) {
+    float2 h;
+    if (F16) h = __half22float2(*reinterpret_cast<const __half2 *>(&packed));
+    else h = unpack_bf16x2(packed);
+    return pack2<F16>(lo - h.x, hi - h.y);
 }
 template <bool F16>
 __device__ __forceinline__ bool nonfinite16(uint32_t x) {
@@ -236,6 +273,8 @@ struct Walk {
     }
     __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kTile, r.T * p.group - m * kTile); }
 };
+// Up to kFewRows rows: turned over; up to kSomeRows: two copies.
+constexpr int kFewRows = 16, kSomeRows = 64;
 
 // 32 bits of row t's mask from drafted token j0 (which may be negative: lower
 // bits are then 0), cut at T.
@@ -274,9 +313,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     using S = Shape<D>;
     const AttnParams &p = k.p;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *q_s = smem, *k_ring = smem + S::kTileBytes, *v_ring = k_ring + S::kSlots * S::kTileBytes;
+    unsigned char *q_s = smem, *k_ring = smem + S::kQBytes, *v_ring = k_ring + S::kSlots * S::kTileBytes;
     float(*pair_s)[2][kTile] = reinterpret_cast<float(*)[2][kTile]>(k_ring + S::kRing);  // a row's two halves, by turns
-    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kPairBytes);
+    int4 *flag_s = reinterpret_cast<int4 *>(k_ring + S::kRing + S::kPairBytes);  // [turn][half] of the four quadrants
+    float(*max_s)[4][8] = reinterpret_cast<float(*)[4][8]>(flag_s + 4), (*sum_s)[4][8] = max_s + 2;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kPairBytes + S::kTurnBytes);
     uint64_t *k_full = bars, *k_empty = k_full + S::kSlots, *v_full = k_empty + S::kSlots, *v_empty = v_full + S::kSlots,
              *s_full = v_empty + S::kSlots, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
              *q_ready = pv_done + kBufs;
@@ -382,21 +423,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         }
         const int gpp_shift = __ffs(p.page_size >> 3) - 1;  // log2 of the 8-row groups of a page
         const int bg = k.box_groups;
+        // the page a lane's load of token tile t needs (0 where it needs none)
+        auto page_of = [&](const Walk &w, int t) {
+            const int g = t * kGroups + lane, whole = (w.r.L >> 3) & ~(bg - 1);
+            const bool ctx = lane < kGroups && g < w.r.ctx_groups();
+            return ctx && (g >= whole || !(lane & (bg - 1))) ? p.page_table[(int64_t)w.r.slot * p.max_pages + (g >> gpp_shift)] : 0;
+        };
         int it = 0;
-        Walk w = w0;
+        Walk w = w0, wn = w0;
+        int page = page_of(w, w.t0);
+        bool more;
         do {
+            more = wn.next(p);  // looked up while this segment's tiles are loaded
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             const int whole = (w.r.L >> 3) & ~(bg - 1);  // groups in boxes that are full of tokens
-            const int32_t *table = p.page_table + (int64_t)w.r.slot * p.max_pages;
-            // the page a lane's load of token tile t needs (0 where it needs none)
-            auto page_of = [&](int t) {
-                const int g = t * kGroups + lane;
-                const bool ctx = lane < kGroups && g < gctx;
-                return ctx && (g >= whole || !(lane & (bg - 1))) ? table[g >> gpp_shift] : 0;
-            };
-            int page = page_of(w.t0);
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
-                const int ahead_page = t + 1 < w.t0 + w.n ? page_of(t + 1) : 0;
+                const int next_page = t + 1 < w.t0 + w.n ? page_of(w, t + 1) : more ? page_of(wn, wn.t0) : 0;
                 const int g = t * kGroups + lane, ng = min(kGroups, gall - t * kGroups);
                 const bool in = lane < ng, ctx = in && g < gctx;
                 const bool box = ctx && g < whole, lead = box && !(lane & (bg - 1));
@@ -419,31 +461,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 } else if (in && !ctx) {
                     tma_load_5d(dst, map_new, 0, w.r.lo + (g - gctx) * 8, 0, w.h, 0, &full[s]);
                 }
-                page = ahead_page;
+                page = next_page;
             }
-        } while (w.next(p));
+            w = wn;
+        } while (more);
     } else if (warp == kWarpMma) {
         // --------------------------------------------------------- products
         const uint32_t lead = elect_lead();
-        const uint32_t ids = idesc16(F16, kTile, D, true);
+        const uint32_t id_pv = idesc16(F16, kTile, D, false, true), id_pv_few = idesc16(F16, kTile, 32, true, true),
+                       id_few = idesc16(F16, kTile, 16, false, false);
         const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes),
-                       v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes);
+                       v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes),
+                       p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
         int it = 0, item = 0;
         Walk w = w0;
+        bool more;
         do {
+            Walk wn = w;
+            more = wn.next(p);
             const int gall = w.r.groups();
+            const bool few = w.rows(p) <= kFewRows;
             auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
             auto scores = [&](int t, int i) {
                 const int s = i % S::kSlots, buf = i % kBufs;
+                // the buffer's last P has been used
+                if (i >= kBufs) mbar_wait(&pv_done[buf], ((i / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
                 mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false), dst = tmem + buf * 128;
+                const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false, false), dst = tmem + buf * 128;
                 const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
+                if (few) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
-                    mma_ss(lead, dst, q_d + off, kd + off, id, x > 0);
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
+                        mma_ss(lead, dst, kd + off, q_d + off, id_few, x > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
+                        mma_ss(lead, dst, q_d + off, kd + off, id, x > 0);
+                    }
                 }
                 commit_one(lead, &k_empty[s]);
                 commit_one(lead, &s_full[buf]);
@@ -454,112 +513,349 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             scores(w.t0, it);
             if (w.n > 1) scores(w.t0 + 1, it + 1);
             for (int j = 0; j < w.n; ++j, ++it) {
-                if (j + 2 < w.n) {
-                    // those scores take the columns that P of the tile before lies in
-                    if (j > 0)
-                        mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
-                    scores(w.t0 + j + 2, it + 2);
-                }
+                if (j + 2 < w.n) scores(w.t0 + j + 2, it + 2);
                 const int s = it % S::kSlots, buf = it % kBufs;
                 mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
                 mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
                 const int steps = steps_of(w.t0 + j);
-                const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4);
+                const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4), pd = p_d + (uint32_t)(buf * 8192 >> 4);
                 const uint32_t pt = tmem + buf * 128;
+                if (few) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    if (x < steps) {
-                        const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
-                        mma_ts(lead, t_o, pt + x * 8, d, ids, j > 0 || x > 0);
-                        if (!F16) mma_ts(lead, t_o, pt + 64 + x * 8, d, ids, true);
+                    for (int x = 0; x < 8; ++x)
+                        if (x < steps)
+                            mma_ss(lead, t_o, vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4), pd + (uint32_t)(x * 1024 >> 4),
+                                   id_pv_few, j > 0 || x > 0);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        if (x < steps) {
+                            const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
+                            mma_ts(lead, t_o, pt + x * 8, d, id_pv, j > 0 || x > 0);
+                            if (!F16) mma_ts(lead, t_o, pt + 64 + x * 8, d, id_pv, true);
+                        }
                     }
                 }
                 commit_one(lead, &v_empty[s]);
                 commit_one(lead, &pv_done[buf]);
             }
             ++item;
-        } while (w.next(p));
+            w = wn;
+        } while (more);
     } else {
         // ---------------------------------------------------------- softmax
-        // warps w and w + 4 share 32 rows: tokens (or elements) 0 .. 63 and 64 .. 127 (the two halves of D)
-        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+        // warps w and w + 4 share 32 lanes
+        const int quad = warp & 3, half = warp >> 2, pos = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const float c = p.scale * kLog2e;
         constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
         int it = 0, item = 0;
         Walk w = w0;
-        do {
-            const int rows = w.rows(p);
-            const bool live = row < rows, warp_live = quad * 32 < rows;
-            const int at = w.m * kTile + row, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
-            // Q: a thread half a row, into the swizzled tile
-            if (live) {
-                const uint16_t *src = p.q + (int64_t)(w.r.lo + t_row) * p.q_ts + head * p.q_hs + half * (D / 2);
-                const uint32_t dst = smem_u32(q_s) + (row >> 3) * S::kGroupBytes + (row & 7) * 128;
-                uint4 v[D / 16];
+        bool more;
+
+        // Q of a segment: from memory, and into the swizzled tile.  A thread has
+        // half a row; 16 bytes when the products are turned over.
+        uint4 qv[D / 16];
+        auto lane_row = [&](int rows) { return rows <= kSomeRows ? (quad & 1) * 32 + lane : pos; };
+        auto q_src = [&](const Walk &u, int row, int el) {
+            const int at = u.m * kTile + row, t = at / p.group;
+            return p.q + (int64_t)(u.r.lo + t) * p.q_ts + (u.h * p.group + (at - t * p.group)) * p.q_hs + el;
+        };
+        auto q_load = [&](const Walk &u) {
+            const int rows = u.rows(p);
+            if (rows <= kFewRows) {
+                const int row = tid / (D / 8), el = (tid % (D / 8)) * 8;
+                if (row < rows) qv[0] = ldg16(q_src(u, row, el));
+            } else {
+                const int row = lane_row(rows);
+                if (row < rows) {
+                    const uint16_t *src = q_src(u, row, half * (D / 2));
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) v[x] = ldg16(src + x * 8);
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const int y = half * (D / 16) + x;
-                    const uint32_t a = dst + (y >> 3) * 1024 + (((y & 7) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v[x].x), "r"(v[x].y), "r"(v[x].z), "r"(v[x].w)
-                                 : "memory");
+                    for (int x = 0; x < D / 16; ++x) qv[x] = ldg16(src + x * 8);
                 }
+            }
+        };
+        auto q_put = [&](int row, int chunk, uint4 v) {
+            const uint32_t a = smem_u32(q_s) + (row >> 3) * S::kGroupBytes + (row & 7) * 128 + (chunk >> 3) * 1024 +
+                               (((chunk & 7) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        };
+        auto q_store = [&](const Walk &u) {
+            const int rows = u.rows(p);
+            if (rows <= kFewRows) {
+                const int row = tid / (D / 8);
+                if (row < rows) q_put(row, tid % (D / 8), qv[0]);
+            } else if (lane_row(rows) < rows) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) q_put(pos, half * (D / 16) + x, qv[x]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
+        };
+        q_load(w);
+        q_store(w);
 
-            float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this half
+        do {
+            Walk wn = w;
+            more = wn.next(p);
+            const int rows = w.rows(p);
+            const bool few = rows <= kFewRows, twice = !few && rows <= kSomeRows;
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
-            for (int j = 0; j < w.n; ++j, ++it) {
-                const int t = w.t0 + j, buf = it % kBufs;
-                const int nkeys = ((min(kGroups, gall - t * kGroups) + 1) >> 1) * 16;
-                const bool edge = (t + 1) * kTile > w.r.L;  // holds more than cached tokens
-                const uint32_t t_s = tmem + buf * 128 + lane_base;
-                mbar_wait(&s_full[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
+            const bool whole = w.n == w.nt;
+            const int cell = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
+            auto keys_of = [&](int t) { return ((min(kGroups, gall - t * kGroups) + 1) >> 1) * 16; };
+            auto edge = [&](int t) { return (t + 1) * kTile > w.r.L; };  // holds more than cached tokens
+            auto await_s = [&]() {
+                mbar_wait(&s_full[it % kBufs], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
-                if (warp_live) {
-                    float s[64];
-                    if (nkeys > half * 64) {
-                        tmem_ld64(t_s + half * 64, s);
+            };
+            auto await_pv = [&]() {  // of the tile before
+                mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
+                __syncwarp();
+                tc_fence_after();
+            };
+            // V of an edge tile.  Rows that are no token are cleared (a weight of 0 would not silence a
+            // NaN there); what is not finite in a drafted row is taken out, and added at the end to the
+            // rows that see it.
+            auto clean_v = [&](int t) {
+                const int sv = it % S::kSlots;
+                mbar_wait(&v_full[sv], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                const int r0 = max(w.r.L - t * kTile, 0), n = (keys_of(t) - r0) * (D / 8);
+                for (int i = tid; i < n; i += kSoftWarps * 32) {
+                    const int r = r0 + i / (D / 8), y = i % (D / 8), jt = t * kTile + r - gctx * 8;
+                    uint4 *a = reinterpret_cast<uint4 *>(v_ring + sv * S::kTileBytes + (r >> 3) * S::kGroupBytes +
+                                                         (r & 7) * 128 + (y >> 3) * 1024 + (y & 7) * 16);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    bool odd = true;
+                    if (jt >= 0 && jt < w.r.T) {
+                        v = *a;
+                        uint32_t *e = reinterpret_cast<uint32_t *>(&v);
+                        odd = false;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            if (nonfinite16<F16>(e[z])) odd = true, e[z] &= 0xffff0000u;
+                            if (nonfinite16<F16>(e[z] >> 16)) odd = true, e[z] &= 0x0000ffffu;
+                        }
+                        if (odd) *odd_item = item;
+                    }
+                    if (odd) *a = v;
+                }
+                fence_proxy_async_smem();
+            };
+            auto p_is_ready = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[it % kBufs]);
+            };
+            // What row t sees of the drafted tokens' non-finite values, from element el on.
+            auto add_odd = [&](int t, int el, auto &o) {
+                constexpr int N = sizeof(o) / sizeof(float);
+                for (int j = 0; j < w.r.T; ++j) {
+                    const int vt = (gctx * 8 + j) / kTile;
+                    if (vt < w.t0 || vt >= w.t0 + w.n || !(tree_word(p, w.r, t, j) & 1)) continue;
+                    const uint16_t *v = p.v_new + (int64_t)(w.r.lo + j) * p.n_ts + w.h * p.n_hs + el;
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (nonfinite16<F16>(v[i])) o[i] += widen<F16>(v[i]);
+                }
+            };
+            auto inverse = [](float l) { return l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l; };  // NaN stays
+            auto put_row = [&](int row, float m, float l) {  // what a row leaves beside O
+                if (!whole) {
+                    k.ml[cell * 2 * kTile + row] = m;
+                    k.ml[cell * 2 * kTile + kTile + row] = l;
+                } else if (p.lse) {
+                    const int at = w.m * kTile + row, t = at / p.group;
+                    p.lse[(int64_t)(w.r.lo + t) * p.hq + w.h * p.group + (at - t * p.group)] =
+                        l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+                }
+            };
+
+            if (few) {
+                // ------------------------------------------- turned over
+                // a thread has token `pos` and rows 8 half .. 8 half + 7, of which nl are real
+                const int nl = min(8, rows - 8 * half);
+                float m[8], l[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+                for (int j = 0; j < w.n; ++j, ++it) {
+                    const int t = w.t0 + j, buf = it % kBufs;
+                    await_s();
+                    if (nl > 0) {
+                        float s[8];
+                        tmem_ld8(tmem + buf * 128 + lane_base + 8 * half, s);
+                        uint32_t see = (1u << nl) - 1u;
+                        const int vk = t * kTile + pos;
+                        if (vk >= w.r.L) {
+                            const int jt = vk - gctx * 8;
+                            uint32_t bits = 0;
+                            if (jt >= 0 && jt < w.r.T)
+                                for (int r = 0; r < nl; ++r)
+                                    bits |= (tree_word(p, w.r, (w.m * kTile + 8 * half + r) / p.group, jt) & 1u) << r;
+                            see &= bits;
+                        }
+                        __syncwarp();
+                        bool grow = false;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            s[r] = (see >> r) & 1 ? s[r] : -INFINITY;
+                            grow |= s[r] * c > m[r] + kLazy;  // from -inf: any score at all
+                        }
+                        const bool any = __any_sync(kFullMask, grow);
+                        if (lane == 0) reinterpret_cast<int *>(flag_s + (it & 1) * 2 + half)[quad] = any;
+                        named_bar_sync(6 + half, 128);
+                        const int4 f4 = flag_s[(it & 1) * 2 + half];
+                        if (f4.x | f4.y | f4.z | f4.w) {
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) {
+                                float x = s[r] * c;
+#pragma unroll
+                                for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, o));
+                                if (lane == 0) max_s[half][quad][r] = x;
+                            }
+                            named_bar_sync(6 + half, 128);
+                            float f[8];
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) {
+                                const float x = fmaxf(fmaxf(max_s[half][0][r], max_s[half][1][r]),
+                                                      fmaxf(max_s[half][2][r], max_s[half][3][r]));
+                                const float mn = x > m[r] + kLazy ? x : m[r];
+                                f[r] = mn > m[r] ? ex2(m[r] - mn) : 1.0f;
+                                m[r] = mn;
+                                l[r] *= f[r];
+                            }
+                            if (j > 0) {  // O^T so far
+                                await_pv();
+#pragma unroll
+                                for (int part = 0; part < 2; ++part) {
+                                    const uint32_t a = t_o + lane_base + part * 16 + half * 8;
+                                    float o[8];
+                                    uint32_t u[8];
+                                    tmem_ld8(a, o);
+#pragma unroll
+                                    for (int r = 0; r < 8; ++r) u[r] = __float_as_uint(o[r] * f[r]);
+                                    tmem_st8(a, u);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        uint32_t hi[4], low[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float e[2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int r = 2 * i + y;
+                                e[y] = ex2(fmaf(s[r], c, m[r] == -INFINITY ? 0.0f : kShift - m[r]));
+                                l[r] += e[y];
+                            }
+                            hi[i] = pack2<F16>(e[0], e[1]);
+                            low[i] = pack2_rest<F16>(hi[i], e[0], e[1]);
+                        }
+                        if (it >= kBufs)  // the product before in this buffer
+                            mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
+                        // P^T: 64 bytes a token, high parts of 16 rows, then the low parts; 64-byte swizzle
+                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + ((half ^ x) << 4)), "r"(hi[0]),
+                                     "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + (((2 + half) ^ x) << 4)), "r"(low[0]),
+                                     "r"(low[1]), "r"(low[2]), "r"(low[3])
+                                     : "memory");
+                    }
+                    if (edge(t)) clean_v(t);
+                    else fence_proxy_async_smem();
+                    p_is_ready();
+                }
+                // Q of the next segment, unless P^T is still read where it goes
+                const bool early = more && wn.rows(p) <= kFewRows;
+                if (more) q_load(wn);
+                if (nl > 0) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        l[r] = warp_sum(l[r]);
+                        if (lane == 0) sum_s[half][quad][r] = l[r];
+                    }
+                    named_bar_sync(6 + half, 128);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        l[r] = (sum_s[half][0][r] + sum_s[half][1][r]) + (sum_s[half][2][r] + sum_s[half][3][r]);
+                }
+                if (early) q_store(wn);
+                await_pv();
+                if (nl > 0) {
+                    float o[8], low[8];
+                    tmem_ld8(t_o + lane_base + half * 8, o);
+                    tmem_ld8(t_o + lane_base + 16 + half * 8, low);
+                    if (pos < D) {  // a thread has element `pos`
+                        const bool odd = *odd_item == item;
+                        float *part = k.part + ((int64_t)cell * (D / 4) + pos / 4) * kTile * 4 + (pos & 3);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            if (r < nl) {
+                                const int row = 8 * half + r, at = w.m * kTile + row, tr = at / p.group;
+                                float x[1] = {o[r] + low[r]};
+                                if (odd) add_odd(tr, pos, x);
+                                if (whole)
+                                    p.out[(int64_t)(w.r.lo + tr) * p.o_ts + (w.h * p.group + (at - tr * p.group)) * p.o_hs + pos] =
+                                        (uint16_t)pack2<F16>(x[0] * inverse(l[r]), 0.0f);
+                                else part[row * 4] = x[0];
+                                if (pos == 0) put_row(row, m[r], l[r]);
+                            }
+                        }
+                    }
+                }
+                if (more && !early) q_store(wn);
+            } else {
+                // ------------------------------------------------- as is
+                // a thread has a row, and half of its copy's share of the tokens (and of O's columns)
+                const int copy = twice ? quad >> 1 : 0, row = lane_row(rows);
+                const bool live = row < rows, warp_live = row - lane < rows;
+                const int at = w.m * kTile + row, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
+                float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this half
+                // P of one tile; N: tokens of this warp
+                auto weigh = [&](auto n_tag, int j) {
+                    constexpr int N = decltype(n_tag)::value;
+                    const int t = w.t0 + j, c0 = (2 * copy + half) * N;
+                    const uint32_t t_s = tmem + (it % kBufs) * 128 + lane_base;
+                    float s[N];
+                    if (keys_of(t) > c0) {
+                        tmem_load(t_s + c0, s);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = -INFINITY;
+                        for (int i = 0; i < N; ++i) s[i] = -INFINITY;
                     }
-                    if (edge) {
+                    if (edge(t)) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int k0 = t * kTile + half * 64 + x * 32, n = w.r.L - k0;
+                        for (int x = 0; x < N; x += 32) {
+                            const int k0 = t * kTile + c0 + x, n = w.r.L - k0;
                             uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
                             if (live) bits |= tree_word(p, w.r, t_row, k0 - gctx * 8);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[x * 32 + i] = (bits >> i) & 1 ? s[x * 32 + i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) s[x + i] = (bits >> i) & 1 ? s[x + i] : -INFINITY;
                         }
                     }
+                    __syncwarp();
                     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                    for (int i = 4; i < N; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
                     float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    // the row's other half; both have read S once the barrier is passed, so P may
-                    // take its place
-                    pair_s[it & 1][half][row] = top;
+                    // the other half; both have read S once the barrier is passed, so P may take its place
+                    pair_s[it & 1][half][pos] = top;
                     tc_fence_before();
                     named_bar_sync(1 + quad, 64);
                     tc_fence_after();
-                    top = fmaxf(top, pair_s[it & 1][half ^ 1][row]);
-                    const bool grow = live && (top > m + kLazy || (m == -INFINITY && top > m));
+                    top = fmaxf(top, pair_s[it & 1][half ^ 1][pos]);
+                    const bool grow = live && top > m + kLazy;  // from -inf: any score at all
                     if (__any_sync(kFullMask, grow)) {
                         const float mn = grow ? top : m;
                         if (j > 0) {  // O so far, in units of 2^m: this warp's half of its columns
                             const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
-                            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
-                            __syncwarp();
-                            tc_fence_after();
+                            await_pv();
 #pragma unroll
                             for (int x = 0; x < D / 64; ++x) {
                                 float o[32];
@@ -577,130 +873,129 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     const float base = m == -INFINITY ? 0.0f : kShift - m;
                     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < N / 2; x += 16) {
                         uint32_t u[16], low[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float e0 = ex2(fmaf(s[x * 32 + 2 * i], c, base)), e1 = ex2(fmaf(s[x * 32 + 2 * i + 1], c, base));
+                            const float e0 = ex2(fmaf(s[2 * (x + i)], c, base)), e1 = ex2(fmaf(s[2 * (x + i) + 1], c, base));
                             sum[i & 3] += e0 + e1;
                             u[i] = pack2<F16>(e0, e1);
-                            if (!F16) {
-                                const float2 h = unpack_bf16x2(u[i]);
-                                low[i] = pack_bf16x2(e0 - h.x, e1 - h.y);
-                            }
+                            if (!F16) low[i] = pack2_rest<F16>(u[i], e0, e1);
                         }
-                        tmem_st16(t_s + half * 32 + x * 16, u);
-                        if (!F16) tmem_st16(t_s + 64 + half * 32 + x * 16, low);
+                        tmem_st16(t_s + c0 / 2 + x, u);
+                        if (!F16) tmem_st16(t_s + 64 + c0 / 2 + x, low);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
-                }
-                if (edge) {
-                    // V: a thread half a token's row.  Rows that are no token are cleared (a weight of
-                    // 0 would not silence a NaN there); what is not finite in a drafted row is taken
-                    // out, and added at the end to the rows that see it.
-                    const int sv = it % S::kSlots;
-                    mbar_wait(&v_full[sv], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
-                    const int vk = t * kTile + row, jt = vk - gctx * 8;
-                    const bool drafted = jt >= 0 && jt < w.r.T;
-                    if (row < nkeys && (drafted || vk >= w.r.L)) {
-                        unsigned char *line = v_ring + sv * S::kTileBytes + (row >> 3) * S::kGroupBytes + (row & 7) * 128;
-#pragma unroll
-                        for (int x = 0; x < D / 16; ++x) {
-                            const int y = half * (D / 16) + x;
-                            uint4 *a = reinterpret_cast<uint4 *>(line + (y >> 3) * 1024 + (y & 7) * 16);
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            bool odd = true;
-                            if (drafted) {
-                                v = *a;
-                                uint32_t *e = reinterpret_cast<uint32_t *>(&v);
-                                odd = false;
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    if (nonfinite16<F16>(e[z])) odd = true, e[z] &= 0xffff0000u;
-                                    if (nonfinite16<F16>(e[z] >> 16)) odd = true, e[z] &= 0x0000ffffu;
-                                }
-                                if (odd) *odd_item = item;
-                            }
-                            if (odd) *a = v;
-                        }
+                    if constexpr (N < 64) {  // no weight for the other copy's tokens: half its columns each
+                        const uint32_t zero[16] = {};
+                        const uint32_t a = t_s + (copy ^ 1) * 32 + half * 16;
+                        tmem_st16(a, zero);
+                        if (!F16) tmem_st16(a + 64, zero);
                     }
-                    fence_proxy_async_smem();
+                    tmem_wait_st();
+                };
+                for (int j = 0; j < w.n; ++j, ++it) {
+                    await_s();
+                    if (warp_live) {
+                        if (twice) weigh(std::integral_constant<int, 32>{}, j);
+                        else weigh(std::integral_constant<int, 64>{}, j);
+                    }
+                    if (edge(w.t0 + j)) clean_v(w.t0 + j);
+                    p_is_ready();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[buf]);
-            }
-            // the segment's sums.  (A warp may be here before another has P of the tile
-            // before last ready: pv_done has a barrier a buffer, so that the parity waited
-            // for cannot be that of an older product.)
-            if (warp_live) {
-                pair_s[it & 1][half][row] = l;
-                named_bar_sync(1 + quad, 64);
-                l += pair_s[it & 1][half ^ 1][row];
-                // the next tile's exchange uses the other turn, but a one-tile item after it this one
-                named_bar_sync(1 + quad, 64);
-            }
-            mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
-            __syncwarp();
-            tc_fence_after();
-            if (warp_live) {
-                const bool whole = w.n == w.nt, odd = *odd_item == item;
-                const int cell = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
-                const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays
-                uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs;
-                float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + row;
+                // Q of the next segment (its products with this one's Q are done), unless the copies
+                // are joined where it goes
+                if (more) q_load(wn);
+                if (warp_live) {
+                    pair_s[it & 1][half][pos] = l;
+                    named_bar_sync(1 + quad, 64);
+                    l += pair_s[it & 1][half ^ 1][pos];
+                    named_bar_sync(1 + quad, 64);  // the next tile's exchange may be in this turn again
+                }
+                if (more && !twice) q_store(wn);
+                // (A warp may be here before another has P of the tile before last ready: pv_done has a
+                // barrier a buffer, so that the parity waited for cannot be that of an older product.)
+                await_pv();
+                float f = 1.0f;
+                float4 *o_s = reinterpret_cast<float4 *>(q_s) + row;  // [D / 4][64 rows] of the upper copy
+                if (twice) {
+                    if (warp_live && half == 0) {
+                        pair_s[0][0][pos] = m;
+                        pair_s[0][1][pos] = l;
+                    }
+                    named_bar_sync(5, kSoftWarps * 32);
+                    const float m2 = pair_s[0][0][pos ^ 64], l2 = pair_s[0][1][pos ^ 64], ma = fmaxf(m, m2);
+                    const float base = ma == -INFINITY ? 0.0f : ma;
+                    f = ex2(m - base);
+                    l = l * f + l2 * ex2(m2 - base);
+                    m = ma;
+                    if (copy == 1 && warp_live) {
 #pragma unroll 1
-                for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
-                    float o[32];
-                    tmem_ld32(t_o + lane_base + x * 32, o);
-                    if (live) {
-                        if (odd) {
-                            for (int j = 0; j < w.r.T; ++j) {
-                                const int vt = (gctx * 8 + j) / kTile;
-                                if (vt < w.t0 || vt >= w.t0 + w.n || !(tree_word(p, w.r, t_row, j) & 1)) continue;
-                                const uint16_t *v = p.v_new + (int64_t)(w.r.lo + j) * p.n_ts + w.h * p.n_hs + x * 32;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (nonfinite16<F16>(v[i])) o[i] += widen<F16>(v[i]);
-                            }
-                        }
-                        if (whole) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint4 v;
-                                v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                                v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                                v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                                v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-                                *reinterpret_cast<uint4 *>(dst + x * 32 + i * 8) = v;
-                            }
-                        } else {
+                        for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
+                            float o[32];
+                            tmem_ld32(t_o + lane_base + x * 32, o);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                part[(x * 8 + i) * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                                o_s[(x * 8 + i) * 64] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
                         }
                     }
-                    __syncwarp();  // the next load is the whole warp's
+                    named_bar_sync(5, kSoftWarps * 32);
                 }
-                if (live && half == 0) {
-                    if (!whole) {
-                        k.ml[cell * 2 * kTile + row] = m;
-                        k.ml[cell * 2 * kTile + kTile + row] = l;
-                    } else if (p.lse) {
-                        p.lse[(int64_t)(w.r.lo + t_row) * p.hq + head] =
-                            l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+                if (warp_live && copy == 0) {
+                    const bool odd = *odd_item == item;
+                    const float inv = inverse(l);
+                    uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs;
+                    float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + row;
+#pragma unroll 1
+                    for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
+                        float o[32];
+                        tmem_ld32(t_o + lane_base + x * 32, o);
+                        if (live) {
+                            if (twice) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 v = o_s[(x * 8 + i) * 64];
+                                    o[4 * i] = o[4 * i] * f + v.x;
+                                    o[4 * i + 1] = o[4 * i + 1] * f + v.y;
+                                    o[4 * i + 2] = o[4 * i + 2] * f + v.z;
+                                    o[4 * i + 3] = o[4 * i + 3] * f + v.w;
+                                }
+                            }
+                            if (odd) add_odd(t_row, x * 32, o);
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    uint4 v;
+                                    v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                                    v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                                    v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                                    v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                                    *reinterpret_cast<uint4 *>(dst + x * 32 + i * 8) = v;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    part[(x * 8 + i) * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            }
+                        }
+                        __syncwarp();  // the next load is the whole warp's
                     }
+                    if (live && half == 0) put_row(row, m, l);
                 }
-                if (tid == 0 && !whole && w.t0 == 0) {
-                    // and the CTA that holds the item's last tile
-                    k.starters[2 * blockIdx.x + 1] = make_int4(cut.part(last - w.left + w.nt - 1), 0, 0, 0);
-                    k.starters[2 * blockIdx.x] = make_int4(w.b, w.h, w.m, rows);
+                if (twice) {
+                    named_bar_sync(5, kSoftWarps * 32);
+                    if (more) q_store(wn);
                 }
+            }
+            if (tid == 0 && !whole && w.t0 == 0) {
+                // this CTA begins the item; and the CTA that holds its last tile
+                k.starters[2 * blockIdx.x + 1] = make_int4(cut.part(last - w.left + w.nt - 1), 0, 0, 0);
+                k.starters[2 * blockIdx.x] = make_int4(w.b, w.h, w.m, rows);
             }
             tc_fence_before();
             ++item;
-        } while (w.next(p));
+            w = wn;
+        } while (more);
     }
     tc_fence_before();
     __syncthreads();
