@@ -543,7 +543,9 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  * rounded to half, or to a bfloat16 pair of 16 bits.  Results do not depend on
  * timing.  A page number out of range sets CSGMV_KV_STATUS_BAD_PAGE and makes
  * its request's rows meaningless; other bad requests are left out (their rows
- * of out and lse stay as they are).  bs <= 16384.
+ * of out and lse stay as they are).  bs <= 16000;
+ * CSGMV_KV_STATUS_CAPACITY and no output when the batch's cost does not fit 31
+ * bits (some 10^9 cached tokens times kv heads).
  *   workspace      csgmv_tree_attention_workspace_bytes(); contents do not matter
  */
 CSGMV_API int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads,

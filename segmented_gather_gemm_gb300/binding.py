@@ -399,17 +399,30 @@ def _need(ok: bool, msg: str):
 
 def _need_i32(name: str, t: torch.Tensor | None, *shape):
     """t is a dense int32 tensor on a GPU of that shape (None: any extent)."""
-    if t is None:
-        return
-    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous int32 CUDA tensor")
-    _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)),
-          f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t is not None and (t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or
+                          not _has_shape(t.shape, shape)):
+        raise CsgmvError(-1, f"{name} must be a contiguous int32 CUDA tensor of shape {shape}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _need_f32(name: str, t: torch.Tensor, *shape):
-    _need(t.dtype == torch.float32 and t.is_cuda, f"{name} must be a float32 CUDA tensor")
-    _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)),
-          f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype is not torch.float32 or not t.is_cuda or not _has_shape(t.shape, shape):
+        raise CsgmvError(-1, f"{name} must be a float32 CUDA tensor of shape {shape}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _has_shape(have, want) -> bool:
+    return have == want or (len(have) == len(want) and all(w is None or w == n for n, w in zip(have, want)))
+
+
+def _at(t: torch.Tensor | None):
+    """t's address, as the calls take it."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    """The CUDA stream handle to launch on: stream, or torch's current one."""
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
 
 
 def _alike(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -508,9 +521,9 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
     _need_i32("accept_index", accept_index, bs, width)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need_i32("seq_slots", seq_slots, bs)
-    _check(lib().csgmv_kv_commit(cache._ref, _ptr(k_new), _ptr(v_new), int(k_new.stride(0)), int(k_new.stride(1)),
-                                 int(k_new.stride(2)), int(k_new.shape[1]), _ptr(accept_index), width,
-                                 _ptr(accept_len), _ptr(tree_indptr), _ptr(seq_slots), bs, _stream(stream)))
+    _check(lib().csgmv_kv_commit(cache._ref, _at(k_new), _at(v_new), int(k_new.stride(0)), int(k_new.stride(1)),
+                                 int(k_new.stride(2)), int(k_new.shape[1]), _at(accept_index), width,
+                                 _at(accept_len), _at(tree_indptr), _at(seq_slots), bs, _raw_stream(stream)))
 
 
 def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
@@ -518,7 +531,7 @@ def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor,
     n = int(parents.numel())
     _need_i32("parents", parents, n)
     _need_i32("children", children, n)
-    _check(lib().csgmv_kv_fork(cache._ref, _ptr(parents), _ptr(children), n, _stream(stream)))
+    _check(lib().csgmv_kv_fork(cache._ref, _at(parents), _at(children), n, _raw_stream(stream)))
 
 
 def csgmv_kv_free(cache: KvCache, seqs: torch.Tensor, keep_lens: torch.Tensor | None = None, stream=None) -> None:
@@ -526,12 +539,12 @@ def csgmv_kv_free(cache: KvCache, seqs: torch.Tensor, keep_lens: torch.Tensor | 
     n = int(seqs.numel())
     _need_i32("seqs", seqs, n)
     _need_i32("keep_lens", keep_lens, n)
-    _check(lib().csgmv_kv_free(cache._ref, _ptr(seqs), _ptr(keep_lens), n, _stream(stream)))
+    _check(lib().csgmv_kv_free(cache._ref, _at(seqs), _at(keep_lens), n, _raw_stream(stream)))
 
 
 def csgmv_kv_compact(cache: KvCache, stream=None) -> None:
     """Moves live pages into the holes below them; live pages end up first."""
-    _check(lib().csgmv_kv_compact(cache._ref, _stream(stream)))
+    _check(lib().csgmv_kv_compact(cache._ref, _raw_stream(stream)))
 
 
 def csgmv_kv_copy_pages(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -539,7 +552,7 @@ def csgmv_kv_copy_pages(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, st
     n = int(src.numel())
     _need_i32("src", src, n)
     _need_i32("dst", dst, n)
-    _check(lib().csgmv_kv_copy_pages(cache._ref, _ptr(src), _ptr(dst), n, _stream(stream)))
+    _check(lib().csgmv_kv_copy_pages(cache._ref, _at(src), _at(dst), n, _raw_stream(stream)))
 
 
 def csgmv_tree_attention_workspace_bytes(cache: KvCache, num_q_heads: int) -> int:
@@ -574,10 +587,10 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     if workspace is None:
         workspace = torch.empty(csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
     _check(lib().csgmv_tree_attention(
-        _ptr(q), int(q.stride(0)), int(q.stride(1)), hq, _ptr(k_new), _ptr(v_new), int(k_new.stride(0)),
-        int(k_new.stride(1)), cache._ref, int(layer), _ptr(tree_indptr), _ptr(seq_slots), bs, n, _ptr(mask), words,
-        float(d ** -0.5 if scale is None else scale), _ptr(out), int(out.stride(0)), int(out.stride(1)), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _at(q), int(q.stride(0)), int(q.stride(1)), hq, _at(k_new), _at(v_new), int(k_new.stride(0)),
+        int(k_new.stride(1)), cache._ref, int(layer), _at(tree_indptr), _at(seq_slots), bs, n, _at(mask), words,
+        float(d ** -0.5 if scale is None else scale), _at(out), int(out.stride(0)), int(out.stride(1)), _at(lse),
+        _at(workspace), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
     return out
 
 
@@ -606,9 +619,9 @@ def csgmv_build_draft_tree(tree: DraftTree, parents: torch.Tensor, tree_indptr: 
     _need_i32("parents", parents, n)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need(n <= int(tree.depth.numel()), f"{n} nodes exceed the tree's {tree.depth.numel()}")
-    _check(lib().csgmv_build_draft_tree(_ptr(parents), _ptr(tree_indptr), bs, n, tree.words, _ptr(tree.mask),
-                                        _ptr(tree.depth), _ptr(tree.first_child), _ptr(tree.next_sibling),
-                                        _ptr(tree.status), _stream(stream)))
+    _check(lib().csgmv_build_draft_tree(_at(parents), _at(tree_indptr), bs, n, tree.words, _at(tree.mask),
+                                        _at(tree.depth), _at(tree.first_child), _at(tree.next_sibling),
+                                        _at(tree.status), _raw_stream(stream)))
 
 
 def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, tree_indptr: torch.Tensor,
@@ -645,8 +658,8 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
     ts = int(target_probs.stride(0)) if n > 1 else vocab
     ds = 0 if draft_probs is None else int(draft_probs.stride(0)) if n > 1 else vocab
     _check(lib().csgmv_verify_drafts(
-        _ptr(target_probs), ts, _ptr(draft_probs), ds, _ptr(draft_tokens), _ptr(tree_indptr),
-        _ptr(tree.first_child), _ptr(tree.next_sibling), _ptr(accept_uniforms), _ptr(sample_uniforms), bs, n, vocab,
-        _ptr(accept_index), int(accept_index.shape[1]), _ptr(accept_len), _ptr(next_token), _ptr(tree.status),
-        _stream(stream)))
+        _at(target_probs), ts, _at(draft_probs), ds, _at(draft_tokens), _at(tree_indptr),
+        _at(tree.first_child), _at(tree.next_sibling), _at(accept_uniforms), _at(sample_uniforms), bs, n, vocab,
+        _at(accept_index), int(accept_index.shape[1]), _at(accept_len), _at(next_token), _at(tree.status),
+        _raw_stream(stream)))
     return accept_index, accept_len, next_token

@@ -23,11 +23,11 @@
 // weights for the other half are 0), and the copies are joined once an item.
 //
 // Split.  The tiles of all (request, kv head, row tile) items form one axis
-// that is cut into equal parts, one a CTA (one CTA an SM), so a batch of
-// ragged lengths and a single long sequence both fill the GPU.  An item cut
-// by the ends of a part leaves fp32 partial sums in the workspace (at most two
-// a CTA), which a second kernel joins in order of the axis: results do not
-// depend on timing.
+// that is cut into parts of equal cost (cost_of below), one a CTA (one CTA an
+// SM), so a batch of ragged lengths and a single long sequence both fill the
+// GPU.  An item cut by the ends of a part leaves fp32 partial sums in the
+// workspace (at most two a CTA), which a second kernel joins in order of the
+// axis: results do not depend on timing.
 //
 // Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
 // keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
@@ -57,7 +57,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kWarpK = kSoftWarps, kWarpV = kSoftWarps + 1, kWarpMma = kSoftWarps + 2;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 3);
 constexpr int kBufs = 3;           // S buffers in tensor memory
-constexpr int kMaxRequests = 16384;
+constexpr int kMaxRequests = 16000;  // 12 bytes each in the rings' memory
 constexpr int kCombineThreads = 128;
 constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
 constexpr float kLog2e = 1.4426950408889634f;
@@ -77,7 +77,7 @@ struct Shape {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-struct alignas(64) AttnMaps {
+struct AttnMaps {
     CUtensorMap k, v;    // whole boxes of a page
     CUtensorMap k8, v8;  // 8 rows of a page
     CUtensorMap kn, vn;  // 8 rows of the drafted tokens
@@ -89,7 +89,8 @@ struct AttnKernelParams {
     AttnMaps maps;
     float *part;      // [2 * kAttnCtas][D / 4][kTile] float4: unscaled O
     float *ml;        // [2 * kAttnCtas][2][kTile]: m, l
-    int4 *starters;   // [2 * kAttnCtas]: item a CTA begins and does not end: {b, h, row tile, rows}, {last CTA, ..}
+    int4 *starters;   // [kAttnCtas]: the item a CTA begins and does not end {first token, h, row tile, rows}, or {-1}
+    int *tails;       // [kAttnCtas]: of an item begun by an earlier CTA: 0 nothing, 1 a middle part, 2 its end
     int form;         // kPages*
     int box_groups;   // 8-row groups of a whole box
 };
@@ -222,9 +223,6 @@ struct Req {
     __device__ __forceinline__ int groups() const { return ctx_groups() + ((T + 7) >> 3); }
     __device__ __forceinline__ int token_tiles() const { return (groups() + kGroups - 1) / kGroups; }
     __device__ __forceinline__ int row_tiles(int group) const { return (T * group + kTile - 1) / kTile; }
-    __device__ __forceinline__ long long tiles(int group, int hkv) const {
-        return (long long)row_tiles(group) * hkv * token_tiles();
-    }
 };
 
 // Request b, with T = 0 (no work) when it is not sound; the status bit why.
@@ -246,35 +244,76 @@ __device__ __forceinline__ Req load_req(const AttnParams &p, int b, int *bad) {
     return r;
 }
 
+// Up to kFewRows rows: turned over; up to kSomeRows: two copies.
+constexpr int kFewRows = 16, kSomeRows = 64;
+
+// What the parts of the axis are weighed by, in units of 64 clocks.  Measured
+// on long axes: a tile's K and V come in 2870 (head_dim 64: 1430) clocks of an
+// SM's share of HBM, shared by the row tiles of a head, which find them in L2;
+// its softmax takes 1000 clocks turned over, 1400 in two copies, 1750 (half) or
+// 2100 (bfloat16) for a full row tile.  Beginning and ending an item costs 800
+// turned over, 5000 otherwise.  With equal tile counts instead, the CTAs of
+// short sequences ran 15 to 30 % longer than the others.
+struct Cost {
+    int mt, nt;          // row tiles and token tiles
+    int tile[2], item[2];  // of a full row tile, of the last: one token tile, the whole item
+    int head;            // a kv head's items
+};
+__device__ __forceinline__ int tile_cost(int rows, int mt, int d, bool f16) {
+    const int bytes = (d == 128 ? 45 : 22) / mt;
+    return max(bytes, rows <= kFewRows ? 16 : rows <= kSomeRows ? 22 : f16 ? 28 : 33);
+}
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 78; }
+__device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p) {
+    Cost c;
+    const Req r = {0, T, L, 0};
+    c.mt = r.row_tiles(p.group);
+    c.nt = r.token_tiles();
+    const int rest = T * p.group - (c.mt - 1) * kTile;
+    c.tile[0] = tile_cost(kTile, c.mt, p.d, p.f16);
+    c.tile[1] = tile_cost(rest, c.mt, p.d, p.f16);
+    c.item[0] = item_cost(kTile) + c.nt * c.tile[0];
+    c.item[1] = item_cost(rest) + c.nt * c.tile[1];
+    c.head = (c.mt - 1) * c.item[0] + c.item[1];
+    return c;
+}
+
+// A place on the axis: token tile t of an item.
+struct Place {
+    int b, h, m, t;
+    __device__ __forceinline__ bool same_item(int b2, int h2, int m2) const { return b == b2 && h == h2 && m == m2; }
+};
+
 // A CTA's part of the axis, walked item by item.
 struct Walk {
     Req r;
     int b, h, m, t0;   // request, kv head, row tile, first token tile of the segment
     int n, nt;         // token tiles of the segment, of the item
-    int left;          // tiles of the part, this segment's included
-    __device__ __forceinline__ void cut() { n = min(nt - t0, left); }
+    Place end;         // first tile past the part
+    __device__ __forceinline__ bool cut() {
+        n = (end.same_item(b, h, m) ? min(end.t, nt) : nt) - t0;
+        return n > 0;
+    }
     __device__ __forceinline__ bool next(const AttnParams &p) {
-        left -= n;
-        if (left <= 0 || (m + 1 == r.row_tiles(p.group) && h + 1 == p.hkv && b + 1 >= p.bs)) return false;
+        if (end.same_item(b, h, m)) return false;
         t0 = 0;
         if (++m == r.row_tiles(p.group)) {
             m = 0;
             if (++h == p.hkv) {
                 h = 0;
-                int bad;
                 do {
-                    r = load_req(p, ++b, &bad);
-                } while (r.T == 0 && b + 1 < p.bs);
+                    if (++b >= p.bs) return false;
+                    int bad;
+                    r = load_req(p, b, &bad);
+                } while (r.T == 0 && b < end.b);
+                if (r.T == 0) return false;
                 nt = r.token_tiles();
             }
         }
-        cut();
-        return true;
+        return cut();
     }
     __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kTile, r.T * p.group - m * kTile); }
 };
-// Up to kFewRows rows: turned over; up to kSomeRows: two copies.
-constexpr int kFewRows = 16, kSomeRows = 64;
 
 // 32 bits of row t's mask from drafted token j0 (which may be negative: lower
 // bits are then 0), cut at T.
@@ -296,17 +335,38 @@ __device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r,
     return lim >= 32 ? x : x & ((1u << lim) - 1u);
 }
 
-// The even cut of W tiles into n parts: the first W % n have one tile more.
-struct Cut {
-    int q, r;
-    __device__ __forceinline__ Cut(int W, int n) : q(W / n), r(W - W / n * n) {}
-    __device__ __forceinline__ int first(int c) const { return c * q + min(c, r); }
-    // The part that holds tile x.
-    __device__ __forceinline__ int part(int x) const {
-        const int big = r * (q + 1);
-        return x < big ? x / (q + 1) : r + (x - big) / q;
+// The place x units of cost along the axis (every CTA rounds it alike).
+// `ahead`: cost before each request, and the total; `tl`: their T and L.
+__device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead, const int2 *tl, int x) {
+    Place q = {p.bs, 0, 0, 0};
+    if (x >= ahead[p.bs]) return q;
+    int lo = 0, hi = p.bs;  // the last request with ahead <= x: it has work of its own
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ahead[mid] <= x) lo = mid; else hi = mid;
     }
-};
+    const Cost c = cost_of(tl[lo].x, tl[lo].y, p);
+    q.b = lo;
+    int y = x - ahead[lo];
+    q.h = y / c.head;
+    y -= q.h * c.head;
+    q.m = min(y / c.item[0], c.mt - 1);
+    y -= q.m * c.item[0];
+    const int last = q.m == c.mt - 1, cost = c.tile[last];
+    y -= c.item[last] - c.nt * cost;
+    q.t = y <= 0 ? 0 : (y + cost - 1) / cost;
+    if (q.t >= c.nt) {  // the next item's beginning
+        q.t = 0;
+        if (++q.m == c.mt) {
+            q.m = 0;
+            if (++q.h == p.hkv) {
+                q.h = 0;
+                do ++q.b; while (q.b < p.bs && ahead[q.b + 1] == ahead[q.b]);
+            }
+        }
+    }
+    return q;
+}
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant__ AttnKernelParams k) {
@@ -325,11 +385,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    griddep_launch_dependents();
+    // (The join is not launched early: its blocks among this kernel's cost 12 us a call.)
     if (smem_u32(smem) & 1023) {  // the swizzled tiles count on it
         if (tid == 0) {
             atomicOr(p.status, kKvStatusTimeout);
-            k.starters[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+            k.starters[blockIdx.x] = make_int4(-1, 0, 0, 0);
         }
         return;
     }
@@ -353,17 +413,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         fence_mbar_init();
         *odd_item = -1;
     }
-    // The axis: tiles ahead of each request, in the rings' memory.
+    griddep_wait();
+    // The axis: cost ahead of each request, and its T and L, in the rings' memory.
     int *ahead = reinterpret_cast<int *>(k_ring);
+    int2 *tl = reinterpret_cast<int2 *>(k_ring + ((4 * p.bs + 4 + 15) & ~15));
+    Place *ends = reinterpret_cast<Place *>(q_s);
     long long all = 0;
     {
-        long long *ws = reinterpret_cast<long long *>(q_s);
+        long long *ws = reinterpret_cast<long long *>(q_s + 64);
         for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
             const int b = b0 + tid;
             long long n = 0, tot;
             if (b < p.bs) {
                 int bad;
-                n = load_req(p, b, &bad).tiles(p.group, p.hkv);
+                const Req r = load_req(p, b, &bad);
+                if (r.T) n = (long long)cost_of(r.T, r.L, p).head * p.hkv;
+                tl[b] = make_int2(r.T, r.L);
                 if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
             }
             const long long pre = block_scan_ex(n, ws, &tot);
@@ -371,34 +436,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             all += tot;
         }
     }
-    if (all > INT32_MAX / 2) {  // more work than 32-bit counts hold: refused
+    if (all > INT32_MAX) {  // more than 32 bits of cost: refused
         if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_CAPACITY);
         all = 0;
     }
+    if (tid == 0) ahead[p.bs] = (int)all;
     __syncthreads();
-    const int W = (int)all, nct = min((int)gridDim.x, W);
-    const bool idle = (int)blockIdx.x >= nct;
-    const Cut cut(W, max(nct, 1));
-    const int first = cut.first(blockIdx.x), last = cut.first(blockIdx.x + 1);
-    if (tid == 0) k.starters[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // this CTA's part: two warps find its two ends
+    if (lane == 0 && warp < 2) {
+        const int q = (int)all / (int)gridDim.x, rest = (int)all - q * (int)gridDim.x, c = blockIdx.x + warp;
+        ends[warp] = place_at(p, ahead, tl, c * q + min(c, rest));
+    }
+    if (tid == 0) {
+        k.starters[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        k.tails[blockIdx.x] = 0;
+    }
+    __syncthreads();
     Walk w0 = {};
+    {
+        const Place at = ends[0];
+        w0.b = at.b;
+        w0.h = at.h;
+        w0.m = at.m;
+        w0.t0 = at.t;
+        w0.end = ends[1];
+    }
+    bool idle = all == 0 || w0.b >= p.bs;
     if (!idle) {
-        int lo = 0, hi = p.bs;  // the last request with ahead <= first: it has work of its own
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (ahead[mid] <= first) lo = mid; else hi = mid;
-        }
         int bad;
-        w0.b = lo;
-        w0.r = load_req(p, lo, &bad);
-        w0.nt = max(w0.r.token_tiles(), 1);
-        const int in = first - ahead[lo], item = in / w0.nt;
-        w0.t0 = in - item * w0.nt;
-        const int rt = max(w0.r.row_tiles(p.group), 1);
-        w0.h = item / rt;
-        w0.m = item - w0.h * rt;
-        w0.left = last - first;
-        w0.cut();
+        w0.r = load_req(p, w0.b, &bad);
+        w0.nt = w0.r.token_tiles();
+        idle = !w0.cut();
     }
     fence_proxy_async_smem();  // the rings' memory goes over to TMA
     tc_fence_before();
@@ -987,10 +1055,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     if (more) q_store(wn);
                 }
             }
-            if (tid == 0 && !whole && w.t0 == 0) {
-                // this CTA begins the item; and the CTA that holds its last tile
-                k.starters[2 * blockIdx.x + 1] = make_int4(cut.part(last - w.left + w.nt - 1), 0, 0, 0);
-                k.starters[2 * blockIdx.x] = make_int4(w.b, w.h, w.m, rows);
+            if (tid == 0 && !whole) {
+                if (w.t0 == 0) k.starters[blockIdx.x] = make_int4(w.r.lo, w.h, w.m, rows);
+                else k.tails[blockIdx.x] = w.t0 + w.n == w.nt ? 2 : 1;
             }
             tc_fence_before();
             ++item;
@@ -1004,46 +1071,96 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the items that the axis' cuts went through: block (c, y)
-// the item that CTA c began, in order of the axis.
+// Joins the parts of the items that the axis' cuts went through, in order of
+// the axis.  The rows of all such items are dealt out to the blocks R at a
+// time.  Two rounds of dependent loads: which items and parts there are, and
+// the parts (O and its scales together).
 template <int D, bool F16>
-__global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant__ AttnKernelParams k) {
-    griddep_wait();
+__global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant__ AttnKernelParams k, int ctas) {
+    constexpr int R = kCombineThreads / (D / 4);  // rows of a block
+    static_assert(2 * kCombineThreads >= kAttnCtas, "two items a thread");
+    __shared__ int first[2 * kCombineThreads + 1], ws[33], tails[2 * kCombineThreads];
+    __shared__ int4 items[2 * kCombineThreads];
     const AttnParams &p = k.p;
-    const int c0 = blockIdx.x;
-    const int4 head4 = k.starters[2 * c0];
-    if (head4.x < 0) return;
-    const int c1 = k.starters[2 * c0 + 1].x, rows = head4.w, n = rows * (D / 4);
-    constexpr float kShift = F16 ? 4.0f : 0.0f;
-    const int lo = p.indptr[head4.x];
-    for (int e = blockIdx.y * kCombineThreads + threadIdx.x; e < n; e += gridDim.y * kCombineThreads) {
-        const int d4 = e / rows, row = e - d4 * rows;
-        auto cell = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
-        float m = -INFINITY;
-        for (int c = c0; c <= c1; ++c) m = fmaxf(m, k.ml[cell(c) * 2 * kTile + row]);
-        const float base = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float f = ex2(k.ml[cell(c) * 2 * kTile + row] - base);
-            l += k.ml[cell(c) * 2 * kTile + kTile + row] * f;
-            const float4 v = reinterpret_cast<const float4 *>(k.part)[((int64_t)cell(c) * (D / 4) + d4) * kTile + row];
-            // a part of all-masked tiles counts for nothing (its m is -inf, its O is 0)
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
+    const int tid = threadIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();
+    int mine[2], all;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = 2 * tid + i;
+        items[c] = c < ctas ? k.starters[c] : make_int4(-1, 0, 0, 0);
+        tails[c] = c < ctas ? k.tails[c] : 0;
+        mine[i] = items[c].x < 0 ? 0 : (items[c].w + R - 1) / R;
+    }
+    const int pre = block_scan_ex(mine[0] + mine[1], ws, &all);
+    first[2 * tid] = pre;
+    first[2 * tid + 1] = pre + mine[0];
+    if (tid == 0) first[2 * kCombineThreads] = all;
+    __syncthreads();
+    for (int job = blockIdx.x; job < all; job += gridDim.x) {
+        int c0 = 0;  // the last CTA with first <= job: it begins an item
+        for (int hi = 2 * kCombineThreads; hi - c0 > 1;) {
+            const int mid = (c0 + hi) >> 1;
+            if (first[mid] <= job) c0 = mid; else hi = mid;
         }
-        const int at = head4.z * kTile + row, t = at / p.group, head = head4.y * p.group + (at - t * p.group);
-        const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-        uint2 u;
-        u.x = pack2<F16>(o.x * inv, o.y * inv);
-        u.y = pack2<F16>(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(p.out + (int64_t)(lo + t) * p.o_ts + head * p.o_hs + d4 * 4) = u;
-        if (d4 == 0 && p.lse)
-            p.lse[(int64_t)(lo + t) * p.hq + head] =
-                l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+        const int4 head4 = items[c0];
+        const int r = tid / (D / 4), d4 = tid % (D / 4), row = (job - first[c0]) * R + r;
+        if (row < head4.w) {
+            // the CTAs with a part of it: up to the first that holds its end.  Sums in base 2^m of
+            // the largest maximum so far
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            constexpr int U = 8;  // parts in flight
+            bool end = false;
+            for (int c = c0; c < ctas && !end; c += U) {
+                float ms[U], ls[U];
+                float4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int cu = c + u, cell = 2 * cu + (cu == c0 ? 1 : 0);
+                    const bool has = !end && cu < ctas && (cu == c0 || tails[cu] != 0);
+                    ms[u] = -INFINITY;
+                    ls[u] = 0.0f;
+                    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (has) {
+                        ms[u] = k.ml[cell * 2 * kTile + row];
+                        ls[u] = k.ml[cell * 2 * kTile + kTile + row];
+                        v[u] = reinterpret_cast<const float4 *>(k.part)[((int64_t)cell * (D / 4) + d4) * kTile + row];
+                        end = cu != c0 && tails[cu] == 2;
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int u = 0; u < U; ++u) top = fmaxf(top, ms[u]);
+                const float base = top == -INFINITY ? 0.0f : top, f = ex2(m - base);
+                l *= f;
+                o.x *= f;
+                o.y *= f;
+                o.z *= f;
+                o.w *= f;
+                m = top;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {  // (a part of nothing but masked tokens has m = -inf and O = 0)
+                    const float g = ex2(ms[u] - base);
+                    l += ls[u] * g;
+                    o.x += v[u].x * g;
+                    o.y += v[u].y * g;
+                    o.z += v[u].z * g;
+                    o.w += v[u].w * g;
+                }
+            }
+            constexpr float kShift = F16 ? 4.0f : 0.0f;
+            const int at = head4.z * kTile + row, t = at / p.group, head = head4.y * p.group + (at - t * p.group);
+            const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+            uint2 u;
+            u.x = pack2<F16>(o.x * inv, o.y * inv);
+            u.y = pack2<F16>(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2 *>(p.out + (int64_t)(head4.x + t) * p.o_ts + head * p.o_hs + d4 * 4) = u;
+            if (d4 == 0 && p.lse)
+                p.lse[(int64_t)(head4.x + t) * p.hq + head] =
+                    l == 0.0f ? -INFINITY : (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+        }
     }
 }
 
@@ -1076,9 +1193,19 @@ cudaError_t prepare(int *ctas) {
         {reinterpret_cast<const void *>(attend<64, false>), Shape<64>::kSmem},
         {reinterpret_cast<const void *>(attend<64, true>), Shape<64>::kSmem},
         {reinterpret_cast<const void *>(attend<128, false>), Shape<128>::kSmem},
-        {reinterpret_cast<const void *>(attend<128, true>), Shape<128>::kSmem}};
-    for (const auto &f : all)
-        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess) return e;
+        {reinterpret_cast<const void *>(attend<128, true>), Shape<128>::kSmem},
+        {reinterpret_cast<const void *>(combine<64, false>), 0},
+        {reinterpret_cast<const void *>(combine<64, true>), 0},
+        {reinterpret_cast<const void *>(combine<128, false>), 0},
+        {reinterpret_cast<const void *>(combine<128, true>), 0}};
+    for (const auto &f : all) {
+        if (f.smem && (e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem)) != cudaSuccess)
+            return e;
+        // both kernels with the same split of L1: an SM drains to change it
+        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
+    }
     *ctas = g_ready[dev] = sms < kAttnCtas ? sms : kAttnCtas;
     return cudaSuccess;
 }
@@ -1102,12 +1229,12 @@ bool encode(CUtensorMap *map, const void *base, bool f16, const int64_t (&dim)[5
 
 template <int D, bool F16>
 cudaError_t launch(const AttnKernelParams &k, int ctas, cudaStream_t stream) {
-    cudaError_t e = launch_kernel(attend<D, F16>, dim3((unsigned)ctas), kAttnThreads, Shape<D>::kSmem, stream, 0, false, k);
+    cudaError_t e = launch_kernel(attend<D, F16>, dim3((unsigned)ctas), kAttnThreads, Shape<D>::kSmem, stream, 0, true, k);
     if (e != cudaSuccess) return e;
-    return launch_kernel(combine<D, F16>, dim3((unsigned)ctas, 8), kCombineThreads, 0, stream, 0, true, k);
+    return launch_kernel(combine<D, F16>, dim3(4 * (unsigned)ctas), kCombineThreads, 0, stream, 0, true, k, ctas);
 }
 
-constexpr size_t kStarterBytes = 2 * kAttnCtas * sizeof(int4);
+constexpr size_t kStarterBytes = kAttnCtas * (sizeof(int4) + sizeof(int4));  // starters, then tails
 constexpr size_t kMlBytes = 2 * (size_t)kAttnCtas * 2 * kTile * sizeof(float);
 
 }  // namespace
@@ -1126,6 +1253,7 @@ cudaError_t launch_tree_attention(const AttnParams &p, void *workspace, cudaStre
     k.p = p;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     k.starters = reinterpret_cast<int4 *>(ws);
+    k.tails = reinterpret_cast<int *>(ws + kAttnCtas * sizeof(int4));
     k.ml = reinterpret_cast<float *>(ws + kStarterBytes);
     k.part = reinterpret_cast<float *>(ws + kStarterBytes + kMlBytes);
 
