@@ -420,14 +420,22 @@ def _at(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    """The CUDA stream handle to launch on: stream, or torch's current one."""
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+# torch.cuda.current_stream() builds an object (3 us); the handle alone is a lookup
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device: int):
+    """The CUDA stream handle to launch on: stream, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _alike(a: torch.Tensor, b: torch.Tensor) -> bool:
     """Same shape and the same strides where they matter."""
-    return a.shape == b.shape and (a.numel() == 0 or all(
+    return a.shape == b.shape and (a.stride() == b.stride() or a.numel() == 0 or all(
         n <= 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride())))
 
 
@@ -474,6 +482,9 @@ class KvCache:
         c.num_kv_heads, c.head_dim, c.max_seqs, c.max_pages_per_seq = heads, d, seqs, max_pages
         self.c = c
         self._ref = ctypes.byref(c)
+        self.dtype, self.device = k_pages.dtype, k_pages.get_device()
+        self.num_layers, self.num_pages, self.page_size = layers, pages, ps
+        self.num_kv_heads, self.head_dim, self.max_seqs, self.max_pages_per_seq = heads, d, seqs, max_pages
 
     @classmethod
     def allocate(cls, num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
@@ -486,10 +497,6 @@ class KvCache:
                    torch.full((max_seqs, max_pages_per_seq), -1, **i32), torch.zeros(max_seqs, **i32),
                    torch.zeros(num_pages, **i32), layout=layout)
 
-    @property
-    def dtype(self) -> torch.dtype:
-        return self.k_pages.dtype
-
     def device_status(self) -> int:
         return int(self.status.item())
 
@@ -498,13 +505,16 @@ def csgmv_kv_scratch_ints(num_pages: int, max_seqs: int) -> int:
     return int(lib().csgmv_kv_scratch_ints(int(num_pages), int(max_seqs)))
 
 
-def _new_rows(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, dims: int):
-    _need(k_new.dim() == dims and _alike(k_new, v_new),
-          f"k_new / v_new must have {dims} dimensions and the same shape and strides")
-    _need(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.is_cuda and v_new.is_cuda,
+def _new_rows(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, lead: tuple):
+    """k_new / v_new are (*lead, kv_heads, head_dim) in the cache's type; their strides."""
+    st = k_new.stride()
+    _need(_has_shape(k_new.shape, lead + (cache.num_kv_heads, cache.head_dim)) and st[-1] == 1,
+          f"k_new / v_new must be {lead + (cache.num_kv_heads, cache.head_dim)} (the cache's layers, kv_heads and "
+          f"head_dim), the last dimension dense, not {tuple(k_new.shape)}")
+    _need(_alike(k_new, v_new), "k_new / v_new must have the same shape and strides")
+    _need(k_new.dtype is cache.dtype and v_new.dtype is cache.dtype and k_new.is_cuda and v_new.is_cuda,
           "k_new / v_new must be CUDA tensors of the cache's type")
-    _need(k_new.shape[-1] == cache.c.head_dim and k_new.shape[-2] == cache.c.num_kv_heads and k_new.stride(-1) == 1,
-          "k_new / v_new must end in (kv_heads, head_dim), the last dimension dense")
+    return st
 
 
 def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, accept_index: torch.Tensor | None,
@@ -513,46 +523,48 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
     """Appends accept_len[b] of request b's rows of k_new / v_new (layers,
     tokens, kv_heads, head_dim) to its sequence: rows tree_indptr[b] +
     accept_index[b, j], or its first rows without an accept_index."""
-    _new_rows(cache, k_new, v_new, 4)
-    _need(int(k_new.shape[0]) == cache.c.num_layers, "k_new / v_new must have the cache's layers")
-    bs = int(accept_len.numel())
-    width = 0 if accept_index is None else int(accept_index.shape[-1])
+    st = _new_rows(cache, k_new, v_new, (cache.num_layers, None))
+    bs = accept_len.numel()
+    width = 0 if accept_index is None else accept_index.shape[-1]
     _need_i32("accept_len", accept_len, bs)
     _need_i32("accept_index", accept_index, bs, width)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need_i32("seq_slots", seq_slots, bs)
-    _check(lib().csgmv_kv_commit(cache._ref, _at(k_new), _at(v_new), int(k_new.stride(0)), int(k_new.stride(1)),
-                                 int(k_new.stride(2)), int(k_new.shape[1]), _at(accept_index), width,
-                                 _at(accept_len), _at(tree_indptr), _at(seq_slots), bs, _raw_stream(stream)))
+    rc = lib().csgmv_kv_commit(cache._ref, k_new.data_ptr(), v_new.data_ptr(), st[0], st[1], st[2], k_new.shape[1],
+                               _at(accept_index), width, accept_len.data_ptr(), tree_indptr.data_ptr(),
+                               _at(seq_slots), bs, _raw_stream(stream, cache.device))
+    if rc:
+        _check(rc)
 
 
 def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
     """Sequence children[i] becomes a copy of sequence parents[i]."""
-    n = int(parents.numel())
+    n = parents.numel()
     _need_i32("parents", parents, n)
     _need_i32("children", children, n)
-    _check(lib().csgmv_kv_fork(cache._ref, _at(parents), _at(children), n, _raw_stream(stream)))
+    _check(lib().csgmv_kv_fork(cache._ref, parents.data_ptr(), children.data_ptr(), n,
+                               _raw_stream(stream, cache.device)))
 
 
 def csgmv_kv_free(cache: KvCache, seqs: torch.Tensor, keep_lens: torch.Tensor | None = None, stream=None) -> None:
     """Cuts sequence seqs[i] back to keep_lens[i] tokens (None: to nothing)."""
-    n = int(seqs.numel())
+    n = seqs.numel()
     _need_i32("seqs", seqs, n)
     _need_i32("keep_lens", keep_lens, n)
-    _check(lib().csgmv_kv_free(cache._ref, _at(seqs), _at(keep_lens), n, _raw_stream(stream)))
+    _check(lib().csgmv_kv_free(cache._ref, seqs.data_ptr(), _at(keep_lens), n, _raw_stream(stream, cache.device)))
 
 
 def csgmv_kv_compact(cache: KvCache, stream=None) -> None:
     """Moves live pages into the holes below them; live pages end up first."""
-    _check(lib().csgmv_kv_compact(cache._ref, _raw_stream(stream)))
+    _check(lib().csgmv_kv_compact(cache._ref, _raw_stream(stream, cache.device)))
 
 
 def csgmv_kv_copy_pages(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Copies the contents of pages src[i] to pages dst[i] in every layer."""
-    n = int(src.numel())
+    n = src.numel()
     _need_i32("src", src, n)
     _need_i32("dst", dst, n)
-    _check(lib().csgmv_kv_copy_pages(cache._ref, _at(src), _at(dst), n, _raw_stream(stream)))
+    _check(lib().csgmv_kv_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), n, _raw_stream(stream, cache.device)))
 
 
 def csgmv_tree_attention_workspace_bytes(cache: KvCache, num_q_heads: int) -> int:
@@ -568,16 +580,15 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     cached sequence and over its own rows of k_new / v_new that `mask` (int32
     bits, (tokens, words); None: causal) lets each row see.  scale defaults to
     head_dim ** -0.5; lse (tokens, heads) f32 is optional."""
-    _need(q.dim() == 3 and out.shape == q.shape, "q and out must be (tokens, heads, head_dim)")
-    _need(q.dtype == cache.dtype and out.dtype == cache.dtype and q.is_cuda and out.is_cuda,
+    shape, qs, os_ = q.shape, q.stride(), out.stride()
+    _need(len(shape) == 3 and out.shape == shape, "q and out must be (tokens, heads, head_dim)")
+    _need(q.dtype is cache.dtype and out.dtype is cache.dtype and q.is_cuda and out.is_cuda,
           "q and out must be CUDA tensors of the cache's type")
-    n, hq, d = (int(x) for x in q.shape)
-    _need(d == cache.c.head_dim and (n == 0 or q.stride(2) == 1 and out.stride(2) == 1),
-          "q and out must have the cache's head_dim, dense")
-    _new_rows(cache, k_new, v_new, 3)
-    _need(int(k_new.shape[0]) == n, "k_new / v_new must have q's tokens")
-    bs = int(tree_indptr.numel()) - 1
-    words = 0 if mask is None else int(mask.shape[-1])
+    n, hq, d = shape
+    _need(d == cache.head_dim and (n == 0 or qs[2] == 1 and os_[2] == 1), "q and out must have the cache's head_dim, dense")
+    ks = _new_rows(cache, k_new, v_new, (n,))
+    bs = tree_indptr.numel() - 1
+    words = 0 if mask is None else mask.shape[-1]
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need_i32("mask", mask, n, words)
     _need_i32("seq_slots", seq_slots, bs)
@@ -586,11 +597,13 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         _need(lse.is_contiguous(), "lse must be contiguous")
     if workspace is None:
         workspace = torch.empty(csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
-    _check(lib().csgmv_tree_attention(
-        _at(q), int(q.stride(0)), int(q.stride(1)), hq, _at(k_new), _at(v_new), int(k_new.stride(0)),
-        int(k_new.stride(1)), cache._ref, int(layer), _at(tree_indptr), _at(seq_slots), bs, n, _at(mask), words,
-        float(d ** -0.5 if scale is None else scale), _at(out), int(out.stride(0)), int(out.stride(1)), _at(lse),
-        _at(workspace), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+    rc = lib().csgmv_tree_attention(
+        q.data_ptr(), qs[0], qs[1], hq, k_new.data_ptr(), v_new.data_ptr(), ks[0], ks[1], cache._ref, layer,
+        tree_indptr.data_ptr(), _at(seq_slots), bs, n, _at(mask), words, d ** -0.5 if scale is None else scale,
+        out.data_ptr(), os_[0], os_[1], _at(lse), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, cache.device))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -607,6 +620,8 @@ class DraftTree:
         self.first_child = torch.full((max_nodes,), -1, **i32)
         self.next_sibling = torch.full((max_nodes,), -1, **i32)
         self.status = torch.zeros(1, **i32)
+        self.max_nodes, self.device = int(max_nodes), self.status.get_device()
+        self._at = tuple(t.data_ptr() for t in (self.mask, self.depth, self.first_child, self.next_sibling, self.status))
 
     def device_status(self) -> int:
         return int(self.status.item())
@@ -615,13 +630,12 @@ class DraftTree:
 def csgmv_build_draft_tree(tree: DraftTree, parents: torch.Tensor, tree_indptr: torch.Tensor, stream=None) -> None:
     """Fills tree.mask, depth, first_child and next_sibling from the nodes'
     parents (numbers inside their request, -1 at its node 0)."""
-    n, bs = int(parents.numel()), int(tree_indptr.numel()) - 1
+    n, bs = parents.numel(), tree_indptr.numel() - 1
     _need_i32("parents", parents, n)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
-    _need(n <= int(tree.depth.numel()), f"{n} nodes exceed the tree's {tree.depth.numel()}")
-    _check(lib().csgmv_build_draft_tree(_at(parents), _at(tree_indptr), bs, n, tree.words, _at(tree.mask),
-                                        _at(tree.depth), _at(tree.first_child), _at(tree.next_sibling),
-                                        _at(tree.status), _raw_stream(stream)))
+    _need(n <= tree.max_nodes, f"{n} nodes exceed the tree's {tree.max_nodes}")
+    _check(lib().csgmv_build_draft_tree(parents.data_ptr(), tree_indptr.data_ptr(), bs, n, tree.words, *tree._at,
+                                        _raw_stream(stream, tree.device)))
 
 
 def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, tree_indptr: torch.Tensor,
@@ -631,35 +645,37 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
     """Walks each tree: (accept_index (bs, width), accept_len (bs,), next_token
     (bs,)), allocated unless given; width defaults to tree.max_draft.
     draft_probs None: the drafts were chosen, not sampled."""
-    n, bs = int(draft_tokens.numel()), int(tree_indptr.numel()) - 1
+    n, bs = draft_tokens.numel(), tree_indptr.numel() - 1
     _need_f32("target_probs", target_probs, n, None)
-    _need(n == 0 or target_probs.stride(1) == 1, "target_probs must have dense rows")
-    vocab = int(target_probs.shape[1])
+    ts, vocab = target_probs.stride(), target_probs.shape[1]
+    _need(n == 0 or ts[1] == 1, "target_probs must have dense rows")
+    # the row stride of a single row says nothing
+    ts, ds = ts[0] if n > 1 else vocab, 0
     if draft_probs is not None:
         _need_f32("draft_probs", draft_probs, n, vocab)
-        _need(n == 0 or draft_probs.stride(1) == 1, "draft_probs must have dense rows")
+        ds = draft_probs.stride()
+        _need(n == 0 or ds[1] == 1, "draft_probs must have dense rows")
+        ds = ds[0] if n > 1 else vocab
     _need_i32("draft_tokens", draft_tokens, n)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need_f32("accept_uniforms", accept_uniforms, n)
     _need_f32("sample_uniforms", sample_uniforms, bs)
     _need(accept_uniforms.is_contiguous() and sample_uniforms.is_contiguous(), "the uniform numbers must be contiguous")
-    _need(n <= int(tree.depth.numel()), f"{n} nodes exceed the tree's {tree.depth.numel()}")
-    dev = target_probs.device
-    if accept_index is None:
-        accept_index = torch.empty((bs, tree.max_draft), dtype=torch.int32, device=dev)
-    if accept_len is None:
-        accept_len = torch.empty(bs, dtype=torch.int32, device=dev)
-    if next_token is None:
-        next_token = torch.empty(bs, dtype=torch.int32, device=dev)
-    _need_i32("accept_index", accept_index, bs, None)
+    _need(n <= tree.max_nodes, f"{n} nodes exceed the tree's {tree.max_nodes}")
+    # one buffer for the outputs that are not given
+    width = tree.max_draft if accept_index is None else accept_index.shape[-1]
+    if accept_index is None or accept_len is None or next_token is None:
+        made = torch.empty((width + 2, bs), dtype=torch.int32, device=target_probs.device)
+        accept_index = made[:width].view(bs, width) if accept_index is None else accept_index
+        accept_len = made[width] if accept_len is None else accept_len
+        next_token = made[width + 1] if next_token is None else next_token
+    _need_i32("accept_index", accept_index, bs, width)
     _need_i32("accept_len", accept_len, bs)
     _need_i32("next_token", next_token, bs)
-    # the row stride of a single row says nothing
-    ts = int(target_probs.stride(0)) if n > 1 else vocab
-    ds = 0 if draft_probs is None else int(draft_probs.stride(0)) if n > 1 else vocab
-    _check(lib().csgmv_verify_drafts(
-        _at(target_probs), ts, _at(draft_probs), ds, _at(draft_tokens), _at(tree_indptr),
-        _at(tree.first_child), _at(tree.next_sibling), _at(accept_uniforms), _at(sample_uniforms), bs, n, vocab,
-        _at(accept_index), int(accept_index.shape[1]), _at(accept_len), _at(next_token), _at(tree.status),
-        _raw_stream(stream)))
+    rc = lib().csgmv_verify_drafts(
+        target_probs.data_ptr(), ts, _at(draft_probs), ds, draft_tokens.data_ptr(), tree_indptr.data_ptr(), tree._at[2],
+        tree._at[3], accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), bs, n, vocab, accept_index.data_ptr(), width,
+        accept_len.data_ptr(), next_token.data_ptr(), tree._at[4], _raw_stream(stream, tree.device))
+    if rc:
+        _check(rc)
     return accept_index, accept_len, next_token
