@@ -1,5 +1,9 @@
 // Draft trees: derived fields (masks, depths, child lists) and the
 // verification walk.  See include/csgmv.h for the definitions.
+#include <mutex>
+#include <set>
+#include <type_traits>
+
 #include "serving.cuh"
 
 namespace csgmv {
@@ -71,16 +75,30 @@ constexpr int kVerWarps = kVerThreads / 32;
 __device__ __forceinline__ long long fixed44(float x) {
     return __float2ll_rz(fminf(fmaxf(x, 0.0f), 1.0f) * 17592186044416.0f);
 }
+// The same steps as a high and a low number of 22 bits each: both products and
+// the difference are exact, and sums over a thread's tokens fit 32 bits.
+struct Steps {
+    uint32_t hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float a = fminf(fmaxf(x, 0.0f), 1.0f) * 4194304.0f;
+        const uint32_t h = __float2uint_rz(a);
+        hi += h;
+        lo += __float2uint_rz((a - __uint2float_rn(h)) * 4194304.0f);
+    }
+    __device__ __forceinline__ long long total() const { return ((long long)hi << 22) + lo; }
+};
 // One refusal: r = max(r - z q, 0), each operation rounded.
 __device__ __forceinline__ float refuse(float r, float z, float q) {
     return fmaxf(__fsub_rn(r, __fmul_rn(z, q)), 0.0f);
 }
 
+enum { kRowPlain = 0, kRowRefuse = 1, kRowAgain = 2 };
+
 struct VerSmem {
     int first[kMaxNodes], next[kMaxNodes], parent[kMaxNodes], token[kMaxNodes];
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes], z[kMaxNodes];
-    long long warp[kVerWarps], total, scratch;
-    int path;
+    long long warp[kVerWarps], total;
+    int mine[kMaxNodes], nmine;  // children's tokens in this CTA's part
 };
 
 // A cluster a request; CTA `rank` owns tokens [rank * per, (rank + 1) * per)
@@ -90,15 +108,17 @@ struct VerSmem {
 // distribution.  Rows are read where the sum of what is left matters: after a
 // refusal with another sibling to try, and for the last token.  `r` in shared
 // memory holds the CTA's part of what is left.  Sums are whole numbers, so the
-// reductions' order does not show.
-__global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) verify(VerifyParams v, int per) {
-    extern __shared__ float r[];
+// reductions' order does not show.  What bounds a batch is the rows' bytes; a
+// thread keeps four (eight with a draft) 16-byte loads in flight.
+__global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) verify(VerifyParams v, int per, int vec) {
+    extern __shared__ __align__(16) float r[];
     __shared__ VerSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank();
     const int b = blockIdx.x / kVerCtas;
     const int lo = v.indptr[b], hi = v.indptr[b + 1];
     const int V = v.vocab;
     int n = hi - lo;
+    if (tid == 0) sm.nmine = 0;
     const bool sound = lo >= 0 && hi >= lo && hi <= v.num_nodes && n <= kMaxNodes;
     if (!sound || n == 0) {  // the same in every CTA of the cluster
         if (rank == 0) {
@@ -140,17 +160,59 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
     const int v0 = min(V, rank * per), v1 = min(V, v0 + per);
     const int perw = ((per + kVerWarps - 1) / kVerWarps + 127) & ~127;
     const int w0 = min(v1, v0 + warp * perw), w1 = min(v1, w0 + perw);
-    // Sum over the vocabulary of what f leaves at each token; r is updated.
-    // sm.total: the CTA's part, sm.warp: the running sum ahead of each warp.
-    auto pass = [&](auto f) -> long long {
-        long long s = 0;
-        for (int i = w0 + lane; i < w1; i += 32) {
-            const float x = f(i);
-            r[i - v0] = x;
-            s += fixed44(x);
+    // What a row leaves in r, and its sum over the vocabulary: the row itself,
+    // one refusal of it, or another refusal of what r holds.  sm.total: the
+    // CTA's part, sm.warp: the running sum ahead of each warp.
+    auto pass = [&](auto kind_tag, const float *p, const float *q, float z) -> long long {
+        constexpr int kind = decltype(kind_tag)::value;
+        Steps s = {0, 0};
+        auto one = [&](float x, float y) { return kind == kRowPlain ? x : refuse(x, z, y); };
+        int i0 = w0;
+        if (vec) {
+            constexpr int U = 4;
+            for (; i0 + U * 128 <= w1; i0 += U * 128) {
+                float4 a[U], b[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * 128 + lane * 4;
+                    a[u] = kind == kRowAgain ? *reinterpret_cast<const float4 *>(r + i - v0)
+                                             : __ldg(reinterpret_cast<const float4 *>(p + i));
+                    if (kind != kRowPlain) b[u] = __ldg(reinterpret_cast<const float4 *>(q + i));
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * 128 + lane * 4;
+                    float4 x = a[u];
+                    if (kind != kRowPlain)
+                        x = make_float4(one(a[u].x, b[u].x), one(a[u].y, b[u].y), one(a[u].z, b[u].z), one(a[u].w, b[u].w));
+                    *reinterpret_cast<float4 *>(r + i - v0) = x;
+                    s.add(x.x);
+                    s.add(x.y);
+                    s.add(x.z);
+                    s.add(x.w);
+                }
+            }
         }
-        s = warp_sum(s);
-        if (lane == 0) sm.warp[warp] = s;
+        for (int i = i0 + lane; i < w1; i += 32) {
+            const float x = one(kind == kRowAgain ? r[i - v0] : __ldg(p + i), kind == kRowPlain ? 0.0f : __ldg(q + i));
+            r[i - v0] = x;
+            s.add(x);
+        }
+        // (a lane reads and writes its own part of r only, so another pass may follow)
+        long long t = warp_sum(s.total());
+        if (kind == kRowPlain) {  // the children's tokens are taken out
+            __syncwarp();
+            for (int c = 0; c < sm.nmine; ++c) {
+                const int i = sm.mine[c];
+                if (i >= w0 && i < w1) {
+                    t -= fixed44(r[i - v0]);
+                    __syncwarp();
+                    if (lane == 0) r[i - v0] = 0.0f;
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) sm.warp[warp] = t;
         __syncthreads();
         if (warp == 0) {
             const long long w = lane < kVerWarps ? sm.warp[lane] : 0, inc = warp_scan(w);
@@ -159,9 +221,12 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
         }
         __syncthreads();
         cluster_sync();
-        const long long t = lane < kVerCtas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
-        return warp_sum(t);
+        const long long c = lane < kVerCtas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
+        return warp_sum(c);
     };
+    using Plain = std::integral_constant<int, kRowPlain>;
+    using Refuse = std::integral_constant<int, kRowRefuse>;
+    using Again = std::integral_constant<int, kRowAgain>;
     // The walk, the same in every thread of the cluster.
     int cur = 0, count = 1;
     int32_t *path = v.accept_index + (int64_t)b * v.width;
@@ -186,9 +251,8 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
                 }
                 if (tid == 0) sm.z[refused] = z;
                 ++refused;
-                const float zz = z;
-                if (refused == 1) total = pass([&](int i) { return refuse(p[i], zz, q[i]); });
-                else total = pass([&](int i) { return refuse(r[i - v0], zz, q[i]); });
+                if (refused == 1) total = pass(Refuse{}, p, q, z);
+                else total = pass(Again{}, p, q, z);
                 cluster_sync();  // the other CTAs have read sm.total
                 have_r = true;
                 z = __fmul_rn(__ll2float_rn(total), 1.0f / 17592186044416.0f);
@@ -208,21 +272,28 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
             }
         }
         if (hit < 0) {
-            auto plain = [&](int i) { return p[i]; };
             if (!have_r) {
-                if (!q && sm.first[cur] >= 0) {
-                    total = pass([&](int i) {
-                        bool kid = false;
-                        for (int k = sm.first[cur]; k >= 0; k = sm.next[k]) kid |= sm.token[k] == i;
-                        return kid ? 0.0f : p[i];
-                    });
-                } else {
-                    total = pass(plain);
+                if (!q) {
+                    // the children's distinct tokens in this CTA's part
+                    if (tid == 0) {
+                        int n = 0;
+                        for (int k = sm.first[cur]; k >= 0; k = sm.next[k]) {
+                            const int t = sm.token[k];
+                            bool seen = t < v0 || t >= v1;
+                            for (int e = 0; e < n; ++e) seen |= sm.mine[e] == t;
+                            if (!seen) sm.mine[n++] = t;
+                        }
+                        sm.nmine = n;
+                    }
+                    __syncthreads();
                 }
+                total = pass(Plain{}, p, q, 0.0f);
             }
-            if (total == 0) {
+            if (total == 0) {  // nothing is left: the distribution itself
                 cluster_sync();
-                total = pass(plain);
+                if (tid == 0) sm.nmine = 0;
+                __syncthreads();
+                total = pass(Plain{}, p, q, 0.0f);
             }
             break;
         }
@@ -258,13 +329,24 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
     const long long end = warp + 1 < kVerWarps ? before + sm.warp[warp + 1] : before + mine;
     if (aim < ahead || aim >= end) return;
     long long run = ahead;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const long long x = i < w1 ? fixed44(r[i - v0]) : 0ll;
-        const long long inc = run + warp_scan(x);
+    // 128 tokens at a time, four a lane
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        long long x[4], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + lane * 4 + e;
+            x[e] = i < w1 ? fixed44(r[i - v0]) : 0ll;
+            sum += x[e];
+        }
+        const long long inc = run + warp_scan(sum);
         const unsigned above = __ballot_sync(kFullMask, inc > aim);
         if (above) {
-            if (lane == __ffs(above) - 1) v.next_token[b] = i;
+            if (lane == __ffs(above) - 1) {
+                long long at = inc - sum;
+                int e = 0;
+                while (e < 3 && at + x[e] <= aim) at += x[e++];
+                v.next_token[b] = i0 + lane * 4 + e;
+            }
             return;
         }
         run = __shfl_sync(kFullMask, inc, 31);
@@ -280,9 +362,22 @@ cudaError_t launch_build_tree(const TreeParams &p, cudaStream_t stream) {
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
     const int per = ((p.vocab + kVerCtas - 1) / kVerCtas + 127) & ~127;
     const size_t smem = (size_t)per * sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(verify, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::mutex mu;
+    static std::set<int> ready;  // devices
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return launch_kernel(verify, dim3((unsigned)p.bs * kVerCtas), kVerThreads, smem, stream, 0, false, p, per);
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!ready.count(dev)) {
+            e = cudaFuncSetAttribute(verify, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * ((1 << 18) / kVerCtas + 128));
+            if (e != cudaSuccess) return e;
+            ready.insert(dev);
+        }
+    }
+    auto rows16 = [](const float *q, int64_t stride) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && stride % 4 == 0; };
+    const int vec = rows16(p.target, p.target_stride) && (!p.draft || rows16(p.draft, p.draft_stride));
+    return launch_kernel(verify, dim3((unsigned)p.bs * kVerCtas), kVerThreads, smem, stream, 0, false, p, per, vec);
 }
 
 }  // namespace csgmv
