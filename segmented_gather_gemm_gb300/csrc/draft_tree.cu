@@ -1,9 +1,5 @@
 // Draft trees: derived fields (masks, depths, child lists) and the
 // verification walk.  See include/csgmv.h for the definitions.
-#include <mutex>
-#include <set>
-#include <type_traits>
-
 #include "serving.cuh"
 
 namespace csgmv {
@@ -22,6 +18,7 @@ __global__ void __launch_bounds__(kTreeThreads) build_tree(TreeParams p) {
     __shared__ int par[kMaxNodes];
     __shared__ uint32_t bits[kMaxNodes * kTreeMaxWords];
     __shared__ int bad_s;
+    griddep_launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x;
     const int lo = p.indptr[b], hi = p.indptr[b + 1];
     if (lo < 0 || hi < lo || hi > p.num_nodes) {
@@ -67,7 +64,7 @@ __global__ void __launch_bounds__(kTreeThreads) build_tree(TreeParams p) {
 }
 
 // -------------------------------------------------------------- verification
-constexpr int kVerCtas = 8;       // CTAs of the cluster that walks one tree
+constexpr int kVerMaxCtas = 8;    // CTAs of the cluster that walks one tree, at most
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 
@@ -92,13 +89,11 @@ __device__ __forceinline__ float refuse(float r, float z, float q) {
     return fmaxf(__fsub_rn(r, __fmul_rn(z, q)), 0.0f);
 }
 
-enum { kRowPlain = 0, kRowRefuse = 1, kRowAgain = 2 };
-
 struct VerSmem {
     int first[kMaxNodes], next[kMaxNodes], parent[kMaxNodes], token[kMaxNodes];
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes], z[kMaxNodes];
-    long long warp[kVerWarps], total;
-    int mine[kMaxNodes], nmine;  // children's tokens in this CTA's part
+    long long warp[kVerWarps], chunk[kVerWarps], total;
+    int gone[kMaxNodes], ngone;  // children's distinct tokens in this CTA's part, taken out
 };
 
 // A cluster a request; CTA `rank` owns tokens [rank * per, (rank + 1) * per)
@@ -106,19 +101,24 @@ struct VerSmem {
 // tree by itself from the drafted tokens' own probabilities, gathered at the
 // start in one round of loads, so an accepted draft costs no pass over a
 // distribution.  Rows are read where the sum of what is left matters: after a
-// refusal with another sibling to try, and for the last token.  `r` in shared
-// memory holds the CTA's part of what is left.  Sums are whole numbers, so the
-// reductions' order does not show.  What bounds a batch is the rows' bytes; a
-// thread keeps four (eight with a draft) 16-byte loads in flight.
-__global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) verify(VerifyParams v, int per, int vec) {
-    extern __shared__ __align__(16) float r[];
+// refusal with another sibling to try, and for the last token.  What is left
+// is a function of the row, the draft's row and the z of each refusal, so it
+// is worked out again where it is needed and nothing is kept.  Sums are whole
+// numbers, so the reductions' order does not show.
+//
+// What bounds a batch is the rows' bytes, so there have to be enough loads in
+// flight: a thread keeps four 16-byte loads, and a cluster is as large as
+// leaves the batch two CTAs an SM (launch_verify).
+__global__ void __launch_bounds__(kVerThreads, 2) verify(VerifyParams v, int per, int vec) {
     __shared__ VerSmem sm;
+    const int ctas = (int)cluster_size();
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank();
-    const int b = blockIdx.x / kVerCtas;
+    const int b = blockIdx.x / ctas;
     const int lo = v.indptr[b], hi = v.indptr[b + 1];
     const int V = v.vocab;
     int n = hi - lo;
-    if (tid == 0) sm.nmine = 0;
+    if (tid == 0) sm.ngone = 0;
     const bool sound = lo >= 0 && hi >= lo && hi <= v.num_nodes && n <= kMaxNodes;
     if (!sound || n == 0) {  // the same in every CTA of the cluster
         if (rank == 0) {
@@ -160,57 +160,51 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
     const int v0 = min(V, rank * per), v1 = min(V, v0 + per);
     const int perw = ((per + kVerWarps - 1) / kVerWarps + 127) & ~127;
     const int w0 = min(v1, v0 + warp * perw), w1 = min(v1, w0 + perw);
-    // What a row leaves in r, and its sum over the vocabulary: the row itself,
-    // one refusal of it, or another refusal of what r holds.  sm.total: the
-    // CTA's part, sm.warp: the running sum ahead of each warp.
-    auto pass = [&](auto kind_tag, const float *p, const float *q, float z) -> long long {
-        constexpr int kind = decltype(kind_tag)::value;
+    // Four tokens from i on (0 from `end` on); 16 bytes at once where the rows allow it.
+    auto load4 = [&](const float *row, int i, int end) {
+        if (vec && i + 4 <= end) return __ldg(reinterpret_cast<const float4 *>(row + i));
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < end) x.x = __ldg(row + i);
+        if (i + 1 < end) x.y = __ldg(row + i + 1);
+        if (i + 2 < end) x.z = __ldg(row + i + 2);
+        if (i + 3 < end) x.w = __ldg(row + i + 3);
+        return x;
+    };
+    // What is left of them after n refusals.
+    auto left4 = [&](float4 x, float4 y, int n) {
+#pragma unroll 1
+        for (int m = 0; m < n; ++m) {
+            const float z = sm.z[m];
+            x = make_float4(refuse(x.x, z, y.x), refuse(x.y, z, y.y), refuse(x.z, z, y.z), refuse(x.w, z, y.w));
+        }
+        return x;
+    };
+    // The sum over the vocabulary of what is left of a row after n refusals.
+    // sm.total: the CTA's part, sm.warp: the running sum ahead of each warp.
+    auto pass = [&](const float *p, const float *q, int n) -> long long {
         Steps s = {0, 0};
-        auto one = [&](float x, float y) { return kind == kRowPlain ? x : refuse(x, z, y); };
-        int i0 = w0;
-        if (vec) {
-            constexpr int U = 4;
-            for (; i0 + U * 128 <= w1; i0 += U * 128) {
-                float4 a[U], b[U];
+        constexpr int kFar = 4;  // stretches of 128 tokens in flight
+        for (int i0 = w0 + lane * 4; i0 - lane * 4 < w1; i0 += kFar * 128) {
+            float4 x[kFar], y[kFar];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * 128 + lane * 4;
-                    a[u] = kind == kRowAgain ? *reinterpret_cast<const float4 *>(r + i - v0)
-                                             : __ldg(reinterpret_cast<const float4 *>(p + i));
-                    if (kind != kRowPlain) b[u] = __ldg(reinterpret_cast<const float4 *>(q + i));
-                }
+            for (int u = 0; u < kFar; ++u) {
+                x[u] = load4(p, i0 + u * 128, w1);
+                y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (n) y[u] = load4(q, i0 + u * 128, w1);
+            }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * 128 + lane * 4;
-                    float4 x = a[u];
-                    if (kind != kRowPlain)
-                        x = make_float4(one(a[u].x, b[u].x), one(a[u].y, b[u].y), one(a[u].z, b[u].z), one(a[u].w, b[u].w));
-                    *reinterpret_cast<float4 *>(r + i - v0) = x;
-                    s.add(x.x);
-                    s.add(x.y);
-                    s.add(x.z);
-                    s.add(x.w);
-                }
+            for (int u = 0; u < kFar; ++u) {
+                const float4 r = left4(x[u], y[u], n);
+                s.add(r.x);
+                s.add(r.y);
+                s.add(r.z);
+                s.add(r.w);
             }
         }
-        for (int i = i0 + lane; i < w1; i += 32) {
-            const float x = one(kind == kRowAgain ? r[i - v0] : __ldg(p + i), kind == kRowPlain ? 0.0f : __ldg(q + i));
-            r[i - v0] = x;
-            s.add(x);
-        }
-        // (a lane reads and writes its own part of r only, so another pass may follow)
         long long t = warp_sum(s.total());
-        if (kind == kRowPlain) {  // the children's tokens are taken out
-            __syncwarp();
-            for (int c = 0; c < sm.nmine; ++c) {
-                const int i = sm.mine[c];
-                if (i >= w0 && i < w1) {
-                    t -= fixed44(r[i - v0]);
-                    __syncwarp();
-                    if (lane == 0) r[i - v0] = 0.0f;
-                    __syncwarp();
-                }
-            }
+        for (int c = 0; c < sm.ngone; ++c) {
+            const int i = sm.gone[c];
+            if (i >= w0 && i < w1) t -= fixed44(__ldg(p + i));
         }
         if (lane == 0) sm.warp[warp] = t;
         __syncthreads();
@@ -221,26 +215,22 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
         }
         __syncthreads();
         cluster_sync();
-        const long long c = lane < kVerCtas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
+        const long long c = lane < ctas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
         return warp_sum(c);
     };
-    using Plain = std::integral_constant<int, kRowPlain>;
-    using Refuse = std::integral_constant<int, kRowRefuse>;
-    using Again = std::integral_constant<int, kRowAgain>;
     // The walk, the same in every thread of the cluster.
     int cur = 0, count = 1;
     int32_t *path = v.accept_index + (int64_t)b * v.width;
     if (rank == 0 && tid == 0) path[0] = 0;
-    bool have_r = false;
+    int refused = 0;
     long long total = 0;
     while (true) {
         const float *p = v.target + (int64_t)(lo + cur) * v.target_stride;
         const float *q = v.draft ? v.draft + (int64_t)(lo + cur) * v.draft_stride : nullptr;
         int hit = -1;
-        have_r = false;
+        refused = 0;
         if (q) {
             float z = 1.0f;
-            int refused = 0;
             for (int k = sm.first[cur]; k >= 0 && z > 0.0f; k = sm.next[k]) {
                 if (sm.token[k] < 0) continue;
                 float rk = sm.p[k];
@@ -249,12 +239,13 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
                     hit = k;
                     break;
                 }
+                // (sm.z[0] is always 1, and a later one is written behind a pass's barriers, so
+                // no thread still reads the node before's)
                 if (tid == 0) sm.z[refused] = z;
                 ++refused;
-                if (refused == 1) total = pass(Refuse{}, p, q, z);
-                else total = pass(Again{}, p, q, z);
+                __syncthreads();
+                total = pass(p, q, refused);
                 cluster_sync();  // the other CTAs have read sm.total
-                have_r = true;
                 z = __fmul_rn(__ll2float_rn(total), 1.0f / 17592186044416.0f);
             }
         } else {
@@ -272,28 +263,28 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
             }
         }
         if (hit < 0) {
-            if (!have_r) {
+            if (refused == 0) {
                 if (!q) {
-                    // the children's distinct tokens in this CTA's part
                     if (tid == 0) {
                         int n = 0;
                         for (int k = sm.first[cur]; k >= 0; k = sm.next[k]) {
                             const int t = sm.token[k];
                             bool seen = t < v0 || t >= v1;
-                            for (int e = 0; e < n; ++e) seen |= sm.mine[e] == t;
-                            if (!seen) sm.mine[n++] = t;
+                            for (int e = 0; e < n; ++e) seen |= sm.gone[e] == t;
+                            if (!seen) sm.gone[n++] = t;
                         }
-                        sm.nmine = n;
+                        sm.ngone = n;
                     }
                     __syncthreads();
                 }
-                total = pass(Plain{}, p, q, 0.0f);
+                total = pass(p, q, 0);
             }
             if (total == 0) {  // nothing is left: the distribution itself
                 cluster_sync();
-                if (tid == 0) sm.nmine = 0;
+                if (tid == 0) sm.ngone = 0;
                 __syncthreads();
-                total = pass(Plain{}, p, q, 0.0f);
+                refused = 0;
+                total = pass(p, q, 0);
             }
             break;
         }
@@ -320,36 +311,56 @@ __global__ void __cluster_dims__(kVerCtas, 1, 1) __launch_bounds__(kVerThreads) 
     // first above aim.
     const long long U = (long long)(fminf(fmaxf(v.sample_u[b], 0.0f), 0.99999994f) * 2147483648.0f);
     const long long aim = U * (total >> 31) + ((U * (total & 0x7fffffffll)) >> 31);
-    const long long t = lane < kVerCtas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
+    const long long t = lane < ctas ? dsmem_ld_i64(dsmem_addr(&sm.total, lane)) : 0;
     const long long before = warp_sum(lane < rank ? t : 0ll);
     const long long mine = __shfl_sync(kFullMask, t, rank);
     cluster_sync();  // no CTA leaves while another reads its shared memory
     if (!fits || total == 0 || aim < before || aim >= before + mine) return;
-    const long long ahead = before + sm.warp[warp];
-    const long long end = warp + 1 < kVerWarps ? before + sm.warp[warp + 1] : before + mine;
-    if (aim < ahead || aim >= end) return;
-    long long run = ahead;
-    // 128 tokens at a time, four a lane
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        long long x[4], sum = 0;
+    // its warp's stretch, dealt out to all threads of the CTA
+    int owner = 0;
+    for (int w = 1; w < kVerWarps; ++w)
+        if (before + sm.warp[w] <= aim) owner = w;  // the last: the warps after it that hold nothing start beyond aim
+    const long long ahead = before + sm.warp[owner];
+    const int o0 = min(v1, v0 + owner * perw), o1 = min(v1, o0 + perw);
+    const int each = ((o1 - o0 + kVerThreads - 1) / kVerThreads + 3) & ~3;
+    const int s0 = min(o1, o0 + tid * each), s1 = min(o1, s0 + each);
+    const float *p = v.target + (int64_t)(lo + cur) * v.target_stride;
+    const float *q = v.draft ? v.draft + (int64_t)(lo + cur) * v.draft_stride : nullptr;
+    // Steps of the four tokens from i on.
+    auto steps4 = [&](int i, long long (&n)[4]) {
+        const float4 x = load4(p, i, s1);
+        const float4 r = refused ? left4(x, load4(q, i, s1), refused) : x;
+        n[0] = fixed44(r.x);
+        n[1] = fixed44(r.y);
+        n[2] = fixed44(r.z);
+        n[3] = fixed44(r.w);
+        for (int c = 0; c < sm.ngone; ++c) {
+            const int at = sm.gone[c] - i;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + lane * 4 + e;
-            x[e] = i < w1 ? fixed44(r[i - v0]) : 0ll;
-            sum += x[e];
+            for (int k = 0; k < 4; ++k) n[k] = at == k ? 0 : n[k];
         }
-        const long long inc = run + warp_scan(sum);
-        const unsigned above = __ballot_sync(kFullMask, inc > aim);
-        if (above) {
-            if (lane == __ffs(above) - 1) {
-                long long at = inc - sum;
-                int e = 0;
-                while (e < 3 && at + x[e] <= aim) at += x[e++];
-                v.next_token[b] = i0 + lane * 4 + e;
-            }
-            return;
+    };
+    long long sum = 0, x[4];
+#pragma unroll 2
+    for (int i = s0; i < s1; i += 4) {
+        steps4(i, x);
+        sum += (x[0] + x[1]) + (x[2] + x[3]);
+    }
+    long long inc = warp_scan(sum);
+    if (lane == 31) sm.chunk[warp] = inc;
+    __syncthreads();
+    inc += ahead;
+    for (int w = 0; w < warp; ++w) inc += sm.chunk[w];
+    if (aim < inc - sum || aim >= inc) return;
+    long long run = inc - sum;
+#pragma unroll 1
+    for (int i = s0; i < s1; i += 4) {
+        steps4(i, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (aim >= run && aim < run + x[k]) v.next_token[b] = i + k;
+            run += x[k];
         }
-        run = __shfl_sync(kFullMask, inc, 31);
     }
 }
 
@@ -360,24 +371,14 @@ cudaError_t launch_build_tree(const TreeParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
-    const int per = ((p.vocab + kVerCtas - 1) / kVerCtas + 127) & ~127;
-    const size_t smem = (size_t)per * sizeof(float);
-    static std::mutex mu;
-    static std::set<int> ready;  // devices
-    int dev;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!ready.count(dev)) {
-            e = cudaFuncSetAttribute(verify, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * ((1 << 18) / kVerCtas + 128));
-            if (e != cudaSuccess) return e;
-            ready.insert(dev);
-        }
-    }
+    // CTAs a request: as many as leave the batch at most two an SM (all at once), fewer
+    // where a part of the vocabulary would be under 2048 tokens
+    int ctas = kVerMaxCtas;
+    while (ctas > 1 && ((int64_t)p.bs * ctas > 2 * 152 || p.vocab < 2048 * ctas)) ctas /= 2;
+    const int per = ((p.vocab + ctas - 1) / ctas + 127) & ~127;
     auto rows16 = [](const float *q, int64_t stride) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && stride % 4 == 0; };
     const int vec = rows16(p.target, p.target_stride) && (!p.draft || rows16(p.draft, p.draft_stride));
-    return launch_kernel(verify, dim3((unsigned)p.bs * kVerCtas), kVerThreads, smem, stream, 0, false, p, per, vec);
+    return launch_kernel(verify, dim3((unsigned)(p.bs * ctas)), kVerThreads, 0, stream, ctas, true, p, per, vec);
 }
 
 }  // namespace csgmv
