@@ -523,7 +523,7 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
     """Appends accept_len[b] of request b's rows of k_new / v_new (layers,
     tokens, kv_heads, head_dim) to its sequence: rows tree_indptr[b] +
     accept_index[b, j], or its first rows without an accept_index."""
-    st = _new_rows(cache, k_new, v_new, (cache.num_layers, None))
+    st = _new_rows(cache, k_new, v_new, (cache.num_layers, k_new.shape[1]))
     bs = accept_len.numel()
     width = 0 if accept_index is None else accept_index.shape[-1]
     _need_i32("accept_len", accept_len, bs)

@@ -16,7 +16,7 @@ constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveCtas = 152 * 8;
+constexpr int kMoveCtas = 152 * 16;
 
 // The cache as the kernels see it, with scratch cut into its arrays.
 struct Kv {
@@ -69,20 +69,21 @@ Kv view(const csgmv_kv_cache &c) {
 enum { kHRows = 0, kHMoves = 1, kHLive = 2 };  // entries of Kv::head
 
 // Copies ntok token slots of every head between two pages of one layer of one
-// pool (addresses of the pages' first elements).  `nt` threads, this one `ti`.
+// pool (addresses of the pages' first elements).  `nt` threads, this one `ti`,
+// U loads in flight each.
+template <int U>
 __device__ __forceinline__ void copy_page(const Kv &c, const uint16_t *src, uint16_t *dst, int ntok, int ti, int nt) {
     const unsigned cw = (unsigned)c.d >> 3;  // 16-byte chunks of a row
     const unsigned n = (unsigned)c.heads * ntok * cw;
-    constexpr int U = 8;
     for (unsigned i0 = ti; i0 < n; i0 += U * nt) {
         uint4 v[U];
-        int64_t off[U];
+        unsigned off[U];  // a page spans less than 2^31 elements
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const unsigned i = i0 + u * nt;
             if (i < n) {
                 const unsigned row = i / cw, h = row / (unsigned)ntok;
-                off[u] = h * c.head_stride + (int64_t)(row - h * ntok) * c.token_stride + (int64_t)(i - row * cw) * 8;
+                off[u] = h * (unsigned)c.head_stride + (row - h * ntok) * (unsigned)c.token_stride + (i - row * cw) * 8;
                 v[u] = ld_stream16(src + off[u]);
             }
         }
@@ -93,10 +94,8 @@ __device__ __forceinline__ void copy_page(const Kv &c, const uint16_t *src, uint
 }
 
 // --------------------------------------------------------------- free pages
-// Count of the pages for which `want` holds, by cluster: warp w of the
-// kPlanCtas * kPlanWarps warps owns a contiguous stretch of the pages.  Returns
-// the number before this warp's stretch and the total.  Ends with a cluster
-// barrier behind every read of the other CTAs' shared memory.
+// Counts of the pages for which something holds, by cluster: warp w of the
+// kPlanCtas * kPlanWarps warps owns a contiguous stretch of the pages.
 struct Stretch {
     int lo, hi;
 };
@@ -110,12 +109,14 @@ __device__ __forceinline__ Stretch stretch(int pages) {
 struct PlanSmem {
     int warp[33];
     int cta_total;
-    int a, b;
-    int scan[33];
+    int a;
+    long long scan[33];
 };
 
+// This CTA's part of the count (sm.warp: what is ahead of each warp in the CTA,
+// sm.cta_total).
 template <typename F>
-__device__ int count_pages(PlanSmem &sm, Stretch s, F want, int *total) {
+__device__ void count_mine(PlanSmem &sm, Stretch s, F want) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int mine = 0;
     for (int p = s.lo; p < s.hi; p += 32) mine += __popc(__ballot_sync(kFullMask, p + lane < s.hi && want(p + lane)));
@@ -127,15 +128,15 @@ __device__ int count_pages(PlanSmem &sm, Stretch s, F want, int *total) {
         if (lane == 31) sm.cta_total = inc;
     }
     __syncthreads();
-    cluster_sync();
-    int before = sm.warp[warp], all = 0;
-    const int rank = (int)cluster_rank();
+}
+// The pages counted ahead of this warp's stretch, and the total.  Behind a
+// cluster barrier that follows count_mine(); no CTA may leave before another
+// one.
+__device__ __forceinline__ int count_before(PlanSmem &sm, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)cluster_rank();
     const int t = lane < kPlanCtas ? dsmem_ld_i32(dsmem_addr(&sm.cta_total, lane)) : 0;
-    all = warp_sum(t);
-    before += warp_sum(lane < rank ? t : 0);
-    *total = all;
-    cluster_sync();
-    return before;
+    *total = warp_sum(t);
+    return sm.warp[warp] + warp_sum(lane < rank ? t : 0);
 }
 
 // Writes the `need` lowest free pages, in order, to list.  `before` counts the
@@ -157,111 +158,103 @@ __device__ __forceinline__ int pages_of(const Kv &c, int tokens) { return (token
 // Plan.  sa[b]: first appended row of request b in the batch's order (sa[bs]
 // the total), sb[b]: the sequence's length before, sc / sd[b]: source and
 // destination page of a copy on write, or -1; mark: the request that owns a
-// sequence slot; pb[b ..]: unused; pa: the pages given out.
+// sequence slot; pa: the pages given out.  A warp of the cluster a request: what
+// the plan takes is a chain of dependent loads, so it is kept as short as the
+// requests allow.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
 commit_plan(Kv c, CommitParams p) {
     __shared__ PlanSmem sm;
     griddep_launch_dependents();
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank();
+    const int gw = rank * kPlanWarps + warp, gt = rank * kPlanThreads + tid;
+    constexpr int kAllWarps = kPlanCtas * kPlanWarps, kAllThreads = kPlanCtas * kPlanThreads;
     const Stretch s = stretch(c.pages);
-    if (rank == 0) {
-        auto slot_of = [&](int b) { return p.seq_slots ? p.seq_slots[b] : b; };
-        for (int b = tid; b < p.bs; b += kPlanThreads) {
-            const int q = slot_of(b);
-            if (q >= 0 && q < c.seqs) c.mark[q] = INT32_MAX;
+    auto slot_of = [&](int b) { return p.seq_slots ? p.seq_slots[b] : b; };
+    auto in = [&](int q) { return q >= 0 && q < c.seqs; };
+    if (p.seq_slots) {  // (without slots none can come twice)
+        for (int b = gt; b < p.bs; b += kAllThreads)
+            if (in(slot_of(b))) c.mark[slot_of(b)] = INT32_MAX;
+        cluster_sync();
+        for (int b = gt; b < p.bs; b += kAllThreads)
+            if (in(slot_of(b))) atomicMin(&c.mark[slot_of(b)], b);
+        cluster_sync();
+    }
+    // is the request sound?  sa: its rows, sb: the length before, sd: pages it needs
+    for (int b = gw; b < p.bs; b += kAllWarps) {
+        const int q = slot_of(b), add = p.accept_len[b];
+        const int lo = p.tree_indptr[b], hi = p.tree_indptr[b + 1];
+        int bad = 0, old = 0;
+        bool wrong = false;
+        if (p.accept_index)  // read beside the rest: a bad count is cut to what is there
+            for (int j = lane; j < min(add, p.accept_width); j += 32) {
+                const int node = p.accept_index[(int64_t)b * p.accept_width + j];
+                wrong |= node < 0 || node >= hi - lo;
+            }
+        if (!in(q) || (p.seq_slots && c.mark[q] != b)) bad = CSGMV_KV_STATUS_BAD_SEQ;
+        if (!bad) {
+            old = c.lens[q];
+            if (add < 0 || lo < 0 || hi < lo || hi > p.num_tokens || old < 0 || old > c.max_pages * c.ps ||
+                (p.accept_index ? add > p.accept_width : add > hi - lo))
+                bad = CSGMV_KV_STATUS_BAD_LENS;
+            else if (add > c.max_pages * c.ps - old)
+                bad = CSGMV_KV_STATUS_CAPACITY;
         }
-        __syncthreads();
-        for (int b = tid; b < p.bs; b += kPlanThreads) {
-            const int q = slot_of(b);
-            if (q >= 0 && q < c.seqs) atomicMin(&c.mark[q], b);
+        if (__any_sync(kFullMask, wrong) && !bad) bad = CSGMV_KV_STATUS_BAD_TREE;
+        int cow = -1;
+        if (!bad && add > 0 && (old & (c.ps - 1))) {
+            const int last = c.table[(int64_t)q * c.max_pages + (old >> c.ps_shift)];
+            if (last < 0 || last >= c.pages) bad = CSGMV_KV_STATUS_BAD_PAGE;
+            else if (c.refs[last] > 1) cow = last;
         }
-        __syncthreads();
-        // a warp a request: is it sound?  sb = its length, or -1
-        for (int b = warp; b < p.bs; b += kPlanWarps) {
-            const int q = slot_of(b), add = p.accept_len[b];
-            const int lo = p.tree_indptr[b], hi = p.tree_indptr[b + 1];
-            int bad = 0, old = 0, add_ok = 0;
-            if (q < 0 || q >= c.seqs || c.mark[q] != b) bad = CSGMV_KV_STATUS_BAD_SEQ;
-            if (!bad) {
-                old = c.lens[q];
-                if (add < 0 || lo < 0 || hi < lo || hi > p.num_tokens || old < 0 || old > c.max_pages * c.ps ||
-                    (p.accept_index ? add > p.accept_width : add > hi - lo))
-                    bad = CSGMV_KV_STATUS_BAD_LENS;
-                else if (add > c.max_pages * c.ps - old)
-                    bad = CSGMV_KV_STATUS_CAPACITY;
-            }
-            if (!bad) {
-                bool wrong = false;
-                if (p.accept_index)
-                    for (int j = lane; j < add; j += 32) {
-                        const int node = p.accept_index[(int64_t)b * p.accept_width + j];
-                        wrong |= node < 0 || node >= hi - lo;
-                    }
-                if (__any_sync(kFullMask, wrong)) bad = CSGMV_KV_STATUS_BAD_TREE;
-            }
-            int cow = -1;
-            if (!bad && add > 0 && (old & (c.ps - 1))) {
-                const int last = c.table[(int64_t)q * c.max_pages + (old >> c.ps_shift)];
-                if (last < 0 || last >= c.pages) bad = CSGMV_KV_STATUS_BAD_PAGE;
-                else if (c.refs[last] > 1) cow = last;
-            }
-            add_ok = bad ? 0 : add;
-            if (lane == 0) {
-                if (bad) atomicOr(c.status, bad);
-                c.sa[b] = add_ok;
-                c.sb[b] = old;
-                c.sc[b] = cow;
-            }
+        if (lane == 0) {
+            if (bad) atomicOr(c.status, bad);
+            const int rows = bad ? 0 : add;
+            c.sa[b] = rows;
+            c.sb[b] = old;
+            c.sc[b] = rows ? cow : -1;
+            c.sd[b] = rows ? pages_of(c, old + rows) - pages_of(c, old) + (cow >= 0) : 0;
         }
-        __syncthreads();
-        // running sums of rows and of pages over the requests
-        int rows0 = 0, need0 = 0;
+    }
+    count_mine(sm, s, [&](int q) { return c.refs[q] == 0; });
+    cluster_sync();
+    if (rank == 0) {  // running sums of rows and of pages over the requests
+        long long sum = 0;
         for (int b0 = 0; b0 < p.bs; b0 += kPlanThreads) {
             const int b = b0 + tid;
-            int add = 0, need = 0;
-            if (b < p.bs && (add = c.sa[b]) > 0)
-                need = pages_of(c, c.sb[b] + add) - pages_of(c, c.sb[b]) + (c.sc[b] >= 0);
-            int rt, nt;
-            const int r = block_scan_ex(add, sm.scan, &rt), n = block_scan_ex(need, sm.scan, &nt);
+            long long t;
+            const long long own = b < p.bs ? (long long)c.sa[b] << 32 | (unsigned)c.sd[b] : 0;
+            const long long pre = sum + block_scan_ex(own, sm.scan, &t);
             if (b < p.bs) {
-                c.sa[b] = rows0 + r;
-                c.sd[b] = need0 + n;  // first entry of the page list; the copy's page below
+                c.sa[b] = (int)(pre >> 32);
+                c.sd[b] = (int)pre;  // first entry of the page list
             }
-            rows0 += rt;
-            need0 += nt;
+            sum += t;
         }
         if (tid == 0) {
-            c.sa[p.bs] = rows0;
-            sm.a = need0;
-            sm.b = rows0;
+            c.sa[p.bs] = (int)(sum >> 32);
+            sm.a = (int)sum;
         }
     }
     int nfree;
-    const int before = count_pages(sm, s, [&](int q) { return c.refs[q] == 0; }, &nfree);
+    const int before = count_before(sm, &nfree);
+    cluster_sync();
     const int need = dsmem_ld_i32(dsmem_addr(&sm.a, 0));
     const bool fits = need <= nfree;
     if (fits) list_free(c, s, before, need, c.pa);
     __threadfence();
     cluster_sync();
-    if (rank != 0) return;
-    if (!fits) {
-        if (tid == 0) {
-            atomicOr(c.status, CSGMV_KV_STATUS_CAPACITY);
-            c.head[kHRows] = 0;
-        }
-        return;
+    if (gt == 0) {
+        if (!fits) atomicOr(c.status, CSGMV_KV_STATUS_CAPACITY);
+        c.head[kHRows] = fits ? c.sa[p.bs] : 0;
     }
-    // hand the pages out, a warp a request
-    for (int b = warp; b < p.bs; b += kPlanWarps) {
-        const int add = c.sa[b + 1] - c.sa[b];
-        if (add == 0) {
-            if (lane == 0) c.sc[b] = -1;
-            continue;
-        }
-        const int q = p.seq_slots ? p.seq_slots[b] : b, old = c.sb[b];
-        int32_t *row = c.table + (int64_t)q * c.max_pages;
+    if (!fits) return;
+    // hand the pages out
+    for (int b = gw; b < p.bs; b += kAllWarps) {
+        const int add = c.sa[b + 1] - c.sa[b], q = slot_of(b), old = c.sb[b], cow = c.sc[b];
         int first = c.sd[b];
-        const int cow = c.sc[b];
+        if (add == 0) continue;
+        int32_t *row = c.table + (int64_t)q * c.max_pages;
         __syncwarp();
         if (cow >= 0) {
             if (lane == 0) {
@@ -281,12 +274,11 @@ commit_plan(Kv c, CommitParams p) {
         }
         if (lane == 0) c.lens[q] = old + add;
     }
-    if (tid == 0) c.head[kHRows] = sm.b;
 }
 
-// Move: a warp copies one appended row's K and V of one layer; then CTAs copy
+// Move: a warp copies an appended row's K and V of one layer; then CTAs copy
 // the pages that were shared.
-__global__ void __launch_bounds__(kMoveThreads) commit_move(Kv c, CommitParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) commit_move(Kv c, CommitParams p) {
     griddep_wait();
     const int rows = c.head[kHRows];
     if (rows == 0) return;
@@ -308,24 +300,22 @@ __global__ void __launch_bounds__(kMoveThreads) commit_move(Kv c, CommitParams p
         constexpr int U = 4;
         for (unsigned i0 = lane; i0 < n; i0 += U * 32) {
             uint4 vk[U], vv[U];
-            int64_t off[U];
 #pragma unroll
             for (int x = 0; x < U; ++x) {
-                const unsigned i = i0 + x * 32;
+                const unsigned i = i0 + x * 32, h = i / cw, e = (i - h * cw) * 8;
                 if (i < n) {
-                    const unsigned h = i / cw, e = (i - h * cw) * 8;
-                    const int64_t s = so + h * p.head_stride + e;
-                    off[x] = to + h * c.head_stride + e;
-                    vk[x] = ld_stream16(p.k_new + s);
-                    vv[x] = ld_stream16(p.v_new + s);
+                    vk[x] = ld_stream16(p.k_new + so + h * p.head_stride + e);
+                    vv[x] = ld_stream16(p.v_new + so + h * p.head_stride + e);
                 }
             }
 #pragma unroll
-            for (int x = 0; x < U; ++x)
-                if (i0 + x * 32 < n) {
-                    st_stream16(c.k + off[x], vk[x]);
-                    st_stream16(c.v + off[x], vv[x]);
+            for (int x = 0; x < U; ++x) {
+                const unsigned i = i0 + x * 32, h = i / cw, e = (i - h * cw) * 8;
+                if (i < n) {
+                    st_stream16(c.k + to + h * c.head_stride + e, vk[x]);
+                    st_stream16(c.v + to + h * c.head_stride + e, vv[x]);
                 }
+            }
         }
     }
     for (int b = blockIdx.x; b < p.bs; b += gridDim.x) {
@@ -334,8 +324,8 @@ __global__ void __launch_bounds__(kMoveThreads) commit_move(Kv c, CommitParams p
         const int to = c.sd[b], ntok = c.sb[b] & (c.ps - 1);
         for (int l = 0; l < c.layers; ++l) {
             const int64_t a = l * c.layer_stride + from * c.page_stride, z = l * c.layer_stride + to * c.page_stride;
-            copy_page(c, c.k + a, c.k + z, ntok, threadIdx.x, kMoveThreads);
-            copy_page(c, c.v + a, c.v + z, ntok, threadIdx.x, kMoveThreads);
+            copy_page<2>(c, c.k + a, c.k + z, ntok, threadIdx.x, kMoveThreads);
+            copy_page<2>(c, c.v + a, c.v + z, ntok, threadIdx.x, kMoveThreads);
         }
     }
 }
@@ -348,6 +338,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 fork_plan(Kv c, const int32_t *parents, const int32_t *children, int n) {
     __shared__ PlanSmem sm;
     griddep_launch_dependents();
+    griddep_wait();
     const int tid = threadIdx.x, rank = (int)cluster_rank();
     const Stretch s = stretch(c.pages);
     if (rank == 0) {
@@ -379,7 +370,7 @@ fork_plan(Kv c, const int32_t *parents, const int32_t *children, int n) {
             }
             const int part = len > 0 && (len & (c.ps - 1)) ? 1 : 0;
             int t;
-            const int at = block_scan_ex(part, sm.scan, &t);
+            const int at = block_scan_ex(part, reinterpret_cast<int *>(sm.scan), &t);
             if (i < n) {
                 c.sa[i] = len;
                 c.sb[i] = part ? need0 + at : -1;
@@ -388,9 +379,10 @@ fork_plan(Kv c, const int32_t *parents, const int32_t *children, int n) {
         }
         if (tid == 0) sm.a = need0;
     }
+    count_mine(sm, s, [&](int q) { return c.refs[q] == 0; });
+    cluster_sync();
     int nfree;
-    const int before = count_pages(sm, s, [&](int q) { return c.refs[q] == 0; }, &nfree);
-    const int need = dsmem_ld_i32(dsmem_addr(&sm.a, 0));
+    const int before = count_before(sm, &nfree), need = dsmem_ld_i32(dsmem_addr(&sm.a, 0));
     const bool fits = need <= nfree;
     if (fits) list_free(c, s, before, need, c.pa);
     __threadfence();
@@ -434,7 +426,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move(Kv c, const int32_t *p
     const int y = blockIdx.y - 1;
     uint16_t *pool = (y & 1) ? c.v : c.k;
     const int64_t l = (int64_t)(y >> 1) * c.layer_stride;
-    copy_page(c, pool + l + from[full] * c.page_stride, pool + l + fresh * c.page_stride, ntok, threadIdx.x,
+    copy_page<8>(c, pool + l + from[full] * c.page_stride, pool + l + fresh * c.page_stride, ntok, threadIdx.x,
               kMoveThreads);
 }
 
@@ -442,6 +434,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move(Kv c, const int32_t *p
 // A block a sequence.  A page is given up by whoever takes its table entry
 // (atomic exchange), so a sequence listed twice gives each page up once.
 __global__ void __launch_bounds__(kMoveThreads) free_pages(Kv c, const int32_t *seqs, const int32_t *keep_lens) {
+    griddep_wait();
     const int q = seqs[blockIdx.x], keep = keep_lens ? keep_lens[blockIdx.x] : 0;
     if (q < 0 || q >= c.seqs || keep < 0) {
         if (threadIdx.x == 0) atomicOr(c.status, keep < 0 ? CSGMV_KV_STATUS_BAD_LENS : CSGMV_KV_STATUS_BAD_SEQ);
@@ -479,10 +472,13 @@ __global__ void __launch_bounds__(kMoveThreads) free_pages(Kv c, const int32_t *
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) compact_plan(Kv c) {
     __shared__ PlanSmem sm;
     griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     const Stretch s = stretch(c.pages);
-    int live;
-    int before = count_pages(sm, s, [&](int q) { return c.refs[q] > 0; }, &live);
+    count_mine(sm, s, [&](int q) { return c.refs[q] > 0; });
+    cluster_sync();
+    int live, before = count_before(sm, &live);
+    cluster_arrive();
     for (int p = s.lo; p < s.hi; p += 32) {
         const int q = p + lane;
         const bool l = q < s.hi && c.refs[q] > 0;
@@ -503,6 +499,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         c.head[kHLive] = live;
         if (live == 0) c.head[kHMoves] = 0;
     }
+    cluster_wait();  // no CTA leaves while another reads its count
 }
 
 // Move: CTAs rewrite the sequences' rows of the page table, then copy pages,
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move(Kv c) {
         const int from = c.pb[moves - 1 - k], to = c.pa[k];
         uint16_t *pool = (y & 1) ? c.v : c.k;
         const int64_t l = (int64_t)(y >> 1) * c.layer_stride;
-        copy_page(c, pool + l + from * c.page_stride, pool + l + to * c.page_stride, c.ps, threadIdx.x, kMoveThreads);
+        copy_page<8>(c, pool + l + from * c.page_stride, pool + l + to * c.page_stride, c.ps, threadIdx.x, kMoveThreads);
         if (y == 0 && threadIdx.x == 0) {
             c.refs[to] = c.refs[from];
             c.refs[from] = 0;
@@ -540,6 +537,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move(Kv c) {
 
 // -------------------------------------------------------------- page copies
 __global__ void __launch_bounds__(kMoveThreads) copy_pages(Kv c, const int32_t *src, const int32_t *dst, int n) {
+    griddep_wait();
     const int64_t units = (int64_t)n * c.layers * 2;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int k = (int)(u / (2 * c.layers)), y = (int)(u - (int64_t)k * 2 * c.layers);
@@ -551,7 +549,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages(Kv c, const int32_t *
         if (from == to) continue;
         uint16_t *pool = (y & 1) ? c.v : c.k;
         const int64_t l = (int64_t)(y >> 1) * c.layer_stride;
-        copy_page(c, pool + l + from * c.page_stride, pool + l + to * c.page_stride, c.ps, threadIdx.x, kMoveThreads);
+        copy_page<8>(c, pool + l + from * c.page_stride, pool + l + to * c.page_stride, c.ps, threadIdx.x, kMoveThreads);
     }
 }
 
@@ -563,7 +561,7 @@ dim3 grid_for(int64_t units) {
 
 cudaError_t launch_kv_commit(const csgmv_kv_cache &kv, const CommitParams &p, cudaStream_t stream) {
     const Kv c = view(kv);
-    cudaError_t e = launch_kernel(commit_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, false, c, p);
+    cudaError_t e = launch_kernel(commit_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c, p);
     if (e != cudaSuccess) return e;
     // at most every row of the batch, eight (row, layer) pairs a block
     return launch_kernel(commit_move, grid_for((p.num_tokens * c.layers + 7) / 8), kMoveThreads, 0, stream, 0, true, c,
@@ -574,7 +572,7 @@ cudaError_t launch_kv_fork(const csgmv_kv_cache &kv, const int32_t *parents, con
                            cudaStream_t stream) {
     const Kv c = view(kv);
     cudaError_t e =
-        launch_kernel(fork_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, false, c, parents, children, n);
+        launch_kernel(fork_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c, parents, children, n);
     if (e != cudaSuccess) return e;
     return launch_kernel(fork_move, dim3((unsigned)n, 1 + 2 * (unsigned)c.layers), kMoveThreads, 0, stream, 0, true, c,
                          parents, children);
@@ -582,12 +580,12 @@ cudaError_t launch_kv_fork(const csgmv_kv_cache &kv, const int32_t *parents, con
 
 cudaError_t launch_kv_free(const csgmv_kv_cache &kv, const int32_t *seqs, const int32_t *keep, int n,
                            cudaStream_t stream) {
-    return launch_kernel(free_pages, dim3((unsigned)n), kMoveThreads, 0, stream, 0, false, view(kv), seqs, keep);
+    return launch_kernel(free_pages, dim3((unsigned)n), kMoveThreads, 0, stream, 0, true, view(kv), seqs, keep);
 }
 
 cudaError_t launch_kv_compact(const csgmv_kv_cache &kv, cudaStream_t stream) {
     const Kv c = view(kv);
-    cudaError_t e = launch_kernel(compact_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, false, c);
+    cudaError_t e = launch_kernel(compact_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c);
     if (e != cudaSuccess) return e;
     return launch_kernel(compact_move, grid_for((int64_t)c.pages * c.layers * 2), kMoveThreads, 0, stream, 0, true, c);
 }
@@ -595,7 +593,7 @@ cudaError_t launch_kv_compact(const csgmv_kv_cache &kv, cudaStream_t stream) {
 cudaError_t launch_kv_copy(const csgmv_kv_cache &kv, const int32_t *src, const int32_t *dst, int n,
                            cudaStream_t stream) {
     const Kv c = view(kv);
-    return launch_kernel(copy_pages, grid_for((int64_t)n * c.layers * 2), kMoveThreads, 0, stream, 0, false, c, src,
+    return launch_kernel(copy_pages, grid_for((int64_t)n * c.layers * 2), kMoveThreads, 0, stream, 0, true, c, src,
                          dst, n);
 }
 

@@ -51,6 +51,7 @@ int check_kv(const csgmv_kv_cache *kv) {
         return fail(CSGMV_ERR_INVALID_ARG, "kv cache buffers must be 4-byte aligned");
     if (kv->dtype != CSGMV_DTYPE_BF16 && kv->dtype != CSGMV_DTYPE_F16)
         return fail(CSGMV_ERR_INVALID_ARG, "kv cache dtype %d must be bf16 or f16", kv->dtype);
+    if (kv->num_layers > 16384) return fail(CSGMV_ERR_UNSUPPORTED, "at most 16384 layers");
     if (kv->num_layers <= 0 || kv->num_pages <= 0 || kv->num_kv_heads <= 0 || kv->max_seqs <= 0 ||
         kv->max_pages_per_seq <= 0)
         return fail(CSGMV_ERR_INVALID_ARG, "kv cache sizes must be positive");
@@ -66,6 +67,7 @@ int check_kv(const csgmv_kv_cache *kv) {
     if (kv->layer_stride % 8 || kv->page_stride % 8 || kv->head_stride % 8 || kv->token_stride % 8 ||
         kv->layer_stride < 0 || kv->page_stride <= 0 || kv->head_stride <= 0 || kv->token_stride <= 0)
         return fail(CSGMV_ERR_INVALID_ARG, "kv cache strides must be positive multiples of 8");
+    if (kv->page_stride > INT32_MAX) return fail(CSGMV_ERR_UNSUPPORTED, "page_stride exceeds 2^31 - 1 elements");
     // a head's rows, a page and a layer each keep to themselves: pages with
     // heads outside or inside the token axis, whatever the padding
     const int64_t D = kv->head_dim, H = kv->num_kv_heads, P = kv->page_size;
