@@ -18,9 +18,12 @@
 // lanes and 16 columns of rows, P^T in shared memory.  The tensor core then does
 // an eighth of the work, and that counts although it has time for all of it:
 // with 128-row products the power limit lowers the clock (1.3 to 1.6 GHz).
-// Up to 64 rows the rows are repeated in the upper 64 lanes; each copy
-// keeps its own maximum and sum over its half of every tile's tokens (its
-// weights for the other half are 0), and the copies are joined once an item.
+//
+// More rows.  The exponentials of a full tile take an SM 512 clocks, all of the
+// softmax's instructions some 800; what costs is the latency of its steps (read
+// S, agree on the maximum, exponentials, store P).  So sixteen warps share it,
+// 32 tokens of 32 rows each, and only when some score passes its row's maximum
+// by 2^8 do the four warps of a quadrant exchange maxima.
 //
 // Split.  The tiles of all (request, kv head, row tile) items form one axis
 // that is cut into parts of equal cost (cost_of below), one a CTA (one CTA an
@@ -36,14 +39,13 @@
 //
 // One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, an
 // MMA warp issues S = Q K^T two tiles ahead of O += P V (three S buffers, each
-// P in its S's place), eight warps do the softmax from tensor memory, two for
-// 32 rows: a thread has half a row's tokens.
+// P in its S's place), sixteen warps do the softmax from tensor memory.
+
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include <map>
 #include <mutex>
-#include <type_traits>
 
 #include "serving.cuh"
 
@@ -53,10 +55,10 @@ namespace {
 constexpr int kTile = 128;         // rows of a row tile, tokens of a token tile
 constexpr int kGroups = kTile / 8; // 8-row groups: the unit of the shared-memory layout
 constexpr int kAttnCtas = 152;     // one CTA an SM
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16;
 constexpr int kWarpK = kSoftWarps, kWarpV = kSoftWarps + 1, kWarpMma = kSoftWarps + 2;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 3);
-constexpr int kBufs = 3;           // S buffers in tensor memory
+constexpr int kBufs = 3;           // S buffers in tensor memory, P^T buffers in shared memory
 constexpr int kMaxRequests = 16000;  // 12 bytes each in the rings' memory
 constexpr int kCombineThreads = 128;
 constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
@@ -71,9 +73,9 @@ struct Shape {
     static constexpr int kRing = 2 * kSlots * kTileBytes;
     static constexpr int kBars = 4 * kSlots + 3 * kBufs + 1;
     static constexpr int kQBytes = 32768;               // Q, or 16 rows of it and P^T
-    static constexpr int kPairBytes = 2 * 2 * kTile * 4;
-    static constexpr int kTurnBytes = 64 + 2 * 256;     // flags, maxima, sums
-    static constexpr int kSmem = kQBytes + kRing + kPairBytes + kTurnBytes + (kBars + 1) * 8 + 64;
+    static constexpr int kRedBytes = 4 * kTile * 4;     // maxima or sums of a row's quarters
+    static constexpr int kFlagBytes = 2 * 16 * 4;       // a warp's flag, by turns
+    static constexpr int kSmem = kQBytes + kRing + kRedBytes + kFlagBytes + (kBars + 1) * 8 + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -172,21 +174,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-    uint32_t r[8];
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
+    uint32_t r[4];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
         "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 64) tmem_ld64(taddr, v);
-    else tmem_ld32(taddr, v);
+    if constexpr (N == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[N]) {
+    if constexpr (N == 32) tmem_st32(taddr, v);
+    else tmem_st16(taddr, v);
 }
 
 template <bool F16>
@@ -244,16 +268,15 @@ __device__ __forceinline__ Req load_req(const AttnParams &p, int b, int *bad) {
     return r;
 }
 
-// Up to kFewRows rows: turned over; up to kSomeRows: two copies.
-constexpr int kFewRows = 16, kSomeRows = 64;
+constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 
 // What the parts of the axis are weighed by, in units of 64 clocks.  Measured
 // on long axes: a tile's K and V come in 2870 (head_dim 64: 1430) clocks of an
 // SM's share of HBM, shared by the row tiles of a head, which find them in L2;
-// its softmax takes 1000 clocks turned over, 1400 in two copies, 1750 (half) or
-// 2100 (bfloat16) for a full row tile.  Beginning and ending an item costs 800
-// turned over, 5000 otherwise.  With equal tile counts instead, the CTAs of
-// short sequences ran 15 to 30 % longer than the others.
+// its softmax takes 1000 clocks turned over, otherwise 1350 (half) or 1700
+// (bfloat16).  Beginning and ending an item costs 800 turned over, 4000
+// otherwise.  With equal tile counts instead, the CTAs of short sequences ran
+// 15 to 30 % longer than the others.
 struct Cost {
     int mt, nt;          // row tiles and token tiles
     int tile[2], item[2];  // of a full row tile, of the last: one token tile, the whole item
@@ -261,9 +284,9 @@ struct Cost {
 };
 __device__ __forceinline__ int tile_cost(int rows, int mt, int d, bool f16) {
     const int bytes = (d == 128 ? 45 : 22) / mt;
-    return max(bytes, rows <= kFewRows ? 16 : rows <= kSomeRows ? 22 : f16 ? 28 : 33);
+    return max(bytes, rows <= kFewRows ? 16 : f16 ? 21 : 27);
 }
-__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 78; }
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 62; }
 __device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p) {
     Cost c;
     const Req r = {0, T, L, 0};
@@ -374,10 +397,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     const AttnParams &p = k.p;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *q_s = smem, *k_ring = smem + S::kQBytes, *v_ring = k_ring + S::kSlots * S::kTileBytes;
-    float(*pair_s)[2][kTile] = reinterpret_cast<float(*)[2][kTile]>(k_ring + S::kRing);  // a row's two halves, by turns
-    int4 *flag_s = reinterpret_cast<int4 *>(k_ring + S::kRing + S::kPairBytes);  // [turn][half] of the four quadrants
-    float(*max_s)[4][8] = reinterpret_cast<float(*)[4][8]>(flag_s + 4), (*sum_s)[4][8] = max_s + 2;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kPairBytes + S::kTurnBytes);
+    float *red_s = reinterpret_cast<float *>(k_ring + S::kRing);
+    int *flag_s = reinterpret_cast<int *>(k_ring + S::kRing + S::kRedBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kRedBytes + S::kFlagBytes);
     uint64_t *k_full = bars, *k_empty = k_full + S::kSlots, *v_full = k_empty + S::kSlots, *v_empty = v_full + S::kSlots,
              *s_full = v_empty + S::kSlots, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
              *q_ready = pv_done + kBufs;
@@ -542,6 +564,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                        v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes),
                        p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
         int it = 0, item = 0;
+        int wide = -1;  // the last tile that was not turned over
         Walk w = w0;
         bool more;
         do {
@@ -552,8 +575,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
             auto scores = [&](int t, int i) {
                 const int s = i % S::kSlots, buf = i % kBufs;
-                // the buffer's last P has been used
-                if (i >= kBufs) mbar_wait(&pv_done[buf], ((i / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
+                // The softmax has read what the buffer held; but P may lie there (turned over it
+                // does not) until its product is done.
+                if (i >= kBufs && (!few || i - kBufs <= wide))
+                    mbar_wait(&pv_done[buf], ((i / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
                 mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
@@ -600,22 +625,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         if (x < steps) {
+                            // P of 32 tokens lies in 16 columns, its low parts in the next 16
                             const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
-                            mma_ts(lead, t_o, pt + x * 8, d, id_pv, j > 0 || x > 0);
-                            if (!F16) mma_ts(lead, t_o, pt + 64 + x * 8, d, id_pv, true);
+                            const uint32_t a = pt + (x / 2) * 32 + (x % 2) * 8;
+                            mma_ts(lead, t_o, a, d, id_pv, j > 0 || x > 0);
+                            if (!F16) mma_ts(lead, t_o, a + 16, d, id_pv, true);
                         }
                     }
                 }
                 commit_one(lead, &v_empty[s]);
                 commit_one(lead, &pv_done[buf]);
             }
+            if (!few) wide = it - 1;
             ++item;
             w = wn;
         } while (more);
     } else {
         // ---------------------------------------------------------- softmax
-        // warps w and w + 4 share 32 lanes
-        const int quad = warp & 3, half = warp >> 2, pos = quad * 32 + lane;
+        // warps w, w + 4, w + 8 and w + 12 share 32 lanes (a quadrant): each has a quarter of the work on them
+        const int quad = warp & 3, quarter = warp >> 2, pos = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const float c = p.scale * kLog2e;
         constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
@@ -623,10 +651,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         Walk w = w0;
         bool more;
 
-        // Q of a segment: from memory, and into the swizzled tile.  A thread has
-        // half a row; 16 bytes when the products are turned over.
-        uint4 qv[D / 16];
-        auto lane_row = [&](int rows) { return rows <= kSomeRows ? (quad & 1) * 32 + lane : pos; };
+        // Q of a segment: from memory, and into the swizzled tile.  A thread has a
+        // quarter of a row; 16 bytes when the products are turned over.
+        uint4 qv[D / 32];
         auto q_src = [&](const Walk &u, int row, int el) {
             const int at = u.m * kTile + row, t = at / p.group;
             return p.q + (int64_t)(u.r.lo + t) * p.q_ts + (u.h * p.group + (at - t * p.group)) * p.q_hs + el;
@@ -636,13 +663,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             if (rows <= kFewRows) {
                 const int row = tid / (D / 8), el = (tid % (D / 8)) * 8;
                 if (row < rows) qv[0] = ldg16(q_src(u, row, el));
-            } else {
-                const int row = lane_row(rows);
-                if (row < rows) {
-                    const uint16_t *src = q_src(u, row, half * (D / 2));
+            } else if (pos < rows) {
+                const uint16_t *src = q_src(u, pos, quarter * (D / 4));
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) qv[x] = ldg16(src + x * 8);
-                }
+                for (int x = 0; x < D / 32; ++x) qv[x] = ldg16(src + x * 8);
             }
         };
         auto q_put = [&](int row, int chunk, uint4 v) {
@@ -655,9 +679,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             if (rows <= kFewRows) {
                 const int row = tid / (D / 8);
                 if (row < rows) q_put(row, tid % (D / 8), qv[0]);
-            } else if (lane_row(rows) < rows) {
+            } else if (pos < rows) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) q_put(pos, half * (D / 16) + x, qv[x]);
+                for (int x = 0; x < D / 32; ++x) q_put(pos, quarter * (D / 32) + x, qv[x]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -670,7 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             Walk wn = w;
             more = wn.next(p);
             const int rows = w.rows(p);
-            const bool few = rows <= kFewRows, twice = !few && rows <= kSomeRows;
+            const bool few = rows <= kFewRows;
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             const bool whole = w.n == w.nt;
             const int cell = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
@@ -681,6 +705,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 __syncwarp();
                 tc_fence_after();
             };
+            // (A warp may get here before another has P of the tile before last ready: the barrier is
+            // the buffer's own, so the parity cannot be that of an older product.)
             auto await_pv = [&]() {  // of the tile before
                 mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
@@ -719,6 +745,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[it % kBufs]);
             };
+            // Whether any of the four warps that share maxima (a quadrant, or a turned-over row group:
+            // barriers 1 .. 4 and 5 .. 8, never one for both) has a score past its maximum's leeway.
+            auto any_grows = [&](bool grow, int id, int *flags, int mine) {
+                const bool any = __any_sync(kFullMask, grow);
+                if (lane == 0) flags[(it & 1) * 16 + mine] = any;
+                named_bar_sync(id, 128);
+                const int4 f = *reinterpret_cast<const int4 *>(flags + (it & 1) * 16 + (mine & ~3));
+                return (f.x | f.y | f.z | f.w) != 0;
+            };
             // What row t sees of the drafted tokens' non-finite values, from element el on.
             auto add_odd = [&](int t, int el, auto &o) {
                 constexpr int N = sizeof(o) / sizeof(float);
@@ -745,17 +780,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 
             if (few) {
                 // ------------------------------------------- turned over
-                // a thread has token `pos` and rows 8 half .. 8 half + 7, of which nl are real
-                const int nl = min(8, rows - 8 * half);
-                float m[8], l[8];
+                // a thread has token `pos` and rows 4 quarter .. 4 quarter + 3, of which nl are real
+                const int nl = min(4, rows - 4 * quarter);
+                float m[4], l[4];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+                for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.0f;
                 for (int j = 0; j < w.n; ++j, ++it) {
                     const int t = w.t0 + j, buf = it % kBufs;
                     await_s();
                     if (nl > 0) {
-                        float s[8];
-                        tmem_ld8(tmem + buf * 128 + lane_base + 8 * half, s);
+                        float s[4];
+                        tmem_ld4(tmem + buf * 128 + lane_base + 4 * quarter, s);
                         uint32_t see = (1u << nl) - 1u;
                         const int vk = t * kTile + pos;
                         if (vk >= w.r.L) {
@@ -763,34 +798,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             uint32_t bits = 0;
                             if (jt >= 0 && jt < w.r.T)
                                 for (int r = 0; r < nl; ++r)
-                                    bits |= (tree_word(p, w.r, (w.m * kTile + 8 * half + r) / p.group, jt) & 1u) << r;
+                                    bits |= (tree_word(p, w.r, (w.m * kTile + 4 * quarter + r) / p.group, jt) & 1u) << r;
                             see &= bits;
                         }
                         __syncwarp();
                         bool grow = false;
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
+                        for (int r = 0; r < 4; ++r) {
                             s[r] = (see >> r) & 1 ? s[r] : -INFINITY;
                             grow |= s[r] * c > m[r] + kLazy;  // from -inf: any score at all
                         }
-                        const bool any = __any_sync(kFullMask, grow);
-                        if (lane == 0) reinterpret_cast<int *>(flag_s + (it & 1) * 2 + half)[quad] = any;
-                        named_bar_sync(6 + half, 128);
-                        const int4 f4 = flag_s[(it & 1) * 2 + half];
-                        if (f4.x | f4.y | f4.z | f4.w) {
+                        if (any_grows(grow, 5 + quarter, flag_s, quarter * 4 + quad)) {
+                            float *mx = red_s + quarter * kTile;  // [quadrant][row]
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) {
+                            for (int r = 0; r < 4; ++r) {
                                 float x = s[r] * c;
 #pragma unroll
                                 for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, o));
-                                if (lane == 0) max_s[half][quad][r] = x;
+                                if (lane == 0) mx[quad * 4 + r] = x;
                             }
-                            named_bar_sync(6 + half, 128);
-                            float f[8];
+                            named_bar_sync(5 + quarter, 128);
+                            float f[4];
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                const float x = fmaxf(fmaxf(max_s[half][0][r], max_s[half][1][r]),
-                                                      fmaxf(max_s[half][2][r], max_s[half][3][r]));
+                            for (int r = 0; r < 4; ++r) {
+                                const float x = fmaxf(fmaxf(mx[r], mx[4 + r]), fmaxf(mx[8 + r], mx[12 + r]));
                                 const float mn = x > m[r] + kLazy ? x : m[r];
                                 f[r] = mn > m[r] ? ex2(m[r] - mn) : 1.0f;
                                 m[r] = mn;
@@ -800,20 +831,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                 await_pv();
 #pragma unroll
                                 for (int part = 0; part < 2; ++part) {
-                                    const uint32_t a = t_o + lane_base + part * 16 + half * 8;
-                                    float o[8];
-                                    uint32_t u[8];
-                                    tmem_ld8(a, o);
+                                    const uint32_t a = t_o + lane_base + part * 16 + quarter * 4;
+                                    float o[4];
+                                    uint32_t u[4];
+                                    tmem_ld4(a, o);
 #pragma unroll
-                                    for (int r = 0; r < 8; ++r) u[r] = __float_as_uint(o[r] * f[r]);
-                                    tmem_st8(a, u);
+                                    for (int r = 0; r < 4; ++r) u[r] = __float_as_uint(o[r] * f[r]);
+                                    tmem_st4(a, u);
                                 }
                                 tmem_wait_st();
                             }
                         }
-                        uint32_t hi[4], low[4];
+                        uint32_t hi[2], low[2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             float e[2];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
@@ -827,12 +858,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         if (it >= kBufs)  // the product before in this buffer
                             mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
                         // P^T: 64 bytes a token, high parts of 16 rows, then the low parts; 64-byte swizzle
-                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + ((half ^ x) << 4)), "r"(hi[0]),
-                                     "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64 + (quarter & 1) * 8, x = (pos >> 1) & 3;
+                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a + (((quarter >> 1) ^ x) << 4)), "r"(hi[0]),
+                                     "r"(hi[1])
                                      : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + (((2 + half) ^ x) << 4)), "r"(low[0]),
-                                     "r"(low[1]), "r"(low[2]), "r"(low[3])
+                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a + (((2 + (quarter >> 1)) ^ x) << 4)), "r"(low[0]),
+                                     "r"(low[1])
                                      : "memory");
                     }
                     if (edge(t)) clean_v(t);
@@ -843,29 +874,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 const bool early = more && wn.rows(p) <= kFewRows;
                 if (more) q_load(wn);
                 if (nl > 0) {
+                    float *sum = red_s + quarter * kTile + 16;  // [quadrant][row], beside the maxima
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
+                    for (int r = 0; r < 4; ++r) {
                         l[r] = warp_sum(l[r]);
-                        if (lane == 0) sum_s[half][quad][r] = l[r];
+                        if (lane == 0) sum[quad * 4 + r] = l[r];
                     }
-                    named_bar_sync(6 + half, 128);
+                    named_bar_sync(5 + quarter, 128);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        l[r] = (sum_s[half][0][r] + sum_s[half][1][r]) + (sum_s[half][2][r] + sum_s[half][3][r]);
+                    for (int r = 0; r < 4; ++r) l[r] = (sum[r] + sum[4 + r]) + (sum[8 + r] + sum[12 + r]);
                 }
                 if (early) q_store(wn);
                 await_pv();
                 if (nl > 0) {
-                    float o[8], low[8];
-                    tmem_ld8(t_o + lane_base + half * 8, o);
-                    tmem_ld8(t_o + lane_base + 16 + half * 8, low);
+                    float o[4], low[4];
+                    tmem_ld4(t_o + lane_base + quarter * 4, o);
+                    tmem_ld4(t_o + lane_base + 16 + quarter * 4, low);
                     if (pos < D) {  // a thread has element `pos`
                         const bool odd = *odd_item == item;
                         float *part = k.part + ((int64_t)cell * (D / 4) + pos / 4) * kTile * 4 + (pos & 3);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
+                        for (int r = 0; r < 4; ++r) {
                             if (r < nl) {
-                                const int row = 8 * half + r, at = w.m * kTile + row, tr = at / p.group;
+                                const int row = 4 * quarter + r, at = w.m * kTile + row, tr = at / p.group;
                                 float x[1] = {o[r] + low[r]};
                                 if (odd) add_odd(tr, pos, x);
                                 if (whole)
@@ -880,179 +911,105 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (more && !early) q_store(wn);
             } else {
                 // ------------------------------------------------- as is
-                // a thread has a row, and half of its copy's share of the tokens (and of O's columns)
-                const int copy = twice ? quad >> 1 : 0, row = lane_row(rows);
-                const bool live = row < rows, warp_live = row - lane < rows;
-                const int at = w.m * kTile + row, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
-                float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this half
-                // P of one tile; N: tokens of this warp
-                auto weigh = [&](auto n_tag, int j) {
-                    constexpr int N = decltype(n_tag)::value;
-                    const int t = w.t0 + j, c0 = (2 * copy + half) * N;
-                    const uint32_t t_s = tmem + (it % kBufs) * 128 + lane_base;
-                    float s[N];
-                    if (keys_of(t) > c0) {
-                        tmem_load(t_s + c0, s);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) s[i] = -INFINITY;
-                    }
-                    if (edge(t)) {
-#pragma unroll
-                        for (int x = 0; x < N; x += 32) {
-                            const int k0 = t * kTile + c0 + x, n = w.r.L - k0;
+                // a thread has a row, and a quarter of every tile's tokens (and of O's columns)
+                const bool live = pos < rows, warp_live = quad * 32 < rows;
+                const int at = w.m * kTile + pos, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
+                float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this quarter
+                for (int j = 0; j < w.n; ++j, ++it) {
+                    const int t = w.t0 + j;
+                    await_s();
+                    if (warp_live) {
+                        const uint32_t t_s = tmem + (it % kBufs) * 128 + lane_base + quarter * 32;
+                        float s[32];
+                        tmem_ld32(t_s, s);
+                        if (edge(t)) {
+                            const int k0 = t * kTile + quarter * 32, n = w.r.L - k0;
                             uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
                             if (live) bits |= tree_word(p, w.r, t_row, k0 - gctx * 8);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[x + i] = (bits >> i) & 1 ? s[x + i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1 ? s[i] : -INFINITY;
                         }
-                    }
-                    __syncwarp();
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
+                        __syncwarp();
+                        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int i = 4; i < N; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    // the other half; both have read S once the barrier is passed, so P may take its place
-                    pair_s[it & 1][half][pos] = top;
-                    tc_fence_before();
-                    named_bar_sync(1 + quad, 64);
-                    tc_fence_after();
-                    top = fmaxf(top, pair_s[it & 1][half ^ 1][pos]);
-                    const bool grow = live && top > m + kLazy;  // from -inf: any score at all
-                    if (__any_sync(kFullMask, grow)) {
-                        const float mn = grow ? top : m;
-                        if (j > 0) {  // O so far, in units of 2^m: this warp's half of its columns
-                            const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
-                            await_pv();
+                        for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                        // from -inf: any score at all
+                        if (any_grows(live && top > m + kLazy, 1 + quad, flag_s, quad * 4 + quarter)) {
+                            red_s[quarter * kTile + pos] = top;
+                            named_bar_sync(1 + quad, 128);
+                            top = fmaxf(fmaxf(red_s[pos], red_s[kTile + pos]), fmaxf(red_s[2 * kTile + pos], red_s[3 * kTile + pos]));
+                            const bool grow = live && top > m + kLazy;
+                            const float mn = grow ? top : m;
+                            if (j > 0) {  // O so far, in units of 2^m: this warp's quarter of its columns
+                                const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
+                                await_pv();
+                                float o[D / 4];
+                                uint32_t u[D / 4];
+                                const uint32_t a = t_o + lane_base + quarter * (D / 4);
+                                tmem_load(a, o);
 #pragma unroll
-                            for (int x = 0; x < D / 64; ++x) {
-                                float o[32];
-                                uint32_t u[32];
-                                const uint32_t a = t_o + lane_base + half * (D / 2) + x * 32;
-                                tmem_ld32(a, o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                                tmem_st32(a, u);
+                                for (int i = 0; i < D / 4; ++i) u[i] = __float_as_uint(o[i] * f);
+                                tmem_store(a, u);
+                                l *= f;
                             }
-                            l *= f;
+                            m = mn;
                         }
-                        m = mn;
-                    }
-                    const float base = m == -INFINITY ? 0.0f : kShift - m;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int x = 0; x < N / 2; x += 16) {
+                        const float base = m == -INFINITY ? 0.0f : kShift - m;
+                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         uint32_t u[16], low[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float e0 = ex2(fmaf(s[2 * (x + i)], c, base)), e1 = ex2(fmaf(s[2 * (x + i) + 1], c, base));
+                            const float e0 = ex2(fmaf(s[2 * i], c, base)), e1 = ex2(fmaf(s[2 * i + 1], c, base));
                             sum[i & 3] += e0 + e1;
                             u[i] = pack2<F16>(e0, e1);
                             if (!F16) low[i] = pack2_rest<F16>(u[i], e0, e1);
                         }
-                        tmem_st16(t_s + c0 / 2 + x, u);
-                        if (!F16) tmem_st16(t_s + 64 + c0 / 2 + x, low);
+                        tmem_st16(t_s, u);
+                        if (!F16) tmem_st16(t_s + 16, low);
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_wait_st();
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    if constexpr (N < 64) {  // no weight for the other copy's tokens: half its columns each
-                        const uint32_t zero[16] = {};
-                        const uint32_t a = t_s + (copy ^ 1) * 32 + half * 16;
-                        tmem_st16(a, zero);
-                        if (!F16) tmem_st16(a + 64, zero);
-                    }
-                    tmem_wait_st();
-                };
-                for (int j = 0; j < w.n; ++j, ++it) {
-                    await_s();
-                    if (warp_live) {
-                        if (twice) weigh(std::integral_constant<int, 32>{}, j);
-                        else weigh(std::integral_constant<int, 64>{}, j);
-                    }
-                    if (edge(w.t0 + j)) clean_v(w.t0 + j);
+                    if (edge(t)) clean_v(t);
                     p_is_ready();
                 }
-                // Q of the next segment (its products with this one's Q are done), unless the copies
-                // are joined where it goes
+                // Q of the next segment: its products with this one's Q are done
                 if (more) q_load(wn);
                 if (warp_live) {
-                    pair_s[it & 1][half][pos] = l;
-                    named_bar_sync(1 + quad, 64);
-                    l += pair_s[it & 1][half ^ 1][pos];
-                    named_bar_sync(1 + quad, 64);  // the next tile's exchange may be in this turn again
+                    named_bar_sync(1 + quad, 128);  // (the maxima have been read)
+                    red_s[quarter * kTile + pos] = l;
+                    named_bar_sync(1 + quad, 128);
+                    l = (red_s[pos] + red_s[kTile + pos]) + (red_s[2 * kTile + pos] + red_s[3 * kTile + pos]);
                 }
-                if (more && !twice) q_store(wn);
-                // (A warp may be here before another has P of the tile before last ready: pv_done has a
-                // barrier a buffer, so that the parity waited for cannot be that of an older product.)
+                if (more) q_store(wn);
                 await_pv();
-                float f = 1.0f;
-                float4 *o_s = reinterpret_cast<float4 *>(q_s) + row;  // [D / 4][64 rows] of the upper copy
-                if (twice) {
-                    if (warp_live && half == 0) {
-                        pair_s[0][0][pos] = m;
-                        pair_s[0][1][pos] = l;
-                    }
-                    named_bar_sync(5, kSoftWarps * 32);
-                    const float m2 = pair_s[0][0][pos ^ 64], l2 = pair_s[0][1][pos ^ 64], ma = fmaxf(m, m2);
-                    const float base = ma == -INFINITY ? 0.0f : ma;
-                    f = ex2(m - base);
-                    l = l * f + l2 * ex2(m2 - base);
-                    m = ma;
-                    if (copy == 1 && warp_live) {
-#pragma unroll 1
-                        for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
-                            float o[32];
-                            tmem_ld32(t_o + lane_base + x * 32, o);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                o_s[(x * 8 + i) * 64] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-                        }
-                    }
-                    named_bar_sync(5, kSoftWarps * 32);
-                }
-                if (warp_live && copy == 0) {
+                if (warp_live) {
                     const bool odd = *odd_item == item;
                     const float inv = inverse(l);
-                    uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs;
-                    float4 *part = reinterpret_cast<float4 *>(k.part) + (int64_t)cell * (D / 4) * kTile + row;
-#pragma unroll 1
-                    for (int x = half * (D / 64); x < (half + 1) * (D / 64); ++x) {
-                        float o[32];
-                        tmem_ld32(t_o + lane_base + x * 32, o);
-                        if (live) {
-                            if (twice) {
+                    const int el = quarter * (D / 4);
+                    float o[D / 4];
+                    tmem_load(t_o + lane_base + el, o);
+                    if (live) {
+                        if (odd) add_odd(t_row, el, o);
+                        if (whole) {
+                            uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs + el;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float4 v = o_s[(x * 8 + i) * 64];
-                                    o[4 * i] = o[4 * i] * f + v.x;
-                                    o[4 * i + 1] = o[4 * i + 1] * f + v.y;
-                                    o[4 * i + 2] = o[4 * i + 2] * f + v.z;
-                                    o[4 * i + 3] = o[4 * i + 3] * f + v.w;
-                                }
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint4 v;
+                                v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                                v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                                v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                                v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                                *reinterpret_cast<uint4 *>(dst + i * 8) = v;
                             }
-                            if (odd) add_odd(t_row, x * 32, o);
-                            if (whole) {
+                        } else {
+                            float4 *part = reinterpret_cast<float4 *>(k.part) + ((int64_t)cell * (D / 4) + el / 4) * kTile + pos;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    uint4 v;
-                                    v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                                    v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                                    v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                                    v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-                                    *reinterpret_cast<uint4 *>(dst + x * 32 + i * 8) = v;
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    part[(x * 8 + i) * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                            }
+                            for (int i = 0; i < D / 16; ++i)
+                                part[i * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
-                        __syncwarp();  // the next load is the whole warp's
+                        if (quarter == 0) put_row(pos, m, l);
                     }
-                    if (live && half == 0) put_row(row, m, l);
-                }
-                if (twice) {
-                    named_bar_sync(5, kSoftWarps * 32);
-                    if (more) q_store(wn);
                 }
             }
             if (tid == 0 && !whole) {
