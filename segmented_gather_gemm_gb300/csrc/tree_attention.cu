@@ -150,6 +150,33 @@ __device__ __forceinline__ uint32_t elect_lead() {
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
     return r;
 }
+// Two fp32 numbers in one 64-bit register: one instruction for two of the same
+// operation (as long as two, but half the issue slots).
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 apart(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -930,10 +957,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1 ? s[i] : -INFINITY;
                         }
                         __syncwarp();
-                        float mx[4] = {s[0], s[1], s[2], s[3]};
+                        float mx[2] = {s[0], s[1]};
 #pragma unroll
-                        for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                        for (int i = 2; i < 30; i += 4) {
+                            mx[0] = max3(mx[0], s[i], s[i + 1]);
+                            mx[1] = max3(mx[1], s[i + 2], s[i + 3]);
+                        }
+                        float top = fmaxf(max3(mx[0], s[30], s[31]), mx[1]) * c;
                         // from -inf: any score at all
                         if (any_grows(live && top > m + kLazy, 1 + quad, flag_s, quad * 4 + quarter)) {
                             red_s[quarter * kTile + pos] = top;
@@ -956,18 +986,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             m = mn;
                         }
                         const float base = m == -INFINITY ? 0.0f : kShift - m;
-                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        const uint64_t c2 = two(c, c), base2 = two(base, base), minus = two(-1.0f, -1.0f);
+                        uint64_t sum[2] = {0, 0};
                         uint32_t u[16], low[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float e0 = ex2(fmaf(s[2 * i], c, base)), e1 = ex2(fmaf(s[2 * i + 1], c, base));
-                            sum[i & 3] += e0 + e1;
+                            const float2 x = apart(fma2(two(s[2 * i], s[2 * i + 1]), c2, base2));
+                            const float e0 = ex2(x.x), e1 = ex2(x.y);
+                            const uint64_t e = two(e0, e1);
+                            sum[i & 1] = add2(sum[i & 1], e);
                             u[i] = pack2<F16>(e0, e1);
-                            if (!F16) low[i] = pack2_rest<F16>(u[i], e0, e1);
+                            if (!F16) {
+                                const float2 h = unpack_bf16x2(u[i]), r = apart(fma2(two(h.x, h.y), minus, e));
+                                low[i] = pack2<F16>(r.x, r.y);
+                            }
                         }
                         tmem_st16(t_s, u);
                         if (!F16) tmem_st16(t_s + 16, low);
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        const float2 both = apart(add2(sum[0], sum[1]));
+                        l += both.x + both.y;
                         tmem_wait_st();
                     }
                     if (edge(t)) clean_v(t);
