@@ -32,6 +32,17 @@
 // workspace (at most two a CTA), which a second kernel joins in order of the
 // axis: results do not depend on timing.
 //
+// More than 128 rows.  Taken one after the other, the row tiles of a head each
+// read its K and V from HBM: a head's tokens do not stay in L2 while an SM goes
+// through them.  So two CTAs may share a part and walk it together, each with
+// one of two row tiles, the second to ask for a tile of K and V finding it in
+// L2.  That doubles a part's length, and the CTA whose row tile is missing or
+// small waits; every CTA adds up the cost of both ways and takes the cheaper
+// (`ways`).  32 trees of 33 to 64 tokens, 4 query heads a kv head, 500 to 8192
+// cached: 174 us together, 232 us apart.  (Both row tiles in one CTA, K and V
+// read once: 221 us, for each tile then waits for the other's softmax, products
+// and their hand-overs.)
+//
 // Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
 // keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
 // rounding, so there P goes in as a high and a low part (16 bits) in two
@@ -91,7 +102,7 @@ struct AttnKernelParams {
     AttnMaps maps;
     float *part;      // [2 * kAttnCtas][D / 4][kTile] float4: unscaled O
     float *ml;        // [2 * kAttnCtas][2][kTile]: m, l
-    int4 *starters;   // [kAttnCtas]: the item a CTA begins and does not end {first token, h, row tile, rows}, or {-1}
+    int4 *starters;   // [kAttnCtas]: the item a CTA begins and does not end {first token, h, first row, rows and ways}, or {-1}
     int *tails;       // [kAttnCtas]: of an item begun by an earlier CTA: 0 nothing, 1 a middle part, 2 its end
     int form;         // kPages*
     int box_groups;   // 8-row groups of a whole box
@@ -273,7 +284,7 @@ struct Req {
     __device__ __forceinline__ int ctx_groups() const { return (L + 7) >> 3; }
     __device__ __forceinline__ int groups() const { return ctx_groups() + ((T + 7) >> 3); }
     __device__ __forceinline__ int token_tiles() const { return (groups() + kGroups - 1) / kGroups; }
-    __device__ __forceinline__ int row_tiles(int group) const { return (T * group + kTile - 1) / kTile; }
+    __device__ __forceinline__ int items(int group, int ways) const { return (T * group + kTile * ways - 1) / (kTile * ways); }
 };
 
 // Request b, with T = 0 (no work) when it is not sound; the status bit why.
@@ -298,33 +309,33 @@ __device__ __forceinline__ Req load_req(const AttnParams &p, int b, int *bad) {
 constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 
 // What the parts of the axis are weighed by, in units of 64 clocks.  Measured
-// on long axes: a tile's K and V come in 2870 (head_dim 64: 1430) clocks of an
-// SM's share of HBM, shared by the row tiles of a head, which find them in L2;
-// its softmax takes 1000 clocks turned over, otherwise 1350 (half) or 1700
-// (bfloat16).  Beginning and ending an item costs 800 turned over, 4000
-// otherwise.  With equal tile counts instead, the CTAs of short sequences ran
-// 15 to 30 % longer than the others.
+// on long axes: a tile's K and V of head_dim 128 come in 2870 clocks of an SM's
+// share of HBM, half of that when two CTAs read them together (of head_dim 64 in
+// less than the softmax takes); its softmax takes 1000 clocks turned over,
+// otherwise 1400 (half) or 1800 (bfloat16).  Beginning and ending an item costs
+// 800 turned over, 5800 otherwise.  With equal tile counts instead, the CTAs of
+// short sequences ran 15 to 30 % longer than the others.
 struct Cost {
-    int mt, nt;          // row tiles and token tiles
-    int tile[2], item[2];  // of a full row tile, of the last: one token tile, the whole item
+    int mi, nt;          // items and token tiles
+    int tile[2], item[2];  // of a full item, of the last: one token tile, the whole item
     int head;            // a kv head's items
 };
-__device__ __forceinline__ int tile_cost(int rows, int mt, int d, bool f16) {
-    const int bytes = (d == 128 ? 45 : 22) / mt;
-    return max(bytes, rows <= kFewRows ? 16 : f16 ? 21 : 27);
+__device__ __forceinline__ int tile_cost(int rows, bool shared, int d, bool f16) {
+    const int bytes = (d == 128 ? 45 : 16) >> (int)shared;
+    return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 28);
 }
-__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 62; }
-__device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p) {
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 90; }
+__device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p, int ways) {
     Cost c;
     const Req r = {0, T, L, 0};
-    c.mt = r.row_tiles(p.group);
+    c.mi = r.items(p.group, ways);
     c.nt = r.token_tiles();
-    const int rest = T * p.group - (c.mt - 1) * kTile;
-    c.tile[0] = tile_cost(kTile, c.mt, p.d, p.f16);
-    c.tile[1] = tile_cost(rest, c.mt, p.d, p.f16);
+    const int rest = T * p.group - (c.mi - 1) * ways * kTile, last = min(kTile, rest);  // the last item's rows, its first tile's
+    c.tile[0] = tile_cost(kTile, ways == 2, p.d, p.f16);
+    c.tile[1] = tile_cost(last, rest > kTile, p.d, p.f16);
     c.item[0] = item_cost(kTile) + c.nt * c.tile[0];
-    c.item[1] = item_cost(rest) + c.nt * c.tile[1];
-    c.head = (c.mt - 1) * c.item[0] + c.item[1];
+    c.item[1] = item_cost(last) + c.nt * c.tile[1];
+    c.head = (c.mi - 1) * c.item[0] + c.item[1];
     return c;
 }
 
@@ -344,23 +355,29 @@ struct Walk {
         n = (end.same_item(b, h, m) ? min(end.t, nt) : nt) - t0;
         return n > 0;
     }
-    __device__ __forceinline__ bool next(const AttnParams &p) {
-        if (end.same_item(b, h, m)) return false;
-        t0 = 0;
-        if (++m == r.row_tiles(p.group)) {
-            m = 0;
-            if (++h == p.hkv) {
-                h = 0;
-                do {
-                    if (++b >= p.bs) return false;
-                    int bad;
-                    r = load_req(p, b, &bad);
-                } while (r.T == 0 && b < end.b);
-                if (r.T == 0) return false;
-                nt = r.token_tiles();
+    // (`ways` row tiles are an item, of which the CTA has one.)
+    __device__ __forceinline__ bool next(const AttnParams &p, int ways) {
+        do {
+            if (end.same_item(b, h, m)) return false;
+            t0 = 0;
+            const int way = blockIdx.x & (ways - 1);
+            m += ways;
+            if ((m - way) * kTile >= r.T * p.group) {
+                m = way;
+                if (++h == p.hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= p.bs) return false;
+                        int bad;
+                        r = load_req(p, b, &bad);
+                    } while (r.T == 0 && b < end.b);
+                    if (r.T == 0) return false;
+                    nt = r.token_tiles();
+                }
             }
-        }
-        return cut();
+            if (!cut()) return false;
+        } while (rows(p) <= 0);  // an item without this way's row tile
+        return true;
     }
     __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kTile, r.T * p.group - m * kTile); }
 };
@@ -387,7 +404,7 @@ __device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r,
 
 // The place x units of cost along the axis (every CTA rounds it alike).
 // `ahead`: cost before each request, and the total; `tl`: their T and L.
-__device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead, const int2 *tl, int x) {
+__device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead, const int2 *tl, int ways, int x) {
     Place q = {p.bs, 0, 0, 0};
     if (x >= ahead[p.bs]) return q;
     int lo = 0, hi = p.bs;  // the last request with ahead <= x: it has work of its own
@@ -395,19 +412,19 @@ __device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead,
         const int mid = (lo + hi) >> 1;
         if (ahead[mid] <= x) lo = mid; else hi = mid;
     }
-    const Cost c = cost_of(tl[lo].x, tl[lo].y, p);
+    const Cost c = cost_of(tl[lo].x, tl[lo].y, p, ways);
     q.b = lo;
     int y = x - ahead[lo];
     q.h = y / c.head;
     y -= q.h * c.head;
-    q.m = min(y / c.item[0], c.mt - 1);
+    q.m = min(y / c.item[0], c.mi - 1);
     y -= q.m * c.item[0];
-    const int last = q.m == c.mt - 1, cost = c.tile[last];
+    const int last = q.m == c.mi - 1, cost = c.tile[last];
     y -= c.item[last] - c.nt * cost;
     q.t = y <= 0 ? 0 : (y + cost - 1) / cost;
     if (q.t >= c.nt) {  // the next item's beginning
         q.t = 0;
-        if (++q.m == c.mt) {
+        if (++q.m == c.mi) {
             q.m = 0;
             if (++q.h == p.hkv) {
                 q.h = 0;
@@ -468,21 +485,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     int2 *tl = reinterpret_cast<int2 *>(k_ring + ((4 * p.bs + 4 + 15) & ~15));
     Place *ends = reinterpret_cast<Place *>(q_s);
     long long all = 0;
+    int ways = 1;
     {
         long long *ws = reinterpret_cast<long long *>(q_s + 64);
+        long long shared = 0;  // of two CTAs that walk together
         for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
             const int b = b0 + tid;
             long long n = 0, tot;
             if (b < p.bs) {
                 int bad;
                 const Req r = load_req(p, b, &bad);
-                if (r.T) n = (long long)cost_of(r.T, r.L, p).head * p.hkv;
+                if (r.T) {
+                    n = (long long)cost_of(r.T, r.L, p, 1).head * p.hkv;
+                    shared += (long long)cost_of(r.T, r.L, p, 2).head * p.hkv;
+                }
                 tl[b] = make_int2(r.T, r.L);
                 if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
             }
             const long long pre = block_scan_ex(n, ws, &tot);
             if (b < p.bs) ahead[b] = (int)min(all + pre, (long long)INT32_MAX);
             all += tot;
+        }
+        if (p.num_tokens * p.group > kTile && gridDim.x > 1) {
+            long long tot;
+            block_scan_ex(shared, ws, &tot);
+            if (2 * tot < all && all <= INT32_MAX) {
+                ways = 2;
+                all = 0;
+                for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
+                    const int b = b0 + tid;
+                    long long n = 0;
+                    if (b < p.bs && tl[b].x) n = (long long)cost_of(tl[b].x, tl[b].y, p, 2).head * p.hkv;
+                    const long long pre = block_scan_ex(n, ws, &tot);
+                    if (b < p.bs) ahead[b] = (int)(all + pre);
+                    all += tot;
+                }
+            }
         }
     }
     if (all > INT32_MAX) {  // more than 32 bits of cost: refused
@@ -493,8 +531,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     __syncthreads();
     // this CTA's part: two warps find its two ends
     if (lane == 0 && warp < 2) {
-        const int q = (int)all / (int)gridDim.x, rest = (int)all - q * (int)gridDim.x, c = blockIdx.x + warp;
-        ends[warp] = place_at(p, ahead, tl, c * q + min(c, rest));
+        const int parts = gridDim.x / ways, q = (int)all / parts, rest = (int)all - q * parts, c = blockIdx.x / ways + warp;
+        ends[warp] = place_at(p, ahead, tl, ways, c < parts ? c * q + min(c, rest) : (int)all);
     }
     if (tid == 0) {
         k.starters[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -504,18 +542,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     Walk w0 = {};
     {
         const Place at = ends[0];
+        const int way = blockIdx.x & (ways - 1);
         w0.b = at.b;
         w0.h = at.h;
-        w0.m = at.m;
+        w0.m = at.m * ways + way;
         w0.t0 = at.t;
         w0.end = ends[1];
+        w0.end.m = w0.end.m * ways + way;
     }
     bool idle = all == 0 || w0.b >= p.bs;
     if (!idle) {
         int bad;
         w0.r = load_req(p, w0.b, &bad);
         w0.nt = w0.r.token_tiles();
-        idle = !w0.cut();
+        idle = !w0.cut() || (w0.rows(p) <= 0 && !w0.next(p, ways));
     }
     fence_proxy_async_smem();  // the rings' memory goes over to TMA
     tc_fence_before();
@@ -551,7 +591,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         int page = page_of(w, w.t0);
         bool more;
         do {
-            more = wn.next(p);  // looked up while this segment's tiles are loaded
+            more = wn.next(p, ways);  // looked up while this segment's tiles are loaded
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             const int whole = (w.r.L >> 3) & ~(bg - 1);  // groups in boxes that are full of tokens
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
@@ -596,7 +636,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         bool more;
         do {
             Walk wn = w;
-            more = wn.next(p);
+            more = wn.next(p, ways);
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
             auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
@@ -719,7 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 
         do {
             Walk wn = w;
-            more = wn.next(p);
+            more = wn.next(p, ways);
             const int rows = w.rows(p);
             const bool few = rows <= kFewRows;
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
@@ -1050,7 +1090,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 }
             }
             if (tid == 0 && !whole) {
-                if (w.t0 == 0) k.starters[blockIdx.x] = make_int4(w.r.lo, w.h, w.m, rows);
+                if (w.t0 == 0) k.starters[blockIdx.x] = make_int4(w.r.lo, w.h, w.m * kTile, rows | ways << 16);
                 else k.tails[blockIdx.x] = w.t0 + w.n == w.nt ? 2 : 1;
             }
             tc_fence_before();
@@ -1085,7 +1125,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant
         const int c = 2 * tid + i;
         items[c] = c < ctas ? k.starters[c] : make_int4(-1, 0, 0, 0);
         tails[c] = c < ctas ? k.tails[c] : 0;
-        mine[i] = items[c].x < 0 ? 0 : (items[c].w + R - 1) / R;
+        mine[i] = items[c].x < 0 ? 0 : ((items[c].w & 0xffff) + R - 1) / R;
     }
     const int pre = block_scan_ex(mine[0] + mine[1], ws, &all);
     first[2 * tid] = pre;
@@ -1100,19 +1140,20 @@ __global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant
         }
         const int4 head4 = items[c0];
         const int r = tid / (D / 4), d4 = tid % (D / 4), row = (job - first[c0]) * R + r;
-        if (row < head4.w) {
+        const int ways = head4.w >> 16;
+        if (row < (head4.w & 0xffff)) {
             // the CTAs with a part of it: up to the first that holds its end.  Sums in base 2^m of
             // the largest maximum so far
             float m = -INFINITY, l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             constexpr int U = 8;  // parts in flight
             bool end = false;
-            for (int c = c0; c < ctas && !end; c += U) {
+            for (int c = c0; c < ctas && !end; c += U * ways) {
                 float ms[U], ls[U];
                 float4 v[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int cu = c + u, cell = 2 * cu + (cu == c0 ? 1 : 0);
+                    const int cu = c + u * ways, cell = 2 * cu + (cu == c0 ? 1 : 0);
                     const bool has = !end && cu < ctas && (cu == c0 || tails[cu] != 0);
                     ms[u] = -INFINITY;
                     ls[u] = 0.0f;
@@ -1145,7 +1186,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant
                 }
             }
             constexpr float kShift = F16 ? 4.0f : 0.0f;
-            const int at = head4.z * kTile + row, t = at / p.group, head = head4.y * p.group + (at - t * p.group);
+            const int at = head4.z + row, t = at / p.group, head = head4.y * p.group + (at - t * p.group);
             const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
             uint2 u;
             u.x = pack2<F16>(o.x * inv, o.y * inv);
