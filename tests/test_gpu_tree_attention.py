@@ -252,6 +252,19 @@ def test_long_axis_split_over_the_gpu(T, L, hkv):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,L", [
+    ([64, 64, 70, 2, 33], [3000, 2500, 300, 50, 4000]),  # one to three row tiles, the second of 4 rows
+    ([0, 63, 1, 36, 36, 0], [9, 1024, 5000, 129, 0, 64]),  # the second of 16, a request before and after without rows
+    ([128], [20000]), ([64] * 40, [100 + 37 * i for i in range(40)])])
+def test_heads_of_several_row_tiles(T, L, d, dtype):
+    """Row tiles of a head that CTAs take together, and ones that are missing
+    there or small."""
+    c = make(T, L, 8, 2, d, dtype, ps=32, layout="NHD", seed=len(T) + d, qstd=1.5)
+    compare(c, run(c), causal(T))
+
+
 def test_growing_and_falling_scores():
     """Rows whose maximum moves by hundreds along the tokens, both ways."""
     c = make([2, 2], [700, 700], 2, 1, 64, torch.float16, seed=21, poison=False)
