@@ -392,7 +392,9 @@ _KV_DTYPES = {torch.bfloat16: CSGMV_DTYPE_BF16, torch.float16: CSGMV_DTYPE_F16}
 
 def _need(ok: bool, msg: str):
     """Checks that only the binding can make (a tensor's type and shape, which
-    the C ABI does not see) fail as the library's own argument checks do."""
+    the C ABI does not see) fail as the library's own argument checks do.
+    (Where a call's latency counts, a message is put together only when it is
+    raised.)"""
     if not ok:
         raise CsgmvError(-1, msg)
 
@@ -485,6 +487,7 @@ class KvCache:
         self.dtype, self.device = k_pages.dtype, k_pages.get_device()
         self.num_layers, self.num_pages, self.page_size = layers, pages, ps
         self.num_kv_heads, self.head_dim, self.max_seqs, self.max_pages_per_seq = heads, d, seqs, max_pages
+        self.row_shape = (heads, d)
 
     @classmethod
     def allocate(cls, num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
@@ -507,13 +510,14 @@ def csgmv_kv_scratch_ints(num_pages: int, max_seqs: int) -> int:
 
 def _new_rows(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, lead: tuple):
     """k_new / v_new are (*lead, kv_heads, head_dim) in the cache's type; their strides."""
-    st = k_new.stride()
-    _need(_has_shape(k_new.shape, lead + (cache.num_kv_heads, cache.head_dim)) and st[-1] == 1,
-          f"k_new / v_new must be {lead + (cache.num_kv_heads, cache.head_dim)} (the cache's layers, kv_heads and "
-          f"head_dim), the last dimension dense, not {tuple(k_new.shape)}")
-    _need(_alike(k_new, v_new), "k_new / v_new must have the same shape and strides")
-    _need(k_new.dtype is cache.dtype and v_new.dtype is cache.dtype and k_new.is_cuda and v_new.is_cuda,
-          "k_new / v_new must be CUDA tensors of the cache's type")
+    st, want = k_new.stride(), lead + cache.row_shape
+    if k_new.shape != want or st[-1] != 1:
+        raise CsgmvError(-1, f"k_new / v_new must be {want} (the cache's layers, kv_heads and head_dim), the last "
+                             f"dimension dense, not {tuple(k_new.shape)}")
+    if v_new.shape != want or v_new.stride() != st and not _alike(k_new, v_new):
+        raise CsgmvError(-1, "k_new / v_new must have the same shape and strides")
+    if not (k_new.dtype is v_new.dtype is cache.dtype and k_new.is_cuda and v_new.is_cuda):
+        raise CsgmvError(-1, "k_new / v_new must be CUDA tensors of the cache's type")
     return st
 
 
@@ -527,9 +531,11 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
     bs = accept_len.numel()
     width = 0 if accept_index is None else accept_index.shape[-1]
     _need_i32("accept_len", accept_len, bs)
-    _need_i32("accept_index", accept_index, bs, width)
+    if accept_index is not None:
+        _need_i32("accept_index", accept_index, bs, width)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
-    _need_i32("seq_slots", seq_slots, bs)
+    if seq_slots is not None:
+        _need_i32("seq_slots", seq_slots, bs)
     rc = lib().csgmv_kv_commit(cache._ref, k_new.data_ptr(), v_new.data_ptr(), st[0], st[1], st[2], k_new.shape[1],
                                _at(accept_index), width, accept_len.data_ptr(), tree_indptr.data_ptr(),
                                _at(seq_slots), bs, _raw_stream(stream, cache.device))
@@ -581,20 +587,25 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     bits, (tokens, words); None: causal) lets each row see.  scale defaults to
     head_dim ** -0.5; lse (tokens, heads) f32 is optional."""
     shape, qs, os_ = q.shape, q.stride(), out.stride()
-    _need(len(shape) == 3 and out.shape == shape, "q and out must be (tokens, heads, head_dim)")
-    _need(q.dtype is cache.dtype and out.dtype is cache.dtype and q.is_cuda and out.is_cuda,
-          "q and out must be CUDA tensors of the cache's type")
+    if len(shape) != 3 or out.shape != shape:
+        raise CsgmvError(-1, "q and out must be (tokens, heads, head_dim)")
+    if not (q.dtype is out.dtype is cache.dtype and q.is_cuda and out.is_cuda):
+        raise CsgmvError(-1, "q and out must be CUDA tensors of the cache's type")
     n, hq, d = shape
-    _need(d == cache.head_dim and (n == 0 or qs[2] == 1 and os_[2] == 1), "q and out must have the cache's head_dim, dense")
+    if d != cache.head_dim or n and (qs[2] != 1 or os_[2] != 1):
+        raise CsgmvError(-1, "q and out must have the cache's head_dim, dense")
     ks = _new_rows(cache, k_new, v_new, (n,))
-    bs = tree_indptr.numel() - 1
-    words = 0 if mask is None else mask.shape[-1]
+    bs, words = tree_indptr.shape[0] - 1 if tree_indptr.dim() else 0, 0
     _need_i32("tree_indptr", tree_indptr, bs + 1)
-    _need_i32("mask", mask, n, words)
-    _need_i32("seq_slots", seq_slots, bs)
+    if mask is not None:
+        words = mask.shape[-1]
+        _need_i32("mask", mask, n, words)
+    if seq_slots is not None:
+        _need_i32("seq_slots", seq_slots, bs)
     if lse is not None:
         _need_f32("lse", lse, n, hq)
-        _need(lse.is_contiguous(), "lse must be contiguous")
+        if not lse.is_contiguous():
+            raise CsgmvError(-1, "lse must be contiguous")
     if workspace is None:
         workspace = torch.empty(csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
     rc = lib().csgmv_tree_attention(
@@ -633,9 +644,12 @@ def csgmv_build_draft_tree(tree: DraftTree, parents: torch.Tensor, tree_indptr: 
     n, bs = parents.numel(), tree_indptr.numel() - 1
     _need_i32("parents", parents, n)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
-    _need(n <= tree.max_nodes, f"{n} nodes exceed the tree's {tree.max_nodes}")
-    _check(lib().csgmv_build_draft_tree(parents.data_ptr(), tree_indptr.data_ptr(), bs, n, tree.words, *tree._at,
-                                        _raw_stream(stream, tree.device)))
+    if n > tree.max_nodes:
+        raise CsgmvError(-1, f"{n} nodes exceed the tree's {tree.max_nodes}")
+    rc = lib().csgmv_build_draft_tree(parents.data_ptr(), tree_indptr.data_ptr(), bs, n, tree.words, *tree._at,
+                                      _raw_stream(stream, tree.device))
+    if rc:
+        _check(rc)
 
 
 def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, tree_indptr: torch.Tensor,
@@ -648,30 +662,37 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
     n, bs = draft_tokens.numel(), tree_indptr.numel() - 1
     _need_f32("target_probs", target_probs, n, None)
     ts, vocab = target_probs.stride(), target_probs.shape[1]
-    _need(n == 0 or ts[1] == 1, "target_probs must have dense rows")
+    if n and ts[1] != 1:
+        raise CsgmvError(-1, "target_probs must have dense rows")
     # the row stride of a single row says nothing
     ts, ds = ts[0] if n > 1 else vocab, 0
     if draft_probs is not None:
         _need_f32("draft_probs", draft_probs, n, vocab)
         ds = draft_probs.stride()
-        _need(n == 0 or ds[1] == 1, "draft_probs must have dense rows")
+        if n and ds[1] != 1:
+            raise CsgmvError(-1, "draft_probs must have dense rows")
         ds = ds[0] if n > 1 else vocab
     _need_i32("draft_tokens", draft_tokens, n)
     _need_i32("tree_indptr", tree_indptr, bs + 1)
     _need_f32("accept_uniforms", accept_uniforms, n)
     _need_f32("sample_uniforms", sample_uniforms, bs)
-    _need(accept_uniforms.is_contiguous() and sample_uniforms.is_contiguous(), "the uniform numbers must be contiguous")
-    _need(n <= tree.max_nodes, f"{n} nodes exceed the tree's {tree.max_nodes}")
-    # one buffer for the outputs that are not given
+    if not (accept_uniforms.is_contiguous() and sample_uniforms.is_contiguous()):
+        raise CsgmvError(-1, "the uniform numbers must be contiguous")
+    if n > tree.max_nodes:
+        raise CsgmvError(-1, f"{n} nodes exceed the tree's {tree.max_nodes}")
     width = tree.max_draft if accept_index is None else accept_index.shape[-1]
-    if accept_index is None or accept_len is None or next_token is None:
-        made = torch.empty((width + 2, bs), dtype=torch.int32, device=target_probs.device)
-        accept_index = made[:width].view(bs, width) if accept_index is None else accept_index
-        accept_len = made[width] if accept_len is None else accept_len
-        next_token = made[width + 1] if next_token is None else next_token
-    _need_i32("accept_index", accept_index, bs, width)
-    _need_i32("accept_len", accept_len, bs)
-    _need_i32("next_token", next_token, bs)
+    if accept_index is None and accept_len is None and next_token is None:  # one buffer for all
+        accept_index, accept_len, next_token = torch.empty(
+            bs * (width + 2), dtype=torch.int32, device=target_probs.device).split_with_sizes([bs * width, bs, bs])
+        accept_index = accept_index.view(bs, width)
+    else:
+        new = dict(dtype=torch.int32, device=target_probs.device)
+        accept_index = torch.empty((bs, width), **new) if accept_index is None else accept_index
+        accept_len = torch.empty(bs, **new) if accept_len is None else accept_len
+        next_token = torch.empty(bs, **new) if next_token is None else next_token
+        _need_i32("accept_index", accept_index, bs, width)
+        _need_i32("accept_len", accept_len, bs)
+        _need_i32("next_token", next_token, bs)
     rc = lib().csgmv_verify_drafts(
         target_probs.data_ptr(), ts, _at(draft_probs), ds, draft_tokens.data_ptr(), tree_indptr.data_ptr(), tree._at[2],
         tree._at[3], accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), bs, n, vocab, accept_index.data_ptr(), width,
