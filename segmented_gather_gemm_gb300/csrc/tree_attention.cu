@@ -45,8 +45,8 @@
 //
 // Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
 // keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
-// rounding, so there P goes in as a high and a low part (16 bits) in two
-// products, which the tensor core has time for.
+// rounding, so there P goes in as a high part (its upper 16 bits) and what that
+// leaves, rounded, in two products, which the tensor core has time for.
 //
 // One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, an
 // MMA warp issues S = Q K^T two tiles ahead of O += P V (three S buffers, each
@@ -1035,9 +1035,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             const float e0 = ex2(x.x), e1 = ex2(x.y);
                             const uint64_t e = two(e0, e1);
                             sum[i & 1] = add2(sum[i & 1], e);
-                            u[i] = pack2<F16>(e0, e1);
-                            if (!F16) {
-                                const float2 h = unpack_bf16x2(u[i]), r = apart(fma2(two(h.x, h.y), minus, e));
+                            if (F16) {
+                                u[i] = pack2<F16>(e0, e1);
+                            } else {
+                                const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                                u[i] = __byte_perm(b0, b1, 0x7632);
+                                const uint64_t high = two(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u));
+                                const float2 r = apart(fma2(high, minus, e));
                                 low[i] = pack2<F16>(r.x, r.y);
                             }
                         }
