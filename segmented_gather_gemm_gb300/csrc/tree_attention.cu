@@ -55,6 +55,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <map>
 #include <mutex>
 
@@ -1270,7 +1271,11 @@ template <int D, bool F16>
 cudaError_t launch(const AttnKernelParams &k, int ctas, cudaStream_t stream) {
     cudaError_t e = launch_kernel(attend<D, F16>, dim3((unsigned)ctas), kAttnThreads, Shape<D>::kSmem, stream, 0, true, k);
     if (e != cudaSuccess) return e;
-    return launch_kernel(combine<D, F16>, dim3(4 * (unsigned)ctas), kCombineThreads, 0, stream, 0, true, k, ctas);
+    // as many blocks as an SM holds at most, and no more than there are rows for
+    constexpr int R = kCombineThreads / (D / 4);
+    const int64_t jobs = ((int64_t)k.p.num_tokens * k.p.hq + R - 1) / R;
+    return launch_kernel(combine<D, F16>, dim3((unsigned)std::min<int64_t>(8 * ctas, jobs)), kCombineThreads, 0, stream, 0,
+                         true, k, ctas);
 }
 
 constexpr size_t kStarterBytes = kAttnCtas * (sizeof(int4) + sizeof(int4));  // starters, then tails
