@@ -48,9 +48,13 @@
 // rounding, so there P goes in as a high part (its upper 16 bits) and what that
 // leaves, rounded, in two products, which the tensor core has time for.
 //
-// One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, an
-// MMA warp issues S = Q K^T two tiles ahead of O += P V (three S buffers, each
-// P in its S's place), sixteen warps do the softmax from tensor memory.
+// One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, a
+// warp issues S = Q K^T up to three tiles ahead (three S buffers, each P in its
+// S's place), a warp issues O += P V, sixteen warps do the softmax from tensor
+// memory.  An MMA takes 75 to 100 clocks to issue here, whatever its size, and a
+// wait that is over 150; one warp for both products was busy 2330 clocks a tile
+// and held everything up (bfloat16, head_dim 64, 128 rows a kv head over 100003
+// and 131072 tokens: 73 us, with two warps 63.5 us).
 
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -68,8 +72,8 @@ constexpr int kTile = 128;         // rows of a row tile, tokens of a token tile
 constexpr int kGroups = kTile / 8; // 8-row groups: the unit of the shared-memory layout
 constexpr int kAttnCtas = 152;     // one CTA an SM
 constexpr int kSoftWarps = 16;
-constexpr int kWarpK = kSoftWarps, kWarpV = kSoftWarps + 1, kWarpMma = kSoftWarps + 2;
-constexpr int kAttnThreads = 32 * (kSoftWarps + 3);
+constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpO = kWarpK + 3;
+constexpr int kAttnThreads = 32 * (kSoftWarps + 4);
 constexpr int kBufs = 3;           // S buffers in tensor memory, P^T buffers in shared memory
 constexpr int kMaxRequests = 16000;  // 12 bytes each in the rings' memory
 constexpr int kCombineThreads = 128;
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         }
         return;
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpO) {
         tmem_alloc(misc, 512);
         tmem_relinquish();
     }
@@ -623,16 +627,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             }
             w = wn;
         } while (more);
-    } else if (warp == kWarpMma) {
-        // --------------------------------------------------------- products
+    } else if (warp == kWarpS) {
+        // ------------------------------------------------ products: S = Q K^T
         const uint32_t lead = elect_lead();
-        const uint32_t id_pv = idesc16(F16, kTile, D, false, true), id_pv_few = idesc16(F16, kTile, 32, true, true),
-                       id_few = idesc16(F16, kTile, 16, false, false);
-        const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes),
-                       v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes),
-                       p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
+        const uint32_t id_few = idesc16(F16, kTile, 16, false, false);
+        const uint64_t q_d = smem_desc(smem_u32(q_s), 16, S::kGroupBytes), k_d = smem_desc(smem_u32(k_ring), 16, S::kGroupBytes);
         int it = 0, item = 0;
-        int wide = -1;  // the last tile that was not turned over
         Walk w = w0;
         bool more;
         do {
@@ -640,17 +640,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             more = wn.next(p, ways);
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
-            auto steps_of = [&](int t) { return (min(kGroups, gall - t * kGroups) + 1) >> 1; };  // of 16 tokens
-            auto scores = [&](int t, int i) {
-                const int s = i % S::kSlots, buf = i % kBufs;
-                // The softmax has read what the buffer held; but P may lie there (turned over it
-                // does not) until its product is done.
-                if (i >= kBufs && (!few || i - kBufs <= wide))
-                    mbar_wait(&pv_done[buf], ((i / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
-                mbar_wait(&k_full[s], (i / S::kSlots) & 1, p.status, kKvStatusTimeout);
+            mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
+            for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
+                const int s = it % S::kSlots, buf = it % kBufs;
+                // what the buffer held has been read, and P that lay in its place multiplied
+                if (it >= kBufs) mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
+                mbar_wait(&k_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t id = idesc16(F16, kTile, 16 * steps_of(t), false, false), dst = tmem + buf * 128;
+                const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
+                const uint32_t id = idesc16(F16, kTile, 16 * steps, false, false), dst = tmem + buf * 128;
                 const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
                 if (few) {
 #pragma unroll
@@ -667,28 +666,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 }
                 commit_one(lead, &k_empty[s]);
                 commit_one(lead, &s_full[buf]);
-            };
-            mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
-            __syncwarp();
-            tc_fence_after();
-            scores(w.t0, it);
-            if (w.n > 1) scores(w.t0 + 1, it + 1);
-            for (int j = 0; j < w.n; ++j, ++it) {
-                if (j + 2 < w.n) scores(w.t0 + j + 2, it + 2);
+            }
+            ++item;
+            w = wn;
+        } while (more);
+    } else if (warp == kWarpO) {
+        // ------------------------------------------------ products: O += P V
+        const uint32_t lead = elect_lead();
+        const uint32_t id_pv = idesc16(F16, kTile, D, false, true), id_few = idesc16(F16, kTile, 32, true, true);
+        const uint64_t v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes), p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
+        int it = 0;
+        Walk w = w0;
+        bool more;
+        do {
+            Walk wn = w;
+            more = wn.next(p, ways);
+            const int gall = w.r.groups();
+            const bool few = w.rows(p) <= kFewRows;
+            for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
                 const int s = it % S::kSlots, buf = it % kBufs;
                 mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
                 mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
-                const int steps = steps_of(w.t0 + j);
+                const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
                 const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4), pd = p_d + (uint32_t)(buf * 8192 >> 4);
                 const uint32_t pt = tmem + buf * 128;
+                const bool add = t > w.t0;
                 if (few) {
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         if (x < steps)
                             mma_ss(lead, t_o, vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4), pd + (uint32_t)(x * 1024 >> 4),
-                                   id_pv_few, j > 0 || x > 0);
+                                   id_few, add || x > 0);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
@@ -696,7 +706,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             // P of 32 tokens lies in 16 columns, its low parts in the next 16
                             const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
                             const uint32_t a = pt + (x / 2) * 32 + (x % 2) * 8;
-                            mma_ts(lead, t_o, a, d, id_pv, j > 0 || x > 0);
+                            mma_ts(lead, t_o, a, d, id_pv, add || x > 0);
                             if (!F16) mma_ts(lead, t_o, a + 16, d, id_pv, true);
                         }
                     }
@@ -704,8 +714,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 commit_one(lead, &v_empty[s]);
                 commit_one(lead, &pv_done[buf]);
             }
-            if (!few) wide = it - 1;
-            ++item;
             w = wn;
         } while (more);
     } else {
@@ -1107,7 +1115,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     __syncwarp();
-    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    if (warp == kWarpO) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of the items that the axis' cuts went through, in order of
