@@ -21,9 +21,11 @@
 //
 // More rows.  The exponentials of a full tile take an SM 512 clocks, all of the
 // softmax's instructions some 800; what costs is the latency of its steps (read
-// S, agree on the maximum, exponentials, store P).  So sixteen warps share it,
-// 32 tokens of 32 rows each, and only when some score passes its row's maximum
-// by 2^8 do the four warps of a quadrant exchange maxima.
+// S, find the maximum, exponentials, store P).  A warp has 16 rows: four threads
+// share a row, and no warp waits for another.  (Sixteen warps of 32 rows by 32
+// tokens, agreeing on a row's maximum through shared memory, stayed in step
+// with one another: 1950 clocks a tile in half, 2250 in bfloat16, against 1570
+// and 1770.)
 //
 // Split.  The tiles of all (request, kv head, row tile) items form one axis
 // that is cut into parts of equal cost (cost_of below), one a CTA (one CTA an
@@ -50,7 +52,7 @@
 //
 // One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, a
 // warp issues S = Q K^T up to three tiles ahead (three S buffers, each P in its
-// S's place), a warp issues O += P V, sixteen warps do the softmax from tensor
+// S's place), a warp issues O += P V, eight warps do the softmax from tensor
 // memory.  An MMA takes 75 to 100 clocks to issue here, whatever its size, and a
 // wait that is over 150; one warp for both products was busy 2330 clocks a tile
 // and held everything up (bfloat16, head_dim 64, 128 rows a kv head over 100003
@@ -71,7 +73,7 @@ namespace {
 constexpr int kTile = 128;         // rows of a row tile, tokens of a token tile
 constexpr int kGroups = kTile / 8; // 8-row groups: the unit of the shared-memory layout
 constexpr int kAttnCtas = 152;     // one CTA an SM
-constexpr int kSoftWarps = 16;
+constexpr int kSoftWarps = 8;
 constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpO = kWarpK + 3;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 4);
 constexpr int kBufs = 3;           // S buffers in tensor memory, P^T buffers in shared memory
@@ -89,8 +91,8 @@ struct Shape {
     static constexpr int kRing = 2 * kSlots * kTileBytes;
     static constexpr int kBars = 4 * kSlots + 3 * kBufs + 1;
     static constexpr int kQBytes = 32768;               // Q, or 16 rows of it and P^T
-    static constexpr int kRedBytes = 4 * kTile * 4;     // maxima or sums of a row's quarters
-    static constexpr int kFlagBytes = 2 * 16 * 4;       // a warp's flag, by turns
+    static constexpr int kRedBytes = 3 * kTile * 4;     // a row's maximum and sum; the same turned over, by warps
+    static constexpr int kFlagBytes = 2 * 8 * 4;       // a warp's flag, by turns
     static constexpr int kSmem = kQBytes + kRing + kRedBytes + kFlagBytes + (kBars + 1) * 8 + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -198,9 +200,70 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// Tensor memory, 8 columns of 32 lanes: a thread has a lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+// 16 lanes, 8 columns a step i: thread z has columns 8 i + 2 (z & 3) and the one
+// after of lanes z / 4 (v[4 i], v[4 i + 1]) and 8 + z / 4 (v[4 i + 2], v[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_rows128(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_rows64(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_rows64(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
@@ -208,52 +271,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// 16 lanes, 4 columns a step i: column 4 i + (z & 3) of the same two lanes.
+__device__ __forceinline__ void tmem_st_rows64x1(uint32_t taddr, const uint32_t (&v)[32]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-            taddr),
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
-    uint32_t r[4];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 32) tmem_ld32(taddr, v);
-    else tmem_ld16(taddr, v);
-}
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[N]) {
-    if constexpr (N == 32) tmem_st32(taddr, v);
-    else tmem_st16(taddr, v);
 }
 
 template <bool F16>
@@ -318,7 +346,7 @@ constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 // share of HBM, half of that when two CTAs read them together (of head_dim 64 in
 // less than the softmax takes); its softmax takes 1000 clocks turned over,
 // otherwise 1400 (half) or 1800 (bfloat16).  Beginning and ending an item costs
-// 800 turned over, 5800 otherwise.  With equal tile counts instead, the CTAs of
+// 2500 turned over, 12800 otherwise.  With equal tile counts instead, the CTAs of
 // short sequences ran 15 to 30 % longer than the others.
 struct Cost {
     int mi, nt;          // items and token tiles
@@ -329,7 +357,7 @@ __device__ __forceinline__ int tile_cost(int rows, bool shared, int d, bool f16)
     const int bytes = (d == 128 ? 45 : 16) >> (int)shared;
     return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 28);
 }
-__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 12 : 90; }
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 40 : 200; }
 __device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p, int ways) {
     Cost c;
     const Req r = {0, T, L, 0};
@@ -703,11 +731,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         if (x < steps) {
-                            // P of 32 tokens lies in 16 columns, its low parts in the next 16
+                            // P lies in 64 columns, its low parts in the next 64
                             const uint64_t d = vd + (uint32_t)(x * 2 * S::kGroupBytes >> 4);
-                            const uint32_t a = pt + (x / 2) * 32 + (x % 2) * 8;
-                            mma_ts(lead, t_o, a, d, id_pv, add || x > 0);
-                            if (!F16) mma_ts(lead, t_o, a + 16, d, id_pv, true);
+                            mma_ts(lead, t_o, pt + 8 * x, d, id_pv, add || x > 0);
+                            if (!F16) mma_ts(lead, t_o, pt + 64 + 8 * x, d, id_pv, true);
                         }
                     }
                 }
@@ -718,8 +745,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         } while (more);
     } else {
         // ---------------------------------------------------------- softmax
-        // warps w, w + 4, w + 8 and w + 12 share 32 lanes (a quadrant): each has a quarter of the work on them
-        const int quad = warp & 3, quarter = warp >> 2, pos = quad * 32 + lane;
+        // warps w and w + 4 share 32 lanes (a quadrant)
+        const int quad = warp & 3, half = warp >> 2, pos = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const float c = p.scale * kLog2e;
         constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
@@ -727,9 +754,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         Walk w = w0;
         bool more;
 
-        // Q of a segment: from memory, and into the swizzled tile.  A thread has a
-        // quarter of a row; 16 bytes when the products are turned over.
-        uint4 qv[D / 32];
+        // Q of a segment: from memory, and into the swizzled tile.  A thread has half
+        // a row; 16 bytes when the products are turned over.
+        uint4 qv[D / 16];
         auto q_src = [&](const Walk &u, int row, int el) {
             const int at = u.m * kTile + row, t = at / p.group;
             return p.q + (int64_t)(u.r.lo + t) * p.q_ts + (u.h * p.group + (at - t * p.group)) * p.q_hs + el;
@@ -740,9 +767,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 const int row = tid / (D / 8), el = (tid % (D / 8)) * 8;
                 if (row < rows) qv[0] = ldg16(q_src(u, row, el));
             } else if (pos < rows) {
-                const uint16_t *src = q_src(u, pos, quarter * (D / 4));
+                const uint16_t *src = q_src(u, pos, half * (D / 2));
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) qv[x] = ldg16(src + x * 8);
+                for (int x = 0; x < D / 16; ++x) qv[x] = ldg16(src + x * 8);
             }
         };
         auto q_put = [&](int row, int chunk, uint4 v) {
@@ -757,7 +784,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (row < rows) q_put(row, tid % (D / 8), qv[0]);
             } else if (pos < rows) {
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) q_put(pos, quarter * (D / 32) + x, qv[x]);
+                for (int x = 0; x < D / 16; ++x) q_put(pos, half * (D / 16) + x, qv[x]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -821,15 +848,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[it % kBufs]);
             };
-            // Whether any of the four warps that share maxima (a quadrant, or a turned-over row group:
-            // barriers 1 .. 4 and 5 .. 8, never one for both) has a score past its maximum's leeway.
-            auto any_grows = [&](bool grow, int id, int *flags, int mine) {
-                const bool any = __any_sync(kFullMask, grow);
-                if (lane == 0) flags[(it & 1) * 16 + mine] = any;
-                named_bar_sync(id, 128);
-                const int4 f = *reinterpret_cast<const int4 *>(flags + (it & 1) * 16 + (mine & ~3));
-                return (f.x | f.y | f.z | f.w) != 0;
-            };
             // What row t sees of the drafted tokens' non-finite values, from element el on.
             auto add_odd = [&](int t, int el, auto &o) {
                 constexpr int N = sizeof(o) / sizeof(float);
@@ -856,17 +874,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 
             if (few) {
                 // ------------------------------------------- turned over
-                // a thread has token `pos` and rows 4 quarter .. 4 quarter + 3, of which nl are real
-                const int nl = min(4, rows - 4 * quarter);
-                float m[4], l[4];
+                // a thread has token `pos` and rows 8 half .. 8 half + 7, of which nl are real
+                const int nl = min(8, rows - 8 * half);
+                float m[8], l[8];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+                for (int r = 0; r < 8; ++r) m[r] = -INFINITY, l[r] = 0.0f;
                 for (int j = 0; j < w.n; ++j, ++it) {
                     const int t = w.t0 + j, buf = it % kBufs;
                     await_s();
                     if (nl > 0) {
-                        float s[4];
-                        tmem_ld4(tmem + buf * 128 + lane_base + 4 * quarter, s);
+                        float s[8];
+                        tmem_ld8(tmem + buf * 128 + lane_base + 8 * half, s);
                         uint32_t see = (1u << nl) - 1u;
                         const int vk = t * kTile + pos;
                         if (vk >= w.r.L) {
@@ -874,30 +892,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             uint32_t bits = 0;
                             if (jt >= 0 && jt < w.r.T)
                                 for (int r = 0; r < nl; ++r)
-                                    bits |= (tree_word(p, w.r, (w.m * kTile + 4 * quarter + r) / p.group, jt) & 1u) << r;
+                                    bits |= (tree_word(p, w.r, (w.m * kTile + 8 * half + r) / p.group, jt) & 1u) << r;
                             see &= bits;
                         }
                         __syncwarp();
                         bool grow = false;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
+                        for (int r = 0; r < 8; ++r) {
                             s[r] = (see >> r) & 1 ? s[r] : -INFINITY;
                             grow |= s[r] * c > m[r] + kLazy;  // from -inf: any score at all
                         }
-                        if (any_grows(grow, 5 + quarter, flag_s, quarter * 4 + quad)) {
-                            float *mx = red_s + quarter * kTile;  // [quadrant][row]
+                        // whether any of the half's four warps has a score past its maximum's leeway
+                        const bool mine = __any_sync(kFullMask, grow);
+                        int *flags = flag_s + (it & 1) * 8 + half * 4;
+                        if (lane == 0) flags[quad] = mine;
+                        named_bar_sync(5 + half, 128);
+                        const int4 any = *reinterpret_cast<const int4 *>(flags);
+                        if (any.x | any.y | any.z | any.w) {
+                            float *mx = red_s + 2 * kTile + half * 64;  // [quadrant][row]
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
+                            for (int r = 0; r < 8; ++r) {
                                 float x = s[r] * c;
 #pragma unroll
                                 for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFullMask, x, o));
-                                if (lane == 0) mx[quad * 4 + r] = x;
+                                if (lane == 0) mx[quad * 8 + r] = x;
                             }
-                            named_bar_sync(5 + quarter, 128);
-                            float f[4];
+                            named_bar_sync(5 + half, 128);
+                            float f[8];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float x = fmaxf(fmaxf(mx[r], mx[4 + r]), fmaxf(mx[8 + r], mx[12 + r]));
+                            for (int r = 0; r < 8; ++r) {
+                                const float x = fmaxf(fmaxf(mx[r], mx[8 + r]), fmaxf(mx[16 + r], mx[24 + r]));
                                 const float mn = x > m[r] + kLazy ? x : m[r];
                                 f[r] = mn > m[r] ? ex2(m[r] - mn) : 1.0f;
                                 m[r] = mn;
@@ -907,20 +931,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                 await_pv();
 #pragma unroll
                                 for (int part = 0; part < 2; ++part) {
-                                    const uint32_t a = t_o + lane_base + part * 16 + quarter * 4;
-                                    float o[4];
-                                    uint32_t u[4];
-                                    tmem_ld4(a, o);
+                                    const uint32_t a = t_o + lane_base + part * 16 + half * 8;
+                                    float o[8];
+                                    uint32_t u[8];
+                                    tmem_ld8(a, o);
 #pragma unroll
-                                    for (int r = 0; r < 4; ++r) u[r] = __float_as_uint(o[r] * f[r]);
-                                    tmem_st4(a, u);
+                                    for (int r = 0; r < 8; ++r) u[r] = __float_as_uint(o[r] * f[r]);
+                                    tmem_st8(a, u);
                                 }
                                 tmem_wait_st();
                             }
                         }
-                        uint32_t hi[2], low[2];
+                        uint32_t hi[4], low[4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             float e[2];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
@@ -934,12 +958,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         if (it >= kBufs)  // the product before in this buffer
                             mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
                         // P^T: 64 bytes a token, high parts of 16 rows, then the low parts; 64-byte swizzle
-                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64 + (quarter & 1) * 8, x = (pos >> 1) & 3;
-                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a + (((quarter >> 1) ^ x) << 4)), "r"(hi[0]),
-                                     "r"(hi[1])
+                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + ((half ^ x) << 4)), "r"(hi[0]), "r"(hi[1]),
+                                     "r"(hi[2]), "r"(hi[3])
                                      : "memory");
-                        asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a + (((2 + (quarter >> 1)) ^ x) << 4)), "r"(low[0]),
-                                     "r"(low[1])
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + (((2 + half) ^ x) << 4)), "r"(low[0]),
+                                     "r"(low[1]), "r"(low[2]), "r"(low[3])
                                      : "memory");
                     }
                     if (edge(t)) clean_v(t);
@@ -950,29 +974,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 const bool early = more && wn.rows(p) <= kFewRows;
                 if (more) q_load(wn);
                 if (nl > 0) {
-                    float *sum = red_s + quarter * kTile + 16;  // [quadrant][row], beside the maxima
+                    float *sum = red_s + 2 * kTile + half * 64 + 32;  // [quadrant][row], beside the maxima
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         l[r] = warp_sum(l[r]);
-                        if (lane == 0) sum[quad * 4 + r] = l[r];
+                        if (lane == 0) sum[quad * 8 + r] = l[r];
                     }
-                    named_bar_sync(5 + quarter, 128);
+                    named_bar_sync(5 + half, 128);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) l[r] = (sum[r] + sum[4 + r]) + (sum[8 + r] + sum[12 + r]);
+                    for (int r = 0; r < 8; ++r) l[r] = (sum[r] + sum[8 + r]) + (sum[16 + r] + sum[24 + r]);
                 }
                 if (early) q_store(wn);
                 await_pv();
                 if (nl > 0) {
-                    float o[4], low[4];
-                    tmem_ld4(t_o + lane_base + quarter * 4, o);
-                    tmem_ld4(t_o + lane_base + 16 + quarter * 4, low);
+                    float o[8], low[8];
+                    tmem_ld8(t_o + lane_base + half * 8, o);
+                    tmem_ld8(t_o + lane_base + 16 + half * 8, low);
                     if (pos < D) {  // a thread has element `pos`
                         const bool odd = *odd_item == item;
                         float *part = k.part + ((int64_t)cell * (D / 4) + pos / 4) * kTile * 4 + (pos & 3);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
+                        for (int r = 0; r < 8; ++r) {
                             if (r < nl) {
-                                const int row = 4 * quarter + r, at = w.m * kTile + row, tr = at / p.group;
+                                const int row = 8 * half + r, at = w.m * kTile + row, tr = at / p.group;
                                 float x[1] = {o[r] + low[r]};
                                 if (odd) add_odd(tr, pos, x);
                                 if (whole)
@@ -987,60 +1011,86 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (more && !early) q_store(wn);
             } else {
                 // ------------------------------------------------- as is
-                // a thread has a row, and a quarter of every tile's tokens (and of O's columns)
-                const bool live = pos < rows, warp_live = quad * 32 < rows;
-                const int at = w.m * kTile + pos, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
-                float m = -INFINITY, l = 0.0f;  // base 2, and without kShift in m; l of this quarter
+                // a warp has 16 rows, a thread two of them: elements 2 z, 2 z + 1 of every 8 tokens
+                // (z its number in the four that share the rows)
+                const int row0 = quad * 32 + half * 16 + lane / 4, z = lane & 3;
+                const bool warp_live = quad * 32 + half * 16 < rows;
+                const uint32_t lanes = (uint32_t)(quad * 32 + half * 16) << 16;
+                const bool live[2] = {row0 < rows, row0 + 8 < rows};
+                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // base 2, m without kShift; l of this thread's tokens
                 for (int j = 0; j < w.n; ++j, ++it) {
                     const int t = w.t0 + j;
                     await_s();
                     if (warp_live) {
-                        const uint32_t t_s = tmem + (it % kBufs) * 128 + lane_base + quarter * 32;
-                        float s[32];
-                        tmem_ld32(t_s, s);
+                        const uint32_t t_s = tmem + (it % kBufs) * 128 + lanes;
+                        float s[64];
+                        tmem_ld_rows128(t_s, s);
                         if (edge(t)) {
-                            const int k0 = t * kTile + quarter * 32, n = w.r.L - k0;
-                            uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-                            if (live) bits |= tree_word(p, w.r, t_row, k0 - gctx * 8);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1 ? s[i] : -INFINITY;
-                        }
-                        __syncwarp();
-                        float mx[2] = {s[0], s[1]};
+                            for (int r = 0; r < 2; ++r) {
+                                const int tr = (w.m * kTile + row0 + 8 * r) / p.group;
 #pragma unroll
-                        for (int i = 2; i < 30; i += 4) {
-                            mx[0] = max3(mx[0], s[i], s[i + 1]);
-                            mx[1] = max3(mx[1], s[i + 2], s[i + 3]);
-                        }
-                        float top = fmaxf(max3(mx[0], s[30], s[31]), mx[1]) * c;
-                        // from -inf: any score at all
-                        if (any_grows(live && top > m + kLazy, 1 + quad, flag_s, quad * 4 + quarter)) {
-                            red_s[quarter * kTile + pos] = top;
-                            named_bar_sync(1 + quad, 128);
-                            top = fmaxf(fmaxf(red_s[pos], red_s[kTile + pos]), fmaxf(red_s[2 * kTile + pos], red_s[3 * kTile + pos]));
-                            const bool grow = live && top > m + kLazy;
-                            const float mn = grow ? top : m;
-                            if (j > 0) {  // O so far, in units of 2^m: this warp's quarter of its columns
-                                const float f = grow ? ex2(m - mn) : 1.0f;  // m = -inf: 0
-                                await_pv();
-                                float o[D / 4];
-                                uint32_t u[D / 4];
-                                const uint32_t a = t_o + lane_base + quarter * (D / 4);
-                                tmem_load(a, o);
+                                for (int q = 0; q < 4; ++q) {
+                                    const int k0 = t * kTile + 32 * q, n = w.r.L - k0;
+                                    uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+                                    if (live[r]) bits |= tree_word(p, w.r, tr, k0 - gctx * 8);
+                                    bits >>= 2 * z;
 #pragma unroll
-                                for (int i = 0; i < D / 4; ++i) u[i] = __float_as_uint(o[i] * f);
-                                tmem_store(a, u);
-                                l *= f;
+                                    for (int i = 0; i < 8; ++i) {
+                                        float &x = s[16 * q + 4 * (i / 2) + 2 * r + i % 2];
+                                        x = (bits >> (8 * (i / 2) + i % 2)) & 1 ? x : -INFINITY;
+                                    }
+                                }
                             }
-                            m = mn;
+                            __syncwarp();
                         }
-                        const float base = m == -INFINITY ? 0.0f : kShift - m;
-                        const uint64_t c2 = two(c, c), base2 = two(base, base), minus = two(-1.0f, -1.0f);
-                        uint64_t sum[2] = {0, 0};
-                        uint32_t u[16], low[16];
+                        float top[2];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = apart(fma2(two(s[2 * i], s[2 * i + 1]), c2, base2));
+                        for (int r = 0; r < 2; ++r) {
+                            float mx[2] = {s[2 * r], s[2 * r + 1]};
+#pragma unroll
+                            for (int i = 1; i < 15; i += 2) {
+                                mx[0] = max3(mx[0], s[4 * i + 2 * r], s[4 * i + 2 * r + 1]);
+                                mx[1] = max3(mx[1], s[4 * i + 4 + 2 * r], s[4 * i + 4 + 2 * r + 1]);
+                            }
+                            float x = fmaxf(max3(mx[0], s[60 + 2 * r], s[60 + 2 * r + 1]), mx[1]);
+                            x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 1));
+                            top[r] = fmaxf(x, __shfl_xor_sync(kFullMask, x, 2)) * c;
+                        }
+                        // from -inf: any score at all
+                        const bool grow[2] = {live[0] && top[0] > m[0] + kLazy, live[1] && top[1] > m[1] + kLazy};
+                        if (__any_sync(kFullMask, grow[0] || grow[1])) {
+                            float f[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                f[r] = grow[r] ? ex2(m[r] - top[r]) : 1.0f;  // m = -inf: 0
+                                m[r] = grow[r] ? top[r] : m[r];
+                                l[r] *= f[r];
+                            }
+                            if (j > 0) {  // O so far, in units of 2^m
+                                await_pv();
+#pragma unroll
+                                for (int h = 0; h < D / 64; ++h) {
+                                    float o[32];
+                                    uint32_t u[32];
+                                    tmem_ld_rows64(t_o + lanes + 64 * h, o);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f[(i / 2) & 1]);
+                                    tmem_st_rows64(t_o + lanes + 64 * h, u);
+                                }
+                            }
+                        }
+                        const uint64_t c2 = two(c, c), minus = two(-1.0f, -1.0f);
+                        uint64_t base2[2], sum[2] = {0, 0};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float base = m[r] == -INFINITY ? 0.0f : kShift - m[r];
+                            base2[r] = two(base, base);
+                        }
+                        uint32_t u[32], low[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 x = apart(fma2(two(s[2 * i], s[2 * i + 1]), c2, base2[i & 1]));
                             const float e0 = ex2(x.x), e1 = ex2(x.y);
                             const uint64_t e = two(e0, e1);
                             sum[i & 1] = add2(sum[i & 1], e);
@@ -1054,52 +1104,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                 low[i] = pack2<F16>(r.x, r.y);
                             }
                         }
-                        tmem_st16(t_s, u);
-                        if (!F16) tmem_st16(t_s + 16, low);
-                        const float2 both = apart(add2(sum[0], sum[1]));
-                        l += both.x + both.y;
+                        tmem_st_rows64x1(t_s, u);
+                        if (!F16) tmem_st_rows64x1(t_s + 64, low);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float2 both = apart(sum[r]);
+                            l[r] += both.x + both.y;
+                        }
                         tmem_wait_st();
                     }
                     if (edge(t)) clean_v(t);
                     p_is_ready();
                 }
                 // Q of the next segment: its products with this one's Q are done
-                if (more) q_load(wn);
-                if (warp_live) {
-                    named_bar_sync(1 + quad, 128);  // (the maxima have been read)
-                    red_s[quarter * kTile + pos] = l;
-                    named_bar_sync(1 + quad, 128);
-                    l = (red_s[pos] + red_s[kTile + pos]) + (red_s[2 * kTile + pos] + red_s[3 * kTile + pos]);
+                if (more) {
+                    q_load(wn);
+                    q_store(wn);
                 }
-                if (more) q_store(wn);
+                // From here a thread has a row, and half of O's columns.  (All warps have ended the item
+                // before when the last product of this one is done: red_s can be written.)
                 await_pv();
-                if (warp_live) {
-                    const bool odd = *odd_item == item;
-                    const float inv = inverse(l);
-                    const int el = quarter * (D / 4);
-                    float o[D / 4];
-                    tmem_load(t_o + lane_base + el, o);
-                    if (live) {
-                        if (odd) add_odd(t_row, el, o);
-                        if (whole) {
-                            uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs + el;
+                if (quad * 32 < rows) {
 #pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint4 v;
-                                v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
-                                v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                                v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                                v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-                                *reinterpret_cast<uint4 *>(dst + i * 8) = v;
-                            }
-                        } else {
-                            float4 *part = reinterpret_cast<float4 *>(k.part) + ((int64_t)cell * (D / 4) + el / 4) * kTile + pos;
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i)
-                                part[i * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int r = 0; r < 2; ++r) {
+                        l[r] += __shfl_xor_sync(kFullMask, l[r], 1);
+                        l[r] += __shfl_xor_sync(kFullMask, l[r], 2);
+                        if (z == 0) {
+                            red_s[row0 + 8 * r] = m[r];
+                            red_s[kTile + row0 + 8 * r] = l[r];
                         }
-                        if (quarter == 0) put_row(pos, m, l);
                     }
+                    named_bar_sync(1 + quad, 64);
+                    const bool odd = *odd_item == item;
+                    const float mr = red_s[pos], lr = red_s[kTile + pos], inv = inverse(lr);
+                    const int at = w.m * kTile + pos, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        const int el = half * (D / 2) + 32 * h;
+                        float o[32];
+                        tmem_ld32(t_o + lane_base + el, o);
+                        if (pos < rows) {
+                            if (odd) add_odd(t_row, el, o);
+                            if (whole) {
+                                uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs + el;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    uint4 v;
+                                    v.x = pack2<F16>(o[8 * i] * inv, o[8 * i + 1] * inv);
+                                    v.y = pack2<F16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                                    v.z = pack2<F16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                                    v.w = pack2<F16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                                    *reinterpret_cast<uint4 *>(dst + i * 8) = v;
+                                }
+                            } else {
+                                float4 *part = reinterpret_cast<float4 *>(k.part) + ((int64_t)cell * (D / 4) + el / 4) * kTile + pos;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    part[i * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (pos < rows && half == 0) put_row(pos, mr, lr);
                 }
             }
             if (tid == 0 && !whole) {
