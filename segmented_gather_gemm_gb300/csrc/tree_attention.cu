@@ -77,7 +77,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpO = kWarpK + 3;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 4);
 constexpr int kBufs = 3;           // S buffers in tensor memory, P^T buffers in shared memory
-constexpr int kMaxRequests = 16000;  // 12 bytes each in the rings' memory
+constexpr int kMaxRequests = 16000;  // 12 bytes each in the tiles' memory
 constexpr int kCombineThreads = 128;
 constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
 constexpr float kLog2e = 1.4426950408889634f;
@@ -87,14 +87,17 @@ struct Shape {
     static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
     static constexpr int kGroupBytes = kHalves * 1024; // 8 rows
     static constexpr int kTileBytes = kGroups * kGroupBytes;
-    static constexpr int kSlots = D == 128 ? 3 : 6;    // of each ring
-    static constexpr int kRing = 2 * kSlots * kTileBytes;
-    static constexpr int kBars = 4 * kSlots + 3 * kBufs + 1;
-    static constexpr int kQBytes = 32768;               // Q, or 16 rows of it and P^T
+    static constexpr int kSlotsK = D == 128 ? 2 : 5, kSlotsV = D == 128 ? 3 : 5;  // of the rings
+    static constexpr int kRings = (kSlotsK + kSlotsV) * kTileBytes;
+    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1;
+    static constexpr int kQBytes = 32768;               // Q of an item, or 16 rows of it and P^T
+    static constexpr int kTiles = 2 * kQBytes + kRings;  // Q of two items, and the rings
+    static_assert(kTileBytes <= kQBytes && 8192 + kBufs * 8192 <= kQBytes, "Q and P^T");
     static constexpr int kRedBytes = 3 * kTile * 4;     // a row's maximum and sum; the same turned over, by warps
     static constexpr int kFlagBytes = 2 * 8 * 4;       // a warp's flag, by turns
-    static constexpr int kSmem = kQBytes + kRing + kRedBytes + kFlagBytes + (kBars + 1) * 8 + 64;
+    static constexpr int kSmem = kTiles + kRedBytes + kFlagBytes + (kBars + 1) * 8 + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(512 + 12 * kMaxRequests + 32 <= kTiles, "what the axis is cut by");
 };
 
 struct AttnMaps {
@@ -355,9 +358,9 @@ struct Cost {
 };
 __device__ __forceinline__ int tile_cost(int rows, bool shared, int d, bool f16) {
     const int bytes = (d == 128 ? 45 : 16) >> (int)shared;
-    return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 28);
+    return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 26);
 }
-__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 40 : 200; }
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 100 : 200; }
 __device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p, int ways) {
     Cost c;
     const Req r = {0, T, L, 0};
@@ -418,21 +421,19 @@ struct Walk {
 // 32 bits of row t's mask from drafted token j0 (which may be negative: lower
 // bits are then 0), cut at T.
 __device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r, int t, int j0) {
-    if (j0 <= -32 || j0 >= r.T) return 0;
     uint32_t x;
-    const int a = max(j0, 0);
+    const int a = max(j0, 0), w = a >> 5;
     if (p.mask) {
         const int32_t *row = p.mask + (int64_t)(r.lo + t) * p.mask_words;
-        const int w = a >> 5;
-        const uint32_t w0 = (uint32_t)row[w], w1 = w + 1 < p.mask_words ? (uint32_t)row[w + 1] : 0u;
+        const uint32_t w0 = w < p.mask_words ? (uint32_t)row[w] : 0u, w1 = w + 1 < p.mask_words ? (uint32_t)row[w + 1] : 0u;
         x = __funnelshift_r(w0, w1, a & 31);
     } else {
         const int n = t + 1 - a;
         x = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
     }
-    if (j0 < 0) x <<= -j0;
+    if (j0 < 0) x = j0 > -32 ? x << -j0 : 0u;
     const int lim = r.T - j0;
-    return lim >= 32 ? x : x & ((1u << lim) - 1u);
+    return lim >= 32 ? x : lim <= 0 ? 0u : x & ((1u << lim) - 1u);
 }
 
 // The place x units of cost along the axis (every CTA rounds it alike).
@@ -468,17 +469,40 @@ __device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead,
     return q;
 }
 
+// Q of an item into its swizzled tile, by `threads` threads (a multiple of
+// D / 8) of which this is thread `i`: each has one 16-byte column.
+template <int D>
+__device__ __forceinline__ void fetch_q(const AttnParams &p, const Walk &w, unsigned char *q_s, int i, int threads) {
+    const int rows = w.rows(p), chunk = i % (D / 8), step = threads / (D / 8);
+    int row = i / (D / 8), t = (w.m * kTile + row) / p.group, g = w.m * kTile + row - t * p.group;
+    const uint16_t *src = p.q + (int64_t)(w.r.lo + t) * p.q_ts + (w.h * p.group + g) * p.q_hs + chunk * 8;
+    for (; row < rows; row += step) {
+        cp_async16(q_s + (row >> 3) * Shape<D>::kGroupBytes + (row & 7) * 128 + (chunk >> 3) * 1024 + (((chunk & 7) ^ (row & 7)) << 4),
+                   src, 16);
+        g += step;
+        src += step * p.q_hs;
+        while (g >= p.group) {  // the next token
+            g -= p.group;
+            src += p.q_ts - p.group * p.q_hs;
+        }
+    }
+}
+__device__ __forceinline__ void q_landed() {
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    fence_proxy_async_smem();
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant__ AttnKernelParams k) {
     using S = Shape<D>;
     const AttnParams &p = k.p;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *q_s = smem, *k_ring = smem + S::kQBytes, *v_ring = k_ring + S::kSlots * S::kTileBytes;
-    float *red_s = reinterpret_cast<float *>(k_ring + S::kRing);
-    int *flag_s = reinterpret_cast<int *>(k_ring + S::kRing + S::kRedBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(k_ring + S::kRing + S::kRedBytes + S::kFlagBytes);
-    uint64_t *k_full = bars, *k_empty = k_full + S::kSlots, *v_full = k_empty + S::kSlots, *v_empty = v_full + S::kSlots,
-             *s_full = v_empty + S::kSlots, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
+    unsigned char *q_s = smem, *k_ring = q_s + 2 * S::kQBytes, *v_ring = k_ring + S::kSlotsK * S::kTileBytes;
+    float *red_s = reinterpret_cast<float *>(smem + S::kTiles);
+    int *flag_s = reinterpret_cast<int *>(smem + S::kTiles + S::kRedBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
+    uint64_t *k_full = bars, *k_empty = k_full + S::kSlotsK, *v_full = k_empty + S::kSlotsK, *v_empty = v_full + S::kSlotsV,
+             *s_full = v_empty + S::kSlotsV, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
              *q_ready = pv_done + kBufs;
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
@@ -497,12 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
+        for (int i = 0; i < 2 * (S::kSlotsK + S::kSlotsV); ++i) mbar_init(&bars[i], 1);
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], kSoftWarps);
@@ -513,14 +532,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         *odd_item = -1;
     }
     griddep_wait();
-    // The axis: cost ahead of each request, and its T and L, in the rings' memory.
-    int *ahead = reinterpret_cast<int *>(k_ring);
-    int2 *tl = reinterpret_cast<int2 *>(k_ring + ((4 * p.bs + 4 + 15) & ~15));
-    Place *ends = reinterpret_cast<Place *>(q_s);
+    // The axis: cost ahead of each request, and its T and L, in the tiles' memory.
+    int *ahead = reinterpret_cast<int *>(smem + 512);
+    int2 *tl = reinterpret_cast<int2 *>(smem + 512 + ((4 * p.bs + 4 + 15) & ~15));
+    Place *ends = reinterpret_cast<Place *>(smem);
     long long all = 0;
     int ways = 1;
     {
-        long long *ws = reinterpret_cast<long long *>(q_s + 64);
+        long long *ws = reinterpret_cast<long long *>(smem + 64);
         long long shared = 0;  // of two CTAs that walk together
         for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
             const int b = b0 + tid;
@@ -590,7 +609,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         w0.nt = w0.r.token_tiles();
         idle = !w0.cut() || (w0.rows(p) <= 0 && !w0.next(p, ways));
     }
-    fence_proxy_async_smem();  // the rings' memory goes over to TMA
+    fence_proxy_async_smem();  // the tiles' memory goes over to TMA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -619,7 +638,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             const bool ctx = lane < kGroups && g < w.r.ctx_groups();
             return ctx && (g >= whole || !(lane & (bg - 1))) ? p.page_table[(int64_t)w.r.slot * p.max_pages + (g >> gpp_shift)] : 0;
         };
-        int it = 0;
+        const int slots = v ? S::kSlotsV : S::kSlotsK;
+        int s = 0, phase = 0;  // of the ring
         Walk w = w0, wn = w0;
         int page = page_of(w, w.t0);
         bool more;
@@ -627,7 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             more = wn.next(p, ways);  // looked up while this segment's tiles are loaded
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
             const int whole = (w.r.L >> 3) & ~(bg - 1);  // groups in boxes that are full of tokens
-            for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
+            for (int t = w.t0; t < w.t0 + w.n; ++t) {
                 const int next_page = t + 1 < w.t0 + w.n ? page_of(w, t + 1) : more ? page_of(wn, wn.t0) : 0;
                 const int g = t * kGroups + lane, ng = min(kGroups, gall - t * kGroups);
                 const bool in = lane < ng, ctx = in && g < gctx;
@@ -637,8 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     page = p.num_pages;  // past the pool: zeros
                 }
                 const int rg = g & ((1 << gpp_shift) - 1);
-                const int s = it % S::kSlots;
-                mbar_wait(&empty[s], ((it / S::kSlots) & 1) ^ 1, p.status, kKvStatusTimeout);
+                mbar_wait(&empty[s], phase ^ 1, p.status, kKvStatusTimeout);
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
                 __syncwarp();
                 const uint32_t dst = ring + s * S::kTileBytes + lane * S::kGroupBytes;
@@ -652,6 +671,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     tma_load_5d(dst, map_new, 0, w.r.lo + (g - gctx) * 8, 0, w.h, 0, &full[s]);
                 }
                 page = next_page;
+                if (++s == slots) s = 0, phase ^= 1;
             }
             w = wn;
         } while (more);
@@ -668,32 +688,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             more = wn.next(p, ways);
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
-            mbar_wait(q_ready, item & 1, p.status, kKvStatusTimeout);
+            if (item == 0) mbar_wait(q_ready, 0, p.status, kKvStatusTimeout);  // the softmax warps fetch the first
+            else q_landed();
+            __syncwarp();
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
-                const int s = it % S::kSlots, buf = it % kBufs;
+                const int s = it % S::kSlotsK, buf = it % kBufs;
                 // what the buffer held has been read, and P that lay in its place multiplied
                 if (it >= kBufs) mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
-                mbar_wait(&k_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&k_full[s], (it / S::kSlotsK) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
                 const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
                 const uint32_t id = idesc16(F16, kTile, 16 * steps, false, false), dst = tmem + buf * 128;
-                const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4);
+                const uint64_t kd = k_d + (uint32_t)(s * S::kTileBytes >> 4), qd = q_d + (uint32_t)((item & 1) * S::kQBytes >> 4);
                 if (few) {
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
                         const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
-                        mma_ss(lead, dst, kd + off, q_d + off, id_few, x > 0);
+                        mma_ss(lead, dst, kd + off, qd + off, id_few, x > 0);
                     }
                 } else {
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
                         const uint32_t off = ((x / 4) * 1024 + (x % 4) * 32) >> 4;
-                        mma_ss(lead, dst, q_d + off, kd + off, id, x > 0);
+                        mma_ss(lead, dst, qd + off, kd + off, id, x > 0);
                     }
                 }
                 commit_one(lead, &k_empty[s]);
                 commit_one(lead, &s_full[buf]);
+                if (more && t == w.t0 + min(2, w.n - 1)) {
+                    // Q of the next item, where Q and P^T of the one before were: its last product is done
+                    const int last = it - (t - w.t0) - 1;
+                    if (last >= 0) mbar_wait(&pv_done[last % kBufs], (last / kBufs) & 1, p.status, kKvStatusTimeout);
+                    fetch_q<D>(p, wn, q_s + ((item + 1) & 1) * S::kQBytes, lane, 32);
+                }
             }
             ++item;
             w = wn;
@@ -703,7 +731,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         const uint32_t lead = elect_lead();
         const uint32_t id_pv = idesc16(F16, kTile, D, false, true), id_few = idesc16(F16, kTile, 32, true, true);
         const uint64_t v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes), p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
-        int it = 0;
+        int it = 0, item = 0;
         Walk w = w0;
         bool more;
         do {
@@ -712,13 +740,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
-                const int s = it % S::kSlots, buf = it % kBufs;
-                mbar_wait(&v_full[s], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                const int s = it % S::kSlotsV, buf = it % kBufs;
+                mbar_wait(&v_full[s], (it / S::kSlotsV) & 1, p.status, kKvStatusTimeout);
                 mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
                 __syncwarp();
                 tc_fence_after();
                 const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
-                const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4), pd = p_d + (uint32_t)(buf * 8192 >> 4);
+                const uint64_t vd = v_d + (uint32_t)(s * S::kTileBytes >> 4), pd = p_d + (uint32_t)(((item & 1) * S::kQBytes + buf * 8192) >> 4);
                 const uint32_t pt = tmem + buf * 128;
                 const bool add = t > w.t0;
                 if (few) {
@@ -741,6 +769,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 commit_one(lead, &v_empty[s]);
                 commit_one(lead, &pv_done[buf]);
             }
+            ++item;
             w = wn;
         } while (more);
     } else {
@@ -754,44 +783,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         Walk w = w0;
         bool more;
 
-        // Q of a segment: from memory, and into the swizzled tile.  A thread has half
-        // a row; 16 bytes when the products are turned over.
-        uint4 qv[D / 16];
-        auto q_src = [&](const Walk &u, int row, int el) {
-            const int at = u.m * kTile + row, t = at / p.group;
-            return p.q + (int64_t)(u.r.lo + t) * p.q_ts + (u.h * p.group + (at - t * p.group)) * p.q_hs + el;
-        };
-        auto q_load = [&](const Walk &u) {
-            const int rows = u.rows(p);
-            if (rows <= kFewRows) {
-                const int row = tid / (D / 8), el = (tid % (D / 8)) * 8;
-                if (row < rows) qv[0] = ldg16(q_src(u, row, el));
-            } else if (pos < rows) {
-                const uint16_t *src = q_src(u, pos, half * (D / 2));
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) qv[x] = ldg16(src + x * 8);
-            }
-        };
-        auto q_put = [&](int row, int chunk, uint4 v) {
-            const uint32_t a = smem_u32(q_s) + (row >> 3) * S::kGroupBytes + (row & 7) * 128 + (chunk >> 3) * 1024 +
-                               (((chunk & 7) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-        };
-        auto q_store = [&](const Walk &u) {
-            const int rows = u.rows(p);
-            if (rows <= kFewRows) {
-                const int row = tid / (D / 8);
-                if (row < rows) q_put(row, tid % (D / 8), qv[0]);
-            } else if (pos < rows) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) q_put(pos, half * (D / 16) + x, qv[x]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
-        };
-        q_load(w);
-        q_store(w);
+        fetch_q<D>(p, w, q_s, tid, kSoftWarps * 32);
+        q_landed();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
 
         do {
             Walk wn = w;
@@ -819,8 +814,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             // NaN there); what is not finite in a drafted row is taken out, and added at the end to the
             // rows that see it.
             auto clean_v = [&](int t) {
-                const int sv = it % S::kSlots;
-                mbar_wait(&v_full[sv], (it / S::kSlots) & 1, p.status, kKvStatusTimeout);
+                const int sv = it % S::kSlotsV;
+                mbar_wait(&v_full[sv], (it / S::kSlotsV) & 1, p.status, kKvStatusTimeout);
                 const int r0 = max(w.r.L - t * kTile, 0), n = (keys_of(t) - r0) * (D / 8);
                 for (int i = tid; i < n; i += kSoftWarps * 32) {
                     const int r = r0 + i / (D / 8), y = i % (D / 8), jt = t * kTile + r - gctx * 8;
@@ -958,7 +953,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         if (it >= kBufs)  // the product before in this buffer
                             mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
                         // P^T: 64 bytes a token, high parts of 16 rows, then the low parts; 64-byte swizzle
-                        const uint32_t a = smem_u32(q_s) + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
+                        const uint32_t a = smem_u32(q_s) + (item & 1) * S::kQBytes + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + ((half ^ x) << 4)), "r"(hi[0]), "r"(hi[1]),
                                      "r"(hi[2]), "r"(hi[3])
                                      : "memory");
@@ -970,9 +965,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     else fence_proxy_async_smem();
                     p_is_ready();
                 }
-                // Q of the next segment, unless P^T is still read where it goes
-                const bool early = more && wn.rows(p) <= kFewRows;
-                if (more) q_load(wn);
                 if (nl > 0) {
                     float *sum = red_s + 2 * kTile + half * 64 + 32;  // [quadrant][row], beside the maxima
 #pragma unroll
@@ -984,7 +976,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
 #pragma unroll
                     for (int r = 0; r < 8; ++r) l[r] = (sum[r] + sum[8 + r]) + (sum[16 + r] + sum[24 + r]);
                 }
-                if (early) q_store(wn);
                 await_pv();
                 if (nl > 0) {
                     float o[8], low[8];
@@ -1008,7 +999,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         }
                     }
                 }
-                if (more && !early) q_store(wn);
             } else {
                 // ------------------------------------------------- as is
                 // a warp has 16 rows, a thread two of them: elements 2 z, 2 z + 1 of every 8 tokens
@@ -1026,15 +1016,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         float s[64];
                         tmem_ld_rows128(t_s, s);
                         if (edge(t)) {
+                            // a thread looks up two of its rows' eight words: words z of both
+                            const int k0 = t * kTile + 32 * z, n = w.r.L - k0;
+                            uint32_t see[2];
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const int tr = (w.m * kTile + row0 + 8 * r) / p.group;
+                                const int tr = min((w.m * kTile + row0 + 8 * r) / p.group, w.r.T - 1);
+                                see[r] = tree_word(p, w.r, tr, k0 - gctx * 8) | (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+                            }
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int k0 = t * kTile + 32 * q, n = w.r.L - k0;
-                                    uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-                                    if (live[r]) bits |= tree_word(p, w.r, tr, k0 - gctx * 8);
-                                    bits >>= 2 * z;
+                            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const uint32_t bits = __shfl_sync(kFullMask, see[r], q, 4) >> (2 * z);
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) {
                                         float &x = s[16 * q + 4 * (i / 2) + 2 * r + i % 2];
@@ -1042,7 +1036,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                     }
                                 }
                             }
-                            __syncwarp();
                         }
                         float top[2];
 #pragma unroll
@@ -1115,11 +1108,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     }
                     if (edge(t)) clean_v(t);
                     p_is_ready();
-                }
-                // Q of the next segment: its products with this one's Q are done
-                if (more) {
-                    q_load(wn);
-                    q_store(wn);
                 }
                 // From here a thread has a row, and half of O's columns.  (All warps have ended the item
                 // before when the last product of this one is done: red_s can be written.)
