@@ -77,6 +77,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpO = kWarpK + 3;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 4);
 constexpr int kBufs = 3;           // S buffers in tensor memory, P^T buffers in shared memory
+constexpr int kWalks = 4;          // items that the product warp has told the others of
 constexpr int kMaxRequests = 16000;  // 12 bytes each in the tiles' memory
 constexpr int kCombineThreads = 128;
 constexpr float kLazy = 8.0f;      // growth of the maximum (base 2) that is let stand
@@ -89,13 +90,16 @@ struct Shape {
     static constexpr int kTileBytes = kGroups * kGroupBytes;
     static constexpr int kSlotsK = D == 128 ? 2 : 5, kSlotsV = D == 128 ? 3 : 5;  // of the rings
     static constexpr int kRings = (kSlotsK + kSlotsV) * kTileBytes;
-    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1;
+    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1 + kWalks;
     static constexpr int kQBytes = 32768;               // Q of an item, or 16 rows of it and P^T
     static constexpr int kTiles = 2 * kQBytes + kRings;  // Q of two items, and the rings
     static_assert(kTileBytes <= kQBytes && 8192 + kBufs * 8192 <= kQBytes, "Q and P^T");
     static constexpr int kRedBytes = 3 * kTile * 4;     // a row's maximum and sum; the same turned over, by warps
     static constexpr int kFlagBytes = 2 * 8 * 4;       // a warp's flag, by turns
-    static constexpr int kSmem = kTiles + kRedBytes + kFlagBytes + (kBars + 1) * 8 + 64;
+    static constexpr int kWalkBytes = kWalks * 32;
+    static constexpr int kBarsAt = kTiles + kRedBytes + kFlagBytes + kWalkBytes;
+    static constexpr int kSmem = kBarsAt + (kBars + 1) * 8 + 64;
+    static_assert((kTiles + kRedBytes + kFlagBytes) % 16 == 0 && kBarsAt % 8 == 0, "alignment");
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(512 + 12 * kMaxRequests + 32 <= kTiles, "what the axis is cut by");
 };
@@ -469,6 +473,18 @@ __device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead,
     return q;
 }
 
+// What row t sees of the non-finite values of the drafted tokens in n token
+// tiles from t0 on, at element el of V: they are added in the end.
+template <bool F16>
+__device__ __noinline__ float odd_sum(const AttnParams &p, Req r, int h, int t, int el, int t0, int n) {
+    float sum = 0.0f;
+    for (int j = max(0, t0 * kTile - r.ctx_groups() * 8); j < min(r.T, (t0 + n) * kTile - r.ctx_groups() * 8); ++j) {
+        const uint16_t v = p.v_new[(int64_t)(r.lo + j) * p.n_ts + h * p.n_hs + el];
+        if (nonfinite16<F16>(v) && (tree_word(p, r, t, j) & 1)) sum += widen<F16>(v);
+    }
+    return sum;
+}
+
 // Q of an item into its swizzled tile, by `threads` threads (a multiple of
 // D / 8) of which this is thread `i`: each has one 16-byte column.
 template <int D>
@@ -500,11 +516,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     unsigned char *q_s = smem, *k_ring = q_s + 2 * S::kQBytes, *v_ring = k_ring + S::kSlotsK * S::kTileBytes;
     float *red_s = reinterpret_cast<float *>(smem + S::kTiles);
     int *flag_s = reinterpret_cast<int *>(smem + S::kTiles + S::kRedBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBarsAt);
     uint64_t *k_full = bars, *k_empty = k_full + S::kSlotsK, *v_full = k_empty + S::kSlotsK, *v_empty = v_full + S::kSlotsV,
              *s_full = v_empty + S::kSlotsV, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
-             *q_ready = pv_done + kBufs;
+             *q_ready = pv_done + kBufs, *walk_full = q_ready + 1;
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
+    int4 *walk_s = reinterpret_cast<int4 *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -528,6 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_ready, kSoftWarps);
+        for (int i = 0; i < kWalks; ++i) mbar_init(&walk_full[i], 1);
         fence_mbar_init();
         *odd_item = -1;
     }
@@ -615,6 +633,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = misc[0];
     const uint32_t t_o = tmem + kBufs * 128;
+
+    // The next item, from the warp that multiplies Q and K: it is ahead of the others by up to three
+    // tiles, so of four places the one that it writes has been read.  None: n = 0.
+    // (The first that is told of is item 1: place 0, phase 0.)
+    auto tell = [&](const Walk &w, int item) {
+        const int at = (item - 1) % kWalks;
+        if (lane == 0) {
+            walk_s[2 * at] = make_int4(w.r.lo, w.r.T, w.r.L, w.h);
+            walk_s[2 * at + 1] = make_int4(w.m, w.t0, w.n, w.nt);
+            mbar_arrive(&walk_full[at]);
+        }
+    };
+    auto told = [&](Walk &w, int item) {
+        const int at = (item - 1) % kWalks;
+        mbar_wait(&walk_full[at], ((item - 1) / kWalks) & 1, p.status, kKvStatusTimeout);
+        __syncwarp();
+        const int4 a = walk_s[2 * at], b = walk_s[2 * at + 1];
+        w.r.lo = a.x;
+        w.r.T = a.y;
+        w.r.L = a.z;
+        w.h = a.w;
+        w.m = b.x;
+        w.t0 = b.y;
+        w.n = b.z;
+        w.nt = b.w;
+        return w.n > 0;
+    };
 
     if (idle) {
         // nothing
@@ -725,6 +770,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             }
             ++item;
             w = wn;
+            if (!more) w.n = 0;
+            tell(w, item);
         } while (more);
     } else if (warp == kWarpO) {
         // ------------------------------------------------ products: O += P V
@@ -733,10 +780,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         const uint64_t v_d = smem_desc(smem_u32(v_ring), 1024, S::kGroupBytes), p_d = smem_desc(smem_u32(q_s) + 8192, 16, 512, true);
         int it = 0, item = 0;
         Walk w = w0;
-        bool more;
         do {
-            Walk wn = w;
-            more = wn.next(p, ways);
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
@@ -769,9 +813,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 commit_one(lead, &v_empty[s]);
                 commit_one(lead, &pv_done[buf]);
             }
-            ++item;
-            w = wn;
-        } while (more);
+        } while (told(w, ++item));
     } else {
         // ---------------------------------------------------------- softmax
         // warps w and w + 4 share 32 lanes (a quadrant)
@@ -781,7 +823,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         constexpr float kShift = F16 ? 4.0f : 0.0f;  // P up to 2^12 in half: small weights keep more of their bits
         int it = 0, item = 0;
         Walk w = w0;
-        bool more;
 
         fetch_q<D>(p, w, q_s, tid, kSoftWarps * 32);
         q_landed();
@@ -789,8 +830,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         if (lane == 0) mbar_arrive(q_ready);
 
         do {
-            Walk wn = w;
-            more = wn.next(p, ways);
             const int rows = w.rows(p);
             const bool few = rows <= kFewRows;
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
@@ -842,18 +881,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[it % kBufs]);
-            };
-            // What row t sees of the drafted tokens' non-finite values, from element el on.
-            auto add_odd = [&](int t, int el, auto &o) {
-                constexpr int N = sizeof(o) / sizeof(float);
-                for (int j = 0; j < w.r.T; ++j) {
-                    const int vt = (gctx * 8 + j) / kTile;
-                    if (vt < w.t0 || vt >= w.t0 + w.n || !(tree_word(p, w.r, t, j) & 1)) continue;
-                    const uint16_t *v = p.v_new + (int64_t)(w.r.lo + j) * p.n_ts + w.h * p.n_hs + el;
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (nonfinite16<F16>(v[i])) o[i] += widen<F16>(v[i]);
-                }
             };
             auto inverse = [](float l) { return l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l; };  // NaN stays
             auto put_row = [&](int row, float m, float l) {  // what a row leaves beside O
@@ -988,12 +1015,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         for (int r = 0; r < 8; ++r) {
                             if (r < nl) {
                                 const int row = 8 * half + r, at = w.m * kTile + row, tr = at / p.group;
-                                float x[1] = {o[r] + low[r]};
-                                if (odd) add_odd(tr, pos, x);
+                                float x = o[r] + low[r];
+                                if (odd) x += odd_sum<F16>(p, w.r, w.h, tr, pos, w.t0, w.n);
                                 if (whole)
                                     p.out[(int64_t)(w.r.lo + tr) * p.o_ts + (w.h * p.group + (at - tr * p.group)) * p.o_hs + pos] =
-                                        (uint16_t)pack2<F16>(x[0] * inverse(l[r]), 0.0f);
-                                else part[row * 4] = x[0];
+                                        (uint16_t)pack2<F16>(x * inverse(l[r]), 0.0f);
+                                else part[row * 4] = x;
                                 if (pos == 0) put_row(row, m[r], l[r]);
                             }
                         }
@@ -1126,15 +1153,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     const bool odd = *odd_item == item;
                     const float mr = red_s[pos], lr = red_s[kTile + pos], inv = inverse(lr);
                     const int at = w.m * kTile + pos, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < D / 64; ++h) {
                         const int el = half * (D / 2) + 32 * h;
+                        uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs + el;
+                        float *part = k.part + (((int64_t)cell * (D / 4) + el / 4) * kTile + pos) * 4;
                         float o[32];
                         tmem_ld32(t_o + lane_base + el, o);
                         if (pos < rows) {
-                            if (odd) add_odd(t_row, el, o);
                             if (whole) {
-                                uint16_t *dst = p.out + (int64_t)(w.r.lo + t_row) * p.o_ts + head * p.o_hs + el;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     uint4 v;
@@ -1145,10 +1172,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                                     *reinterpret_cast<uint4 *>(dst + i * 8) = v;
                                 }
                             } else {
-                                float4 *part = reinterpret_cast<float4 *>(k.part) + ((int64_t)cell * (D / 4) + el / 4) * kTile + pos;
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
-                                    part[i * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                                    *reinterpret_cast<float4 *>(part + i * kTile * 4) =
+                                        make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            }
+                            if (odd) {
+#pragma unroll 1
+                                for (int i = 0; i < 32; ++i) {
+                                    const float x = odd_sum<F16>(p, w.r, w.h, t_row, el + i, w.t0, w.n);
+                                    if (x == 0.0f) continue;
+                                    if (whole) dst[i] = (uint16_t)pack2<F16>(x * inv, 0.0f);
+                                    else part[(i / 4) * kTile * 4 + (i & 3)] = x;
+                                }
                             }
                         }
                         __syncwarp();
@@ -1161,9 +1197,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 else k.tails[blockIdx.x] = w.t0 + w.n == w.nt ? 2 : 1;
             }
             tc_fence_before();
-            ++item;
-            w = wn;
-        } while (more);
+        } while (told(w, ++item));
     }
     tc_fence_before();
     __syncthreads();

@@ -265,6 +265,16 @@ def test_heads_of_several_row_tiles(T, L, d, dtype):
     compare(c, run(c), causal(T))
 
 
+@pytest.mark.parametrize("T,hq", [([1], 4), ([9], 8), ([1, 9, 33], 8)])
+def test_many_items_of_several_tiles(T, hq):
+    """Ten and more items a CTA, most of two to five token tiles."""
+    n = 800
+    T = [T[i % len(T)] for i in range(n)]
+    c = make(T, [130 + (97 * i) % 500 for i in range(n)], hq, 2, 64, seed=hq)
+    compare(c, run(c), causal(T))
+    assert c["cache"].device_status() == 0
+
+
 def test_growing_and_falling_scores():
     """Rows whose maximum moves by hundreds along the tokens, both ways."""
     c = make([2, 2], [700, 700], 2, 1, 64, torch.float16, seed=21, poison=False)
