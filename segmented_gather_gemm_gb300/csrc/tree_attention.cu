@@ -353,7 +353,7 @@ constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 // share of HBM, half of that when two CTAs read them together (of head_dim 64 in
 // less than the softmax takes); its softmax takes 1000 clocks turned over,
 // otherwise 1400 (half) or 1800 (bfloat16).  Beginning and ending an item costs
-// 2500 turned over, 12800 otherwise.  With equal tile counts instead, the CTAs of
+// 5800 turned over (its tiles' loads start anew), 10200 otherwise.  With equal tile counts instead, the CTAs of
 // short sequences ran 15 to 30 % longer than the others.
 struct Cost {
     int mi, nt;          // items and token tiles
@@ -364,7 +364,7 @@ __device__ __forceinline__ int tile_cost(int rows, bool shared, int d, bool f16)
     const int bytes = (d == 128 ? 45 : 16) >> (int)shared;
     return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 26);
 }
-__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 100 : 200; }
+__device__ __forceinline__ int item_cost(int rows) { return rows <= kFewRows ? 90 : 160; }
 __device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p, int ways) {
     Cost c;
     const Req r = {0, T, L, 0};
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     int2 *tl = reinterpret_cast<int2 *>(smem + 512 + ((4 * p.bs + 4 + 15) & ~15));
     Place *ends = reinterpret_cast<Place *>(smem);
     long long all = 0;
-    int ways = 1;
+    int ways = 1, lo = 0, slot = 0;  // (the last two of request `tid`)
     {
         long long *ws = reinterpret_cast<long long *>(smem + 64);
         long long shared = 0;  // of two CTAs that walk together
@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     shared += (long long)cost_of(r.T, r.L, p, 2).head * p.hkv;
                 }
                 tl[b] = make_int2(r.T, r.L);
+                if (b0 == 0) lo = r.lo, slot = r.slot;
                 if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
             }
             const long long pre = block_scan_ex(n, ws, &tot);
@@ -609,6 +610,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         k.tails[blockIdx.x] = 0;
     }
     __syncthreads();
+    // its first request: known to a thread, if there is one for each
+    const bool known = p.bs <= kAttnThreads;
+    if (known && tid == ends[0].b) walk_s[0] = make_int4(lo, tl[tid].x, tl[tid].y, slot);
+    __syncthreads();
     Walk w0 = {};
     {
         const Place at = ends[0];
@@ -623,7 +628,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     bool idle = all == 0 || w0.b >= p.bs;
     if (!idle) {
         int bad;
-        w0.r = load_req(p, w0.b, &bad);
+        const int4 r = walk_s[0];
+        w0.r = known ? Req{r.x, r.y, r.z, r.w} : load_req(p, w0.b, &bad);
         w0.nt = w0.r.token_tiles();
         idle = !w0.cut() || (w0.rows(p) <= 0 && !w0.next(p, ways));
     }
