@@ -287,10 +287,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) commit_move(Kv c, CommitParam
     const int64_t units = (int64_t)rows * c.layers;
     for (int64_t u = (int64_t)blockIdx.x * nw + warp; u < units; u += (int64_t)gridDim.x * nw) {
         const int layer = (int)(u / rows), r = (int)(u - (int64_t)layer * rows);
-        int lo = 0, hi = p.bs;  // the last request whose first row is at most r
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (c.sa[mid] <= r) lo = mid; else hi = mid;
+        int lo = 0;  // the last request whose first row is at most r: 32 are tried at once
+        for (int len = p.bs; len > 1;) {
+            const int step = (len + 31) >> 5, at = lane * step;
+            const int k = 31 - __clz(__ballot_sync(kFullMask, at < len && c.sa[lo + at] <= r));
+            lo += k * step;
+            len = min(step, len - k * step);
         }
         const int j = r - c.sa[lo], q = p.seq_slots ? p.seq_slots[lo] : lo;
         const int node = p.accept_index ? p.accept_index[(int64_t)lo * p.accept_width + j] : j;
