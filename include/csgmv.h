@@ -528,7 +528,8 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  * over the tokens i of sequence s in layer `layer` of the cache, and over the
  * request's own rows j whose bit is set in row t of `mask`.  A row that sees
  * no token gives out = 0 and lse = -inf.  What is masked has no influence,
- * whatever it holds (infinities and NaN too, and slots past a sequence's end).
+ * whatever it holds (infinities and NaN too, and slots past a sequence's end);
+ * an infinity in a V that a row does see gives an infinity or NaN.
  *   q, out         dtype of the cache; element (t, h, d) at t * q_token_stride
  *                  + h * q_head_stride + d (out_* for out; multiples of 8)
  *   k_new, v_new   element (t, g, d) at t * new_token_stride + g * new_head_stride + d

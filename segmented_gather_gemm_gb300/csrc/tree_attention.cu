@@ -41,9 +41,9 @@
 // L2.  That doubles a part's length, and the CTA whose row tile is missing or
 // small waits; every CTA adds up the cost of both ways and takes the cheaper
 // (`ways`).  32 trees of 33 to 64 tokens, 4 query heads a kv head, 500 to 8192
-// cached: 174 us together, 232 us apart.  (Both row tiles in one CTA, K and V
-// read once: 221 us, for each tile then waits for the other's softmax, products
-// and their hand-overs.)
+// cached: 145 us together, 199 us apart.  (Both row tiles in one CTA, K and V
+// read once, took 221 us when this took 174: each tile then waits for the
+// other's softmax, products and their hand-overs.)
 //
 // Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
 // keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
@@ -353,8 +353,9 @@ constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 // share of HBM, half of that when two CTAs read them together (of head_dim 64 in
 // less than the softmax takes); its softmax takes 1000 clocks turned over,
 // otherwise 1400 (half) or 1800 (bfloat16).  Beginning and ending an item costs
-// 5800 turned over (its tiles' loads start anew), 10200 otherwise.  With equal tile counts instead, the CTAs of
-// short sequences ran 15 to 30 % longer than the others.
+// 5800 turned over (its tiles' loads start anew), 10200 otherwise.  With equal tile counts
+// instead 256 requests of 64 to 4096 tokens take 340 us (328), the trees above
+// 218 us (145).
 struct Cost {
     int mi, nt;          // items and token tiles
     int tile[2], item[2];  // of a full item, of the last: one token tile, the whole item
