@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
              *q_ready = pv_done + kBufs, *walk_full = q_ready + 1;
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     int4 *walk_s = reinterpret_cast<int4 *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
+    volatile int *walks_read = reinterpret_cast<volatile int *>(misc + 3);  // by all warps
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -549,6 +550,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         for (int i = 0; i < kWalks; ++i) mbar_init(&walk_full[i], 1);
         fence_mbar_init();
         *odd_item = -1;
+        *walks_read = 0;
     }
     griddep_wait();
     // The axis: cost ahead of each request, and its T and L, in the tiles' memory.
@@ -641,22 +643,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     const uint32_t tmem = misc[0];
     const uint32_t t_o = tmem + kBufs * 128;
 
-    // The next item, from the warp that multiplies Q and K: it is ahead of the others by up to three
-    // tiles, so of four places the one that it writes has been read.  None: n = 0.
-    // (The first that is told of is item 1: place 0, phase 0.)
+    // The next item, from the warp that multiplies Q and K to those that do the rest (none: n = 0), in
+    // one of kWalks places.  Every warp has to come to the same items, also after a wait was given up:
+    // so these two waits do not look at the status, and a place is written again only when all have
+    // read it.  Neither can last, for all other waits are bounded and both sides come here in turn.
+    constexpr uint64_t kLong = 20000000000ull;
     auto tell = [&](const Walk &w, int item) {
         const int at = (item - 1) % kWalks;
         if (lane == 0) {
+            const uint64_t t0 = global_ns();
+            while (*walks_read < (item - kWalks) * (kSoftWarps + 1) && global_ns() - t0 < kLong) {}
             walk_s[2 * at] = make_int4(w.r.lo, w.r.T, w.r.L, w.h);
             walk_s[2 * at + 1] = make_int4(w.m, w.t0, w.n, w.nt);
             mbar_arrive(&walk_full[at]);
         }
     };
     auto told = [&](Walk &w, int item) {
-        const int at = (item - 1) % kWalks;
-        mbar_wait(&walk_full[at], ((item - 1) / kWalks) & 1, p.status, kKvStatusTimeout);
+        const int at = (item - 1) % kWalks, phase = ((item - 1) / kWalks) & 1;
+        if (!mbar_try_wait(&walk_full[at], phase)) {
+            const uint64_t t0 = global_ns();
+            bool there = false;
+            while (!there && global_ns() - t0 < kLong) there = mbar_try_wait(&walk_full[at], phase);
+            if (!there) {
+                atomicOr(p.status, kKvStatusTimeout);
+                return false;
+            }
+        }
         __syncwarp();
         const int4 a = walk_s[2 * at], b = walk_s[2 * at + 1];
+        __syncwarp();
+        if (lane == 0) atomicAdd(const_cast<int *>(walks_read), 1);
         w.r.lo = a.x;
         w.r.T = a.y;
         w.r.L = a.z;
