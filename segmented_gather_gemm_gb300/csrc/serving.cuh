@@ -74,7 +74,7 @@ __device__ __forceinline__ T block_scan_ex(T v, T *ws, T *total) {
 // stream still runs, and waits for it in griddep_wait().
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t stream, int cluster,
-                                 bool dependent, Args... args) {
+                                 bool dependent, const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);
@@ -96,7 +96,11 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, int block,
     }
     cfg.attrs = at;
     cfg.numAttrs = (unsigned)n;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    auto go = [&](const KArgs &...a) {  // arguments that have the parameters' types are not copied
+        void *at[] = {const_cast<void *>(static_cast<const void *>(&a))...};
+        return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), at);
+    };
+    return go(args...);
 }
 
 }  // namespace csgmv

@@ -62,8 +62,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
+#include <atomic>
 
 #include "serving.cuh"
 
@@ -111,13 +110,15 @@ struct AttnMaps {
 };
 enum { kPagesGeneral = 0, kPagesHeadsOut = 1, kPagesHeadsIn = 2 };
 
-struct AttnKernelParams {
-    AttnParams p;
-    AttnMaps maps;
+struct Parts {  // of the items that the cuts go through
     float *part;      // [2 * kAttnCtas][D / 4][kTile] float4: unscaled O
     float *ml;        // [2 * kAttnCtas][2][kTile]: m, l
     int4 *starters;   // [kAttnCtas]: the item a CTA begins and does not end {first token, h, first row, rows and ways}, or {-1}
     int *tails;       // [kAttnCtas]: of an item begun by an earlier CTA: 0 nothing, 1 a middle part, 2 its end
+};
+struct AttnKernelParams : Parts {
+    AttnParams p;
+    AttnMaps maps;
     int form;         // kPages*
     int box_groups;   // 8-row groups of a whole box
 };
@@ -1229,17 +1230,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     if (warp == kWarpO) tmem_dealloc(tmem, 512);
 }
 
+// What joining them takes of AttnParams.
+struct JoinParams {
+    uint16_t *out;
+    float *lse;
+    int64_t o_ts, o_hs;
+    int hq, group;
+};
+
 // Joins the parts of the items that the axis' cuts went through, in order of
 // the axis.  The rows of all such items are dealt out to the blocks R at a
 // time.  Two rounds of dependent loads: which items and parts there are, and
 // the parts (O and its scales together).
 template <int D, bool F16>
-__global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant__ AttnKernelParams k, int ctas) {
+__global__ void __launch_bounds__(kCombineThreads) combine(const Parts k, const JoinParams p, int ctas) {
     constexpr int R = kCombineThreads / (D / 4);  // rows of a block
     static_assert(2 * kCombineThreads >= kAttnCtas, "two items a thread");
     __shared__ int first[2 * kCombineThreads + 1], ws[33], tails[2 * kCombineThreads];
     __shared__ int4 items[2 * kCombineThreads];
-    const AttnParams &p = k.p;
     const int tid = threadIdx.x;
     griddep_launch_dependents();
     griddep_wait();
@@ -1324,20 +1332,15 @@ __global__ void __launch_bounds__(kCombineThreads) combine(const __grid_constant
 }
 
 // ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::mutex g_mu;
-std::map<int, int> g_ready;  // device -> CTAs to launch
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_ready[kMaxDevices];  // CTAs to launch; 0: not set up yet (twice does no harm)
 
 cudaError_t prepare(int *ctas) {
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto found = g_ready.find(dev);
-    if (found != g_ready.end()) {
-        *ctas = found->second;
-        return cudaSuccess;
-    }
+    if (dev < kMaxDevices && (*ctas = g_ready[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
     if (!g_encode) {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1365,7 +1368,8 @@ cudaError_t prepare(int *ctas) {
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
     }
-    *ctas = g_ready[dev] = sms < kAttnCtas ? sms : kAttnCtas;
+    *ctas = sms < kAttnCtas ? sms : kAttnCtas;
+    if (dev < kMaxDevices) g_ready[dev].store(*ctas, std::memory_order_release);
     return cudaSuccess;
 }
 
@@ -1381,7 +1385,7 @@ bool encode(CUtensorMap *map, const void *base, bool f16, const int64_t (&dim)[5
     }
     // the stride of a dimension of one element is never used
     for (int i = 0; i < 4; ++i) s[i] = dim[i + 1] > 1 ? (cuuint64_t)stride[i] * 2 : 128;
-    return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+    return g_encode.load(std::memory_order_relaxed)(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                     const_cast<void *>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1393,8 +1397,10 @@ cudaError_t launch(const AttnKernelParams &k, int ctas, cudaStream_t stream) {
     // as many blocks as an SM holds at most, and no more than there are rows for
     constexpr int R = kCombineThreads / (D / 4);
     const int64_t jobs = ((int64_t)k.p.num_tokens * k.p.hq + R - 1) / R;
+    const Parts &parts = k;
+    const JoinParams join = {k.p.out, k.p.lse, k.p.o_ts, k.p.o_hs, k.p.hq, k.p.group};
     return launch_kernel(combine<D, F16>, dim3((unsigned)std::min<int64_t>(8 * ctas, jobs)), kCombineThreads, 0, stream, 0,
-                         true, k, ctas);
+                         true, parts, join, ctas);
 }
 
 constexpr size_t kStarterBytes = kAttnCtas * (sizeof(int4) + sizeof(int4));  // starters, then tails
