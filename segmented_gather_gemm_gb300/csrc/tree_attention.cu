@@ -99,6 +99,7 @@ struct Shape {
     static constexpr int kBarsAt = kTiles + kRedBytes + kFlagBytes + kWalkBytes;
     static constexpr int kSmem = kBarsAt + (kBars + 1) * 8 + 64;
     static_assert((kTiles + kRedBytes + kFlagBytes) % 16 == 0 && kBarsAt % 8 == 0, "alignment");
+    static_assert(kTile == 128, "items() shifts by 7");
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(512 + 12 * kMaxRequests + 32 <= kTiles, "what the axis is cut by");
 };
@@ -325,7 +326,7 @@ struct Req {
     __device__ __forceinline__ int ctx_groups() const { return (L + 7) >> 3; }
     __device__ __forceinline__ int groups() const { return ctx_groups() + ((T + 7) >> 3); }
     __device__ __forceinline__ int token_tiles() const { return (groups() + kGroups - 1) / kGroups; }
-    __device__ __forceinline__ int items(int group, int ways) const { return (T * group + kTile * ways - 1) / (kTile * ways); }
+    __device__ __forceinline__ int items(int group, int ways) const { return (T * group + kTile * ways - 1) >> (6 + ways); }  // ways is 1 or 2
 };
 
 // Request b, with T = 0 (no work) when it is not sound; the status bit why.
@@ -606,7 +607,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     __syncthreads();
     // this CTA's part: two warps find its two ends
     if (lane == 0 && warp < 2) {
-        const int parts = gridDim.x / ways, q = (int)all / parts, rest = (int)all - q * parts, c = blockIdx.x / ways + warp;
+        const int parts = gridDim.x >> (ways - 1), q = (int)all / parts, rest = (int)all - q * parts,
+                  c = (blockIdx.x >> (ways - 1)) + warp;
         ends[warp] = place_at(p, ahead, tl, ways, c < parts ? c * q + min(c, rest) : (int)all);
     }
     if (tid == 0) {
