@@ -72,15 +72,18 @@ constexpr int kVerWarps = kVerThreads / 32;
 __device__ __forceinline__ long long fixed44(float x) {
     return __float2ll_rz(fminf(fmaxf(x, 0.0f), 1.0f) * 17592186044416.0f);
 }
-// The same steps as a high and a low number of 22 bits each: both products and
-// the difference are exact, and sums over a thread's tokens fit 32 bits.
+// The same steps as a high and a low number of 22 bits each, whose sums over a
+// thread's tokens fit 32 bits.  A float in [2, 4) counts steps of 2^-22 in its
+// lower bits, so adding 2 towards zero leaves the high number there, and what
+// that leaves out, exact, times 2^22 plus 2 the low one: no conversions (with
+// three a number, 64 sampled trees over 128256 tokens took 37.6 us, now 36.2).
+// The bits of the 2 itself cancel when a multiple of four are added.
 struct Steps {
     uint32_t hi, lo;
     __device__ __forceinline__ void add(float x) {
-        const float a = fminf(fmaxf(x, 0.0f), 1.0f) * 4194304.0f;
-        const uint32_t h = __float2uint_rz(a);
-        hi += h;
-        lo += __float2uint_rz((a - __uint2float_rn(h)) * 4194304.0f);
+        const float a = fminf(fmaxf(x, 0.0f), 1.0f), t = __fadd_rz(a, 2.0f);
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(__fmaf_rz(__fsub_rn(a, __fsub_rn(t, 2.0f)), 4194304.0f, 2.0f));
     }
     __device__ __forceinline__ long long total() const { return ((long long)hi << 22) + lo; }
 };
