@@ -530,7 +530,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     int4 *walk_s = reinterpret_cast<int4 *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
     volatile int *walks_read = reinterpret_cast<volatile int *>(misc + 3);  // by all warps
-    volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 2);  // the last item with a non-finite drafted V
+    // The last item with a non-finite drafted V, of the even and of the odd ones: a softmax warp may be in the
+    // next item while another still ends this one (not two on, for a product takes P of all of them).
+    volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // (The join is not launched early: its blocks among this kernel's cost 12 us a call.)
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         mbar_init(q_ready, kSoftWarps);
         for (int i = 0; i < kWalks; ++i) mbar_init(&walk_full[i], 1);
         fence_mbar_init();
-        *odd_item = -1;
+        odd_item[0] = odd_item[1] = -1;
         *walks_read = 0;
     }
     griddep_wait();
@@ -901,7 +903,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             if (nonfinite16<F16>(e[z])) odd = true, e[z] &= 0xffff0000u;
                             if (nonfinite16<F16>(e[z] >> 16)) odd = true, e[z] &= 0x0000ffffu;
                         }
-                        if (odd) *odd_item = item;
+                        if (odd) odd_item[item & 1] = item;
                     }
                     if (odd) *a = v;
                 }
@@ -1039,7 +1041,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     tmem_ld8(t_o + lane_base + half * 8, o);
                     tmem_ld8(t_o + lane_base + 16 + half * 8, low);
                     if (pos < D) {  // a thread has element `pos`
-                        const bool odd = *odd_item == item;
+                        const bool odd = odd_item[item & 1] == item;
                         float *part = k.part + ((int64_t)cell * (D / 4) + pos / 4) * kTile * 4 + (pos & 3);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
@@ -1180,7 +1182,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                         }
                     }
                     named_bar_sync(1 + quad, 64);
-                    const bool odd = *odd_item == item;
+                    const bool odd = odd_item[item & 1] == item;
                     const float mr = red_s[pos], lr = red_s[kTile + pos], inv = inverse(lr);
                     const int at = w.m * kTile + pos, t_row = at / p.group, head = w.h * p.group + (at - t_row * p.group);
 #pragma unroll 1
