@@ -545,8 +545,10 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  * timing.  A page number out of range sets CSGMV_KV_STATUS_BAD_PAGE and makes
  * its request's rows meaningless; other bad requests are left out (their rows
  * of out and lse stay as they are).  bs <= 16000;
- * CSGMV_KV_STATUS_CAPACITY and no output when the batch's cost does not fit 31
- * bits (some 10^9 cached tokens times kv heads).
+ * num_tokens times the query heads of a kv head <= 2^30.  A batch of more than
+ * some four minutes of work on the whole GPU (2^40 units of 64 clocks of an SM,
+ * of which 128 rows against 128 tokens take 16 to 45, so at least 4 * 10^14
+ * pairs of a row and a token) sets CSGMV_KV_STATUS_CAPACITY and gives no output.
  *   workspace      csgmv_tree_attention_workspace_bytes(); contents do not matter
  */
 CSGMV_API int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads,

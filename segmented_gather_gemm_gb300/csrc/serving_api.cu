@@ -192,6 +192,8 @@ int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
         return fail(CSGMV_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, kv->num_layers);
     if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
     if (num_tokens > INT32_MAX / 128) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds 2^24");
+    if (num_tokens * (num_q_heads / kv->num_kv_heads) > (1 << 30))
+        return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens times the query heads of a kv head exceeds 2^30");
     if (bs > csgmv::attn_max_requests())
         return fail(CSGMV_ERR_UNSUPPORTED, "bs %d exceeds %d", bs, csgmv::attn_max_requests());
     if (bs == 0 || num_tokens == 0) return CSGMV_OK;

@@ -362,11 +362,22 @@ constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 // 5800 turned over (its tiles' loads start anew), 10200 otherwise.  With equal
 // tile counts instead, 256 requests of 64 to 4096 tokens take 340 us (328), the
 // trees above 218 us (145).
+//
+// An item's cost fits 29 bits (2^30 tokens); a head's, and the batch's, may pass
+// 32: those are 64 bits wide, and the axis counts in steps of 2^shift units where
+// 31 bits of them would not do (`scale_of`).
 struct Cost {
     int mi, nt;          // items and token tiles
     int tile[2], item[2];  // of a full item, of the last: one token tile, the whole item
-    int head;            // a kv head's items
+    long long head;      // a kv head's items
 };
+// More than so many units (2^40: four minutes of the whole GPU) are refused.
+constexpr long long kMaxCost = 1ll << 40;
+__device__ __forceinline__ int scale_of(long long all, int bs) {
+    int shift = 0;
+    while ((all >> shift) + bs > INT32_MAX) ++shift;  // (a request's share is rounded up)
+    return shift;
+}
 __device__ __forceinline__ int tile_cost(int rows, bool shared, int d, bool f16) {
     const int bytes = (d == 128 ? 45 : 16) >> (int)shared;
     return max(bytes, rows <= kFewRows ? 16 : f16 ? 22 : 26);
@@ -382,8 +393,12 @@ __device__ __forceinline__ Cost cost_of(int T, int L, const AttnParams &p, int w
     c.tile[1] = tile_cost(last, rest > kTile, p.d, p.f16);
     c.item[0] = item_cost(kTile) + c.nt * c.tile[0];
     c.item[1] = item_cost(last) + c.nt * c.tile[1];
-    c.head = (c.mi - 1) * c.item[0] + c.item[1];
+    c.head = (long long)(c.mi - 1) * c.item[0] + c.item[1];
     return c;
+}
+// A request's cost, no more than one past what is refused (so that sums of 16000 stay in range).
+__device__ __forceinline__ long long request_cost(int T, int L, const AttnParams &p, int ways) {
+    return T ? min(cost_of(T, L, p, ways).head * p.hkv, kMaxCost + 1) : 0;
 }
 
 // A place on the axis: token tile t of an item.
@@ -447,9 +462,10 @@ __device__ __forceinline__ uint32_t tree_word(const AttnParams &p, const Req &r,
     return lim >= 32 ? x : lim <= 0 ? 0u : x & ((1u << lim) - 1u);
 }
 
-// The place x units of cost along the axis (every CTA rounds it alike).
-// `ahead`: cost before each request, and the total; `tl`: their T and L.
-__device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead, const int2 *tl, int ways, int x) {
+// The place x steps of 2^shift units of cost along the axis (every CTA rounds
+// it alike).  `ahead`: steps before each request, and the total; `tl`: their T
+// and L.
+__device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead, const int2 *tl, int ways, int shift, int x) {
     Place q = {p.bs, 0, 0, 0};
     if (x >= ahead[p.bs]) return q;
     int lo = 0, hi = p.bs;  // the last request with ahead <= x: it has work of its own
@@ -459,11 +475,12 @@ __device__ __forceinline__ Place place_at(const AttnParams &p, const int *ahead,
     }
     const Cost c = cost_of(tl[lo].x, tl[lo].y, p, ways);
     q.b = lo;
-    int y = x - ahead[lo];
-    q.h = y / c.head;
-    y -= q.h * c.head;
-    q.m = min(y / c.item[0], c.mi - 1);
-    y -= q.m * c.item[0];
+    // (without a shift everything fits 32 bits, and the divisions are short)
+    const long long in_request = (long long)(x - ahead[lo]) << shift;
+    q.h = shift ? (int)(in_request / c.head) : (int)in_request / (int)c.head;
+    const long long in_head = in_request - q.h * c.head;
+    q.m = min(shift ? (int)(in_head / c.item[0]) : (int)in_head / c.item[0], c.mi - 1);
+    int y = (int)(in_head - (long long)q.m * c.item[0]);
     const int last = q.m == c.mi - 1, cost = c.tile[last];
     y -= c.item[last] - c.nt * cost;
     q.t = y <= 0 ? 0 : (y + cost - 1) / cost;
@@ -566,48 +583,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     int2 *tl = reinterpret_cast<int2 *>(smem + 512 + ((4 * p.bs + 4 + 15) & ~15));
     Place *ends = reinterpret_cast<Place *>(smem);
     long long all = 0;
-    int ways = 1, lo = 0, slot = 0;  // (the last two of request `tid`)
+    int ways = 1, shift = 0, lo = 0, slot = 0;  // (the last two of request `tid`)
     {
         long long *ws = reinterpret_cast<long long *>(smem + 64);
-        long long shared = 0;  // of two CTAs that walk together
+        long long shared = 0, tot;  // of two CTAs that walk together
         for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
             const int b = b0 + tid;
-            long long n = 0, tot;
+            long long n = 0;
             if (b < p.bs) {
                 int bad;
                 const Req r = load_req(p, b, &bad);
-                if (r.T) {
-                    n = (long long)cost_of(r.T, r.L, p, 1).head * p.hkv;
-                    shared += (long long)cost_of(r.T, r.L, p, 2).head * p.hkv;
-                }
+                n = request_cost(r.T, r.L, p, 1);
+                shared += request_cost(r.T, r.L, p, 2);
                 tl[b] = make_int2(r.T, r.L);
                 if (b0 == 0) lo = r.lo, slot = r.slot;
                 if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
             }
             const long long pre = block_scan_ex(n, ws, &tot);
-            if (b < p.bs) ahead[b] = (int)min(all + pre, (long long)INT32_MAX);
+            if (b < p.bs) ahead[b] = (int)min(all + pre, (long long)INT32_MAX);  // counted again below where that cuts it
             all += tot;
         }
         if (p.num_tokens * p.group > kTile && gridDim.x > 1) {
-            long long tot;
             block_scan_ex(shared, ws, &tot);
-            if (2 * tot < all && all <= INT32_MAX) {
-                ways = 2;
-                all = 0;
-                for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
-                    const int b = b0 + tid;
-                    long long n = 0;
-                    if (b < p.bs && tl[b].x) n = (long long)cost_of(tl[b].x, tl[b].y, p, 2).head * p.hkv;
-                    const long long pre = block_scan_ex(n, ws, &tot);
-                    if (b < p.bs) ahead[b] = (int)(all + pre);
-                    all += tot;
-                }
+            if (2 * tot < all) ways = 2, all = tot;
+        }
+        if (all > kMaxCost) {  // refused
+            if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_CAPACITY);
+            all = 0;
+        } else if (ways == 2 || all > INT32_MAX) {
+            shift = scale_of(all, p.bs);
+            all = 0;
+            for (int b0 = 0; b0 < p.bs; b0 += kAttnThreads) {
+                const int b = b0 + tid;
+                const long long n = b < p.bs ? (request_cost(tl[b].x, tl[b].y, p, ways) + (1ll << shift) - 1) >> shift : 0;
+                const long long pre = block_scan_ex(n, ws, &tot);
+                if (b < p.bs) ahead[b] = (int)(all + pre);
+                all += tot;
             }
         }
-    }
-    if (all > INT32_MAX) {  // more than 32 bits of cost: refused
-        if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_CAPACITY);
-        all = 0;
     }
     if (tid == 0) ahead[p.bs] = (int)all;
     __syncthreads();
@@ -615,7 +628,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     if (lane == 0 && warp < 2) {
         const int parts = gridDim.x >> (ways - 1), q = (int)all / parts, rest = (int)all - q * parts,
                   c = (blockIdx.x >> (ways - 1)) + warp;
-        ends[warp] = place_at(p, ahead, tl, ways, c < parts ? c * q + min(c, rest) : (int)all);
+        ends[warp] = place_at(p, ahead, tl, ways, shift, c < parts ? c * q + min(c, rest) : (int)all);
     }
     if (tid == 0) {
         k.starters[blockIdx.x] = make_int4(-1, 0, 0, 0);
