@@ -93,7 +93,7 @@ struct Shape {
     static constexpr int kTileBytes = kGroups * kGroupBytes;
     static constexpr int kSlotsK = D == 128 ? 2 : 5, kSlotsV = D == 128 ? 3 : 5;  // of the rings
     static constexpr int kRings = (kSlotsK + kSlotsV) * kTileBytes;
-    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1 + kWalks;
+    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1 + 2 * kWalks;
     static constexpr int kQBytes = 32768;               // Q of an item, or 16 rows of it and P^T
     static constexpr int kTiles = 2 * kQBytes + kRings;  // Q of two items, and the rings
     static_assert(kTileBytes <= kQBytes && 8192 + kBufs * 8192 <= kQBytes, "Q and P^T");
@@ -543,10 +543,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBarsAt);
     uint64_t *k_full = bars, *k_empty = k_full + S::kSlotsK, *v_full = k_empty + S::kSlotsK, *v_empty = v_full + S::kSlotsV,
              *s_full = v_empty + S::kSlotsV, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
-             *q_ready = pv_done + kBufs, *walk_full = q_ready + 1;
+             *q_ready = pv_done + kBufs, *walk_full = q_ready + 1, *walk_empty = walk_full + kWalks;
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     int4 *walk_s = reinterpret_cast<int4 *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
-    volatile int *walks_read = reinterpret_cast<volatile int *>(misc + 3);  // by all warps
     // The last item with a non-finite drafted V, of the even and of the odd ones: a softmax warp may be in the
     // next item while another still ends this one (not two on, for a product takes P of all of them).
     volatile int *odd_item = reinterpret_cast<volatile int *>(misc + 4);
@@ -572,10 +571,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_ready, kSoftWarps);
-        for (int i = 0; i < kWalks; ++i) mbar_init(&walk_full[i], 1);
+        for (int i = 0; i < kWalks; ++i) {
+            mbar_init(&walk_full[i], 1);
+            mbar_init(&walk_empty[i], kSoftWarps + 1);
+        }
         fence_mbar_init();
         odd_item[0] = odd_item[1] = -1;
-        *walks_read = 0;
     }
     griddep_wait();
     // The axis: cost ahead of each request, and its T and L, in the tiles' memory.
@@ -665,16 +666,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     const uint32_t tmem = misc[0];
     const uint32_t t_o = tmem + kBufs * 128;
 
+    auto within = [&](uint64_t *bar, uint32_t parity, uint64_t ns) {  // a bounded wait that does not look at the status
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        do {
+            if (mbar_try_wait(bar, parity)) return true;
+        } while (global_ns() - t0 < ns);
+        atomicOr(p.status, kKvStatusTimeout);
+        return false;
+    };
+
     // The next item, from the warp that multiplies Q and K to those that do the rest (none: n = 0), in
-    // one of kWalks places.  Every warp has to come to the same items, also after a wait was given up:
-    // so these two waits do not look at the status, and a place is written again only when all have
-    // read it.  Neither can last, for all other waits are bounded and both sides come here in turn.
+    // one of kWalks places, written again only when every one of them has read it.  Neither wait can last,
+    // for all others are bounded and both sides come here in turn.
     constexpr uint64_t kLong = 20000000000ull;
     auto tell = [&](const Walk &w, int item) {
-        const int at = (item - 1) % kWalks;
+        const int at = (item - 1) % kWalks, round = (item - 1) / kWalks;
         if (lane == 0) {
-            const uint64_t t0 = global_ns();
-            while (*walks_read < (item - kWalks) * (kSoftWarps + 1) && global_ns() - t0 < kLong) {}
+            if (round > 0) within(&walk_empty[at], (round - 1) & 1, kLong);
             walk_s[2 * at] = make_int4(w.r.lo, w.r.T, w.r.L, w.h);
             walk_s[2 * at + 1] = make_int4(w.m, w.t0, w.n, w.nt);
             mbar_arrive(&walk_full[at]);
@@ -682,19 +691,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     };
     auto told = [&](Walk &w, int item) {
         const int at = (item - 1) % kWalks, phase = ((item - 1) / kWalks) & 1;
-        if (!mbar_try_wait(&walk_full[at], phase)) {
-            const uint64_t t0 = global_ns();
-            bool there = false;
-            while (!there && global_ns() - t0 < kLong) there = mbar_try_wait(&walk_full[at], phase);
-            if (!there) {
-                atomicOr(p.status, kKvStatusTimeout);
-                return false;
-            }
-        }
+        if (!__all_sync(kFullMask, within(&walk_full[at], phase, kLong))) return false;
         __syncwarp();
         const int4 a = walk_s[2 * at], b = walk_s[2 * at + 1];
         __syncwarp();
-        if (lane == 0) atomicAdd(const_cast<int *>(walks_read), 1);
+        if (lane == 0) mbar_arrive(&walk_empty[at]);
         w.r.lo = a.x;
         w.r.T = a.y;
         w.r.L = a.z;
