@@ -427,7 +427,9 @@ enum {
     CSGMV_KV_STATUS_CAPACITY = 4,  /* no free pages left, or a row of the page table is full */
     CSGMV_KV_STATUS_BAD_LENS = 8,  /* negative or inconsistent lengths */
     CSGMV_KV_STATUS_BAD_TREE = 16, /* a parent that does not come before its child, or a bad node number */
-    CSGMV_KV_STATUS_BAD_TOKEN = 32 /* a drafted token outside the vocabulary, or a distribution without mass */
+    CSGMV_KV_STATUS_BAD_TOKEN = 32, /* a drafted token outside the vocabulary, or a distribution without mass */
+    CSGMV_KV_STATUS_TIMEOUT = 1 << 30 /* csgmv_tree_attention: a bounded wait inside the kernel ran out, the call's
+                                         results are meaningless; while the bit is set its calls give no output */
 };
 
 /*

@@ -9,7 +9,6 @@
 
 namespace csgmv {
 
-constexpr int kKvStatusTimeout = 1 << 30;  // a bounded wait inside a kernel ran out
 constexpr int kTreeMaxWords = 8;           // mask words of csgmv_build_draft_tree
 
 // csgmv_kv_cache.scratch, in ints: a header of counters, then arrays over

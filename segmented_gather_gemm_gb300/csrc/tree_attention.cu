@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     // (The join is not launched early: its blocks among this kernel's cost 12 us a call.)
     if (smem_u32(smem) & 1023) {  // the swizzled tiles count on it
         if (tid == 0) {
-            atomicOr(p.status, kKvStatusTimeout);
+            atomicOr(p.status, CSGMV_KV_STATUS_TIMEOUT);
             k.starters[blockIdx.x] = make_int4(-1, 0, 0, 0);
         }
         return;
@@ -579,6 +579,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         odd_item[0] = odd_item[1] = -1;
     }
     griddep_wait();
+    // A wait that ran out in an earlier call (or in this one, elsewhere): waits would no longer be sat out.
+    const bool stuck = tid == 0 && (*reinterpret_cast<volatile int32_t *>(p.status) & CSGMV_KV_STATUS_TIMEOUT) != 0;
     // The axis: cost ahead of each request, and its T and L, in the tiles' memory.
     int *ahead = reinterpret_cast<int *>(smem + 512);
     int2 *tl = reinterpret_cast<int2 *>(smem + 512 + ((4 * p.bs + 4 + 15) & ~15));
@@ -623,6 +625,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             }
         }
     }
+    if (__syncthreads_or(stuck)) all = 0;
     if (tid == 0) ahead[p.bs] = (int)all;
     __syncthreads();
     // this CTA's part: two warps find its two ends
@@ -672,7 +675,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         do {
             if (mbar_try_wait(bar, parity)) return true;
         } while (global_ns() - t0 < ns);
-        atomicOr(p.status, kKvStatusTimeout);
+        atomicOr(p.status, CSGMV_KV_STATUS_TIMEOUT);
         return false;
     };
 
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     page = p.num_pages;  // past the pool: zeros
                 }
                 const int rg = g & ((1 << gpp_shift) - 1);
-                mbar_wait(&empty[s], phase ^ 1, p.status, kKvStatusTimeout);
+                mbar_wait(&empty[s], phase ^ 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
                 __syncwarp();
                 const uint32_t dst = ring + s * S::kTileBytes + lane * S::kGroupBytes;
@@ -779,14 +782,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             more = wn.next(p, ways);
             const int gall = w.r.groups();
             const bool few = w.rows(p) <= kFewRows;
-            if (item == 0) mbar_wait(q_ready, 0, p.status, kKvStatusTimeout);  // the softmax warps fetch the first
+            if (item == 0) mbar_wait(q_ready, 0, p.status, CSGMV_KV_STATUS_TIMEOUT);  // the softmax warps fetch the first
             else q_landed();
             __syncwarp();
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
                 const int s = it % S::kSlotsK, buf = it % kBufs;
                 // what the buffer held has been read, and P that lay in its place multiplied
-                if (it >= kBufs) mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
-                mbar_wait(&k_full[s], (it / S::kSlotsK) & 1, p.status, kKvStatusTimeout);
+                if (it >= kBufs) mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
+                mbar_wait(&k_full[s], (it / S::kSlotsK) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 __syncwarp();
                 tc_fence_after();
                 const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (more && t == w.t0 + min(2, w.n - 1)) {
                     // Q of the next item, where Q and P^T of the one before were: its last product is done
                     const int last = it - (t - w.t0) - 1;
-                    if (last >= 0) mbar_wait(&pv_done[last % kBufs], (last / kBufs) & 1, p.status, kKvStatusTimeout);
+                    if (last >= 0) mbar_wait(&pv_done[last % kBufs], (last / kBufs) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                     fetch_q<D>(p, wn, q_s + ((item + 1) & 1) * S::kQBytes, lane, 32);
                 }
             }
@@ -831,8 +834,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             const bool few = w.rows(p) <= kFewRows;
             for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
                 const int s = it % S::kSlotsV, buf = it % kBufs;
-                mbar_wait(&v_full[s], (it / S::kSlotsV) & 1, p.status, kKvStatusTimeout);
-                mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&v_full[s], (it / S::kSlotsV) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
+                mbar_wait(&p_ready[buf], (it / kBufs) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 __syncwarp();
                 tc_fence_after();
                 const int steps = (min(kGroups, gall - t * kGroups) + 1) >> 1;  // of 16 tokens
@@ -884,14 +887,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             auto keys_of = [&](int t) { return ((min(kGroups, gall - t * kGroups) + 1) >> 1) * 16; };
             auto edge = [&](int t) { return (t + 1) * kTile > w.r.L; };  // holds more than cached tokens
             auto await_s = [&]() {
-                mbar_wait(&s_full[it % kBufs], (it / kBufs) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&s_full[it % kBufs], (it / kBufs) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 __syncwarp();
                 tc_fence_after();
             };
             // (A warp may get here before another has P of the tile before last ready: the barrier is
             // the buffer's own, so the parity cannot be that of an older product.)
             auto await_pv = [&]() {  // of the tile before
-                mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&pv_done[(it - 1) % kBufs], ((it - 1) / kBufs) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 __syncwarp();
                 tc_fence_after();
             };
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             // rows that see it.
             auto clean_v = [&](int t) {
                 const int sv = it % S::kSlotsV;
-                mbar_wait(&v_full[sv], (it / S::kSlotsV) & 1, p.status, kKvStatusTimeout);
+                mbar_wait(&v_full[sv], (it / S::kSlotsV) & 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                 const int r0 = max(w.r.L - t * kTile, 0), n = (keys_of(t) - r0) * (D / 8);
                 for (int i = tid; i < n; i += kSoftWarps * 32) {
                     const int r = r0 + i / (D / 8), y = i % (D / 8), jt = t * kTile + r - gctx * 8;
@@ -1024,7 +1027,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                             low[i] = pack2_rest<F16>(hi[i], e[0], e[1]);
                         }
                         if (it >= kBufs)  // the product before in this buffer
-                            mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, kKvStatusTimeout);
+                            mbar_wait(&pv_done[buf], ((it / kBufs) & 1) ^ 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
                         // P^T: 64 bytes a token, high parts of 16 rows, then the low parts; 64-byte swizzle
                         const uint32_t a = smem_u32(q_s) + (item & 1) * S::kQBytes + 8192 + buf * 8192 + pos * 64, x = (pos >> 1) & 3;
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a + ((half ^ x) << 4)), "r"(hi[0]), "r"(hi[1]),
