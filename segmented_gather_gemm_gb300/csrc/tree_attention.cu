@@ -93,7 +93,7 @@ struct Shape {
     static constexpr int kTileBytes = kGroups * kGroupBytes;
     static constexpr int kSlotsK = D == 128 ? 2 : 5, kSlotsV = D == 128 ? 3 : 5;  // of the rings
     static constexpr int kRings = (kSlotsK + kSlotsV) * kTileBytes;
-    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1 + 2 * kWalks;
+    static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 1 + 2 * kWalks + 2;
     static constexpr int kQBytes = 32768;               // Q of an item, or 16 rows of it and P^T
     static constexpr int kTiles = 2 * kQBytes + kRings;  // Q of two items, and the rings
     static_assert(kTileBytes <= kQBytes && 8192 + kBufs * 8192 <= kQBytes, "Q and P^T");
@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBarsAt);
     uint64_t *k_full = bars, *k_empty = k_full + S::kSlotsK, *v_full = k_empty + S::kSlotsK, *v_empty = v_full + S::kSlotsV,
              *s_full = v_empty + S::kSlotsV, *p_ready = s_full + kBufs, *pv_done = p_ready + kBufs,
-             *q_ready = pv_done + kBufs, *walk_full = q_ready + 1, *walk_empty = walk_full + kWalks;
+             *q_ready = pv_done + kBufs, *walk_full = q_ready + 1, *walk_empty = walk_full + kWalks,
+             *drained = walk_empty + kWalks;
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + S::kBars + 1);
     int4 *walk_s = reinterpret_cast<int4 *>(smem + S::kTiles + S::kRedBytes + S::kFlagBytes);
     // The last item with a non-finite drafted V, of the even and of the odd ones: a softmax warp may be in the
@@ -575,6 +576,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             mbar_init(&walk_full[i], 1);
             mbar_init(&walk_empty[i], kSoftWarps + 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&drained[i], 1);
         fence_mbar_init();
         odd_item[0] = odd_item[1] = -1;
     }
@@ -669,6 +671,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
     const uint32_t tmem = misc[0];
     const uint32_t t_o = tmem + kBufs * 128;
 
+    // After a wait that ran out (status bit TIMEOUT, results meaningless) every warp still comes to the same
+    // items and meets every barrier that others wait at.  But a warp whose loads have no place to go stops
+    // them (also when the place is free by the barriers' count and what it held has not landed), and the
+    // warps of loads and products wait in the end for what they have in flight: nothing may write to shared
+    // or tensor memory that the CTA has given back.
+    constexpr uint64_t kDrain = 2000000000ull;
     auto within = [&](uint64_t *bar, uint32_t parity, uint64_t ns) {  // a bounded wait that does not look at the status
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = global_ns();
@@ -736,7 +744,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
         int s = 0, phase = 0;  // of the ring
         Walk w = w0, wn = w0;
         int page = page_of(w, w.t0);
-        bool more;
+        bool more, on = true;
         do {
             more = wn.next(p, ways);  // looked up while this segment's tiles are loaded
             const int gctx = w.r.ctx_groups(), gall = w.r.groups();
@@ -751,7 +759,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                     page = p.num_pages;  // past the pool: zeros
                 }
                 const int rg = g & ((1 << gpp_shift) - 1);
-                mbar_wait(&empty[s], phase ^ 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
+                on = mbar_wait(&empty[s], phase ^ 1, p.status, CSGMV_KV_STATUS_TIMEOUT);
+                on &= mbar_try_wait(&full[s], phase ^ 1);  // (so it is, but for waits that ran out)
+                if (!(on = __all_sync(kFullMask, on))) break;
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)ng * S::kGroupBytes);
                 __syncwarp();
                 const uint32_t dst = ring + s * S::kTileBytes + lane * S::kGroupBytes;
@@ -768,7 +778,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 if (++s == slots) s = 0, phase ^= 1;
             }
             w = wn;
-        } while (more);
+        } while (more && on);
+        // each place's last load (of this round, or of the one before)
+        for (int i = 0; i < slots; ++i) within(&full[i], i < s ? phase : phase ^ 1, kDrain);
     } else if (warp == kWarpS) {
         // ------------------------------------------------ products: S = Q K^T
         const uint32_t lead = elect_lead();
@@ -822,6 +834,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             if (!more) w.n = 0;
             tell(w, item);
         } while (more);
+        commit_one(lead, &drained[0]);
+        within(&drained[0], 0, kDrain);
     } else if (warp == kWarpO) {
         // ------------------------------------------------ products: O += P V
         const uint32_t lead = elect_lead();
@@ -863,6 +877,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
                 commit_one(lead, &pv_done[buf]);
             }
         } while (told(w, ++item));
+        commit_one(lead, &drained[1]);
+        within(&drained[1], 0, kDrain);
     } else {
         // ---------------------------------------------------------- softmax
         // warps w and w + 4 share 32 lanes (a quadrant)
