@@ -435,6 +435,16 @@ def _raw_stream(stream, device: int):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _empty(stream, *size, **kw) -> torch.Tensor:
+    """torch.empty for a call on `stream` (None: the current one).  The memory
+    belongs to that stream: another one's could still be in use by what was
+    put on that one before, and be given out again there while the call runs."""
+    if stream is None:
+        return torch.empty(*size, **kw)
+    with torch.cuda.stream(stream):
+        return torch.empty(*size, **kw)
+
+
 def _alike(a: torch.Tensor, b: torch.Tensor) -> bool:
     """Same shape and the same strides where they matter."""
     return a.shape == b.shape and (a.stride() == b.stride() or a.numel() == 0 or all(
@@ -585,7 +595,8 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     """Attention of request b's rows of q (tokens, heads, head_dim) over its
     cached sequence and over its own rows of k_new / v_new that `mask` (int32
     bits, (tokens, words); None: causal) lets each row see.  scale defaults to
-    head_dim ** -0.5; lse (tokens, heads) f32 is optional."""
+    head_dim ** -0.5; lse (tokens, heads) f32 is optional.  A workspace that is
+    not given is allocated on the call's stream."""
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     if len(shape) != 3 or out.shape != shape:
         raise CsgmvError(-1, "q and out must be (tokens, heads, head_dim)")
@@ -607,7 +618,7 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         if not lse.is_contiguous():
             raise CsgmvError(-1, "lse must be contiguous")
     if workspace is None:
-        workspace = torch.empty(csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
     rc = lib().csgmv_tree_attention(
         q.data_ptr(), qs[0], qs[1], hq, k_new.data_ptr(), v_new.data_ptr(), ks[0], ks[1], cache._ref, layer,
         tree_indptr.data_ptr(), _at(seq_slots), bs, n, _at(mask), words, d ** -0.5 if scale is None else scale,
@@ -657,7 +668,8 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
                         draft_probs: torch.Tensor | None = None, accept_index: torch.Tensor | None = None,
                         accept_len: torch.Tensor | None = None, next_token: torch.Tensor | None = None, stream=None):
     """Walks each tree: (accept_index (bs, width), accept_len (bs,), next_token
-    (bs,)), allocated unless given; width defaults to tree.max_draft.
+    (bs,)), allocated (on the call's stream) unless given; width defaults to
+    tree.max_draft.
     draft_probs None: the drafts were chosen, not sampled."""
     n, bs = draft_tokens.numel(), tree_indptr.numel() - 1
     _need_f32("target_probs", target_probs, n, None)
@@ -682,14 +694,14 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
         raise CsgmvError(-1, f"{n} nodes exceed the tree's {tree.max_nodes}")
     width = tree.max_draft if accept_index is None else accept_index.shape[-1]
     if accept_index is None and accept_len is None and next_token is None:  # one buffer for all
-        accept_index, accept_len, next_token = torch.empty(
-            bs * (width + 2), dtype=torch.int32, device=target_probs.device).split_with_sizes([bs * width, bs, bs])
+        accept_index, accept_len, next_token = _empty(
+            stream, bs * (width + 2), dtype=torch.int32, device=target_probs.device).split_with_sizes([bs * width, bs, bs])
         accept_index = accept_index.view(bs, width)
     else:
         new = dict(dtype=torch.int32, device=target_probs.device)
-        accept_index = torch.empty((bs, width), **new) if accept_index is None else accept_index
-        accept_len = torch.empty(bs, **new) if accept_len is None else accept_len
-        next_token = torch.empty(bs, **new) if next_token is None else next_token
+        accept_index = _empty(stream, (bs, width), **new) if accept_index is None else accept_index
+        accept_len = _empty(stream, bs, **new) if accept_len is None else accept_len
+        next_token = _empty(stream, bs, **new) if next_token is None else next_token
         _need_i32("accept_index", accept_index, bs, width)
         _need_i32("accept_len", accept_len, bs)
         _need_i32("next_token", next_token, bs)
