@@ -399,17 +399,17 @@ def _need(ok: bool, msg: str):
         raise CsgmvError(-1, msg)
 
 
-def _need_i32(name: str, t: torch.Tensor | None, *shape):
-    """t is a dense int32 tensor on a GPU of that shape (None: any extent)."""
-    if t is not None and (t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or
+def _need_i32(device: int, name: str, t: torch.Tensor | None, *shape):
+    """t is a dense int32 tensor on that GPU, of that shape (None: any extent)."""
+    if t is not None and (t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous() or
                           not _has_shape(t.shape, shape)):
-        raise CsgmvError(-1, f"{name} must be a contiguous int32 CUDA tensor of shape {shape}, "
+        raise CsgmvError(-1, f"{name} must be a contiguous int32 tensor of shape {shape} on cuda:{device}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _need_f32(name: str, t: torch.Tensor, *shape):
-    if t.dtype is not torch.float32 or not t.is_cuda or not _has_shape(t.shape, shape):
-        raise CsgmvError(-1, f"{name} must be a float32 CUDA tensor of shape {shape}, "
+def _need_f32(device: int, name: str, t: torch.Tensor, *shape):
+    if t.dtype is not torch.float32 or t.get_device() != device or not _has_shape(t.shape, shape):
+        raise CsgmvError(-1, f"{name} must be a float32 tensor of shape {shape} on cuda:{device}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -427,8 +427,14 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _raw_stream(stream, device: int):
-    """The CUDA stream handle to launch on: stream, or the device's current one."""
+    """The CUDA stream handle to launch on: stream, or the device's current one.
+    The library launches on the current device, so that has to be the operands'
+    (a handle does not say: the default stream's is 0 on every device)."""
+    if torch.cuda.current_device() != device:
+        raise CsgmvError(-1, f"the operands are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is not None:
+        if stream.device_index != device:
+            raise CsgmvError(-1, f"the operands are on cuda:{device}, the stream is on cuda:{stream.device_index}")
         return stream.cuda_stream
     if _current_raw_stream is not None:
         return _current_raw_stream(device)
@@ -470,15 +476,17 @@ class KvCache:
         _need(k_pages.dtype in _KV_DTYPES and v_pages.dtype == k_pages.dtype, "k_pages / v_pages must be bf16 or f16, both alike")
         _need(k_pages.dim() == 5 and _alike(k_pages, v_pages),
               "k_pages / v_pages must have five dimensions and the same shape and strides")
-        _need(k_pages.is_cuda and v_pages.is_cuda, "k_pages / v_pages must be CUDA tensors")
+        _need(k_pages.is_cuda and v_pages.get_device() == k_pages.get_device(),
+              "k_pages / v_pages must be CUDA tensors on one device")
         _need(k_pages.stride(4) == 1, "the last dimension of k_pages / v_pages must be dense")
         h, t = (2, 3) if layout == "HND" else (3, 2)
         layers, pages, heads, ps, d = (int(k_pages.shape[i]) for i in (0, 1, h, t, 4))
+        at = k_pages.get_device()
         _need(page_table.dim() == 2, "page_table must have two dimensions")
         seqs, max_pages = (int(n) for n in page_table.shape)
-        _need_i32("page_table", page_table, seqs, max_pages)
-        _need_i32("seq_lens", seq_lens, seqs)
-        _need_i32("page_refs", page_refs, pages)
+        _need_i32(at, "page_table", page_table, seqs, max_pages)
+        _need_i32(at, "seq_lens", seq_lens, seqs)
+        _need_i32(at, "page_refs", page_refs, pages)
         self.k_pages, self.v_pages = k_pages, v_pages
         self.page_table, self.seq_lens, self.page_refs = page_table, seq_lens, page_refs
         self.layout = layout
@@ -494,7 +502,7 @@ class KvCache:
         c.num_kv_heads, c.head_dim, c.max_seqs, c.max_pages_per_seq = heads, d, seqs, max_pages
         self.c = c
         self._ref = ctypes.byref(c)
-        self.dtype, self.device = k_pages.dtype, k_pages.get_device()
+        self.dtype, self.device = k_pages.dtype, at
         self.num_layers, self.num_pages, self.page_size = layers, pages, ps
         self.num_kv_heads, self.head_dim, self.max_seqs, self.max_pages_per_seq = heads, d, seqs, max_pages
         self.row_shape = (heads, d)
@@ -526,8 +534,8 @@ def _new_rows(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, lead: tu
                              f"dimension dense, not {tuple(k_new.shape)}")
     if v_new.shape != want or v_new.stride() != st and not _alike(k_new, v_new):
         raise CsgmvError(-1, "k_new / v_new must have the same shape and strides")
-    if not (k_new.dtype is v_new.dtype is cache.dtype and k_new.is_cuda and v_new.is_cuda):
-        raise CsgmvError(-1, "k_new / v_new must be CUDA tensors of the cache's type")
+    if not (k_new.dtype is v_new.dtype is cache.dtype and k_new.get_device() == v_new.get_device() == cache.device):
+        raise CsgmvError(-1, "k_new / v_new must be CUDA tensors of the cache's type, on its device")
     return st
 
 
@@ -540,12 +548,12 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
     st = _new_rows(cache, k_new, v_new, (cache.num_layers, k_new.shape[1]))
     bs = accept_len.numel()
     width = 0 if accept_index is None else accept_index.shape[-1]
-    _need_i32("accept_len", accept_len, bs)
+    _need_i32(cache.device, "accept_len", accept_len, bs)
     if accept_index is not None:
-        _need_i32("accept_index", accept_index, bs, width)
-    _need_i32("tree_indptr", tree_indptr, bs + 1)
+        _need_i32(cache.device, "accept_index", accept_index, bs, width)
+    _need_i32(cache.device, "tree_indptr", tree_indptr, bs + 1)
     if seq_slots is not None:
-        _need_i32("seq_slots", seq_slots, bs)
+        _need_i32(cache.device, "seq_slots", seq_slots, bs)
     rc = lib().csgmv_kv_commit(cache._ref, k_new.data_ptr(), v_new.data_ptr(), st[0], st[1], st[2], k_new.shape[1],
                                _at(accept_index), width, accept_len.data_ptr(), tree_indptr.data_ptr(),
                                _at(seq_slots), bs, _raw_stream(stream, cache.device))
@@ -556,8 +564,8 @@ def csgmv_kv_commit(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, ac
 def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
     """Sequence children[i] becomes a copy of sequence parents[i]."""
     n = parents.numel()
-    _need_i32("parents", parents, n)
-    _need_i32("children", children, n)
+    _need_i32(cache.device, "parents", parents, n)
+    _need_i32(cache.device, "children", children, n)
     _check(lib().csgmv_kv_fork(cache._ref, parents.data_ptr(), children.data_ptr(), n,
                                _raw_stream(stream, cache.device)))
 
@@ -565,8 +573,8 @@ def csgmv_kv_fork(cache: KvCache, parents: torch.Tensor, children: torch.Tensor,
 def csgmv_kv_free(cache: KvCache, seqs: torch.Tensor, keep_lens: torch.Tensor | None = None, stream=None) -> None:
     """Cuts sequence seqs[i] back to keep_lens[i] tokens (None: to nothing)."""
     n = seqs.numel()
-    _need_i32("seqs", seqs, n)
-    _need_i32("keep_lens", keep_lens, n)
+    _need_i32(cache.device, "seqs", seqs, n)
+    _need_i32(cache.device, "keep_lens", keep_lens, n)
     _check(lib().csgmv_kv_free(cache._ref, seqs.data_ptr(), _at(keep_lens), n, _raw_stream(stream, cache.device)))
 
 
@@ -578,8 +586,8 @@ def csgmv_kv_compact(cache: KvCache, stream=None) -> None:
 def csgmv_kv_copy_pages(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Copies the contents of pages src[i] to pages dst[i] in every layer."""
     n = src.numel()
-    _need_i32("src", src, n)
-    _need_i32("dst", dst, n)
+    _need_i32(cache.device, "src", src, n)
+    _need_i32(cache.device, "dst", dst, n)
     _check(lib().csgmv_kv_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), n, _raw_stream(stream, cache.device)))
 
 
@@ -600,25 +608,27 @@ def csgmv_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     if len(shape) != 3 or out.shape != shape:
         raise CsgmvError(-1, "q and out must be (tokens, heads, head_dim)")
-    if not (q.dtype is out.dtype is cache.dtype and q.is_cuda and out.is_cuda):
-        raise CsgmvError(-1, "q and out must be CUDA tensors of the cache's type")
+    if not (q.dtype is out.dtype is cache.dtype and q.get_device() == out.get_device() == cache.device):
+        raise CsgmvError(-1, "q and out must be CUDA tensors of the cache's type, on its device")
     n, hq, d = shape
     if d != cache.head_dim or n and (qs[2] != 1 or os_[2] != 1):
         raise CsgmvError(-1, "q and out must have the cache's head_dim, dense")
     ks = _new_rows(cache, k_new, v_new, (n,))
     bs, words = tree_indptr.shape[0] - 1 if tree_indptr.dim() else 0, 0
-    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need_i32(cache.device, "tree_indptr", tree_indptr, bs + 1)
     if mask is not None:
         words = mask.shape[-1]
-        _need_i32("mask", mask, n, words)
+        _need_i32(cache.device, "mask", mask, n, words)
     if seq_slots is not None:
-        _need_i32("seq_slots", seq_slots, bs)
+        _need_i32(cache.device, "seq_slots", seq_slots, bs)
     if lse is not None:
-        _need_f32("lse", lse, n, hq)
+        _need_f32(cache.device, "lse", lse, n, hq)
         if not lse.is_contiguous():
             raise CsgmvError(-1, "lse must be contiguous")
     if workspace is None:
         workspace = _empty(stream, csgmv_tree_attention_workspace_bytes(cache, hq), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != cache.device or not workspace.is_contiguous():
+        raise CsgmvError(-1, "the workspace must be a contiguous tensor on the cache's device")
     rc = lib().csgmv_tree_attention(
         q.data_ptr(), qs[0], qs[1], hq, k_new.data_ptr(), v_new.data_ptr(), ks[0], ks[1], cache._ref, layer,
         tree_indptr.data_ptr(), _at(seq_slots), bs, n, _at(mask), words, d ** -0.5 if scale is None else scale,
@@ -653,8 +663,8 @@ def csgmv_build_draft_tree(tree: DraftTree, parents: torch.Tensor, tree_indptr: 
     """Fills tree.mask, depth, first_child and next_sibling from the nodes'
     parents (numbers inside their request, -1 at its node 0)."""
     n, bs = parents.numel(), tree_indptr.numel() - 1
-    _need_i32("parents", parents, n)
-    _need_i32("tree_indptr", tree_indptr, bs + 1)
+    _need_i32(tree.device, "parents", parents, n)
+    _need_i32(tree.device, "tree_indptr", tree_indptr, bs + 1)
     if n > tree.max_nodes:
         raise CsgmvError(-1, f"{n} nodes exceed the tree's {tree.max_nodes}")
     rc = lib().csgmv_build_draft_tree(parents.data_ptr(), tree_indptr.data_ptr(), bs, n, tree.words, *tree._at,
@@ -672,22 +682,22 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
     tree.max_draft.
     draft_probs None: the drafts were chosen, not sampled."""
     n, bs = draft_tokens.numel(), tree_indptr.numel() - 1
-    _need_f32("target_probs", target_probs, n, None)
+    _need_f32(tree.device, "target_probs", target_probs, n, None)
     ts, vocab = target_probs.stride(), target_probs.shape[1]
     if n and ts[1] != 1:
         raise CsgmvError(-1, "target_probs must have dense rows")
     # the row stride of a single row says nothing
     ts, ds = ts[0] if n > 1 else vocab, 0
     if draft_probs is not None:
-        _need_f32("draft_probs", draft_probs, n, vocab)
+        _need_f32(tree.device, "draft_probs", draft_probs, n, vocab)
         ds = draft_probs.stride()
         if n and ds[1] != 1:
             raise CsgmvError(-1, "draft_probs must have dense rows")
         ds = ds[0] if n > 1 else vocab
-    _need_i32("draft_tokens", draft_tokens, n)
-    _need_i32("tree_indptr", tree_indptr, bs + 1)
-    _need_f32("accept_uniforms", accept_uniforms, n)
-    _need_f32("sample_uniforms", sample_uniforms, bs)
+    _need_i32(tree.device, "draft_tokens", draft_tokens, n)
+    _need_i32(tree.device, "tree_indptr", tree_indptr, bs + 1)
+    _need_f32(tree.device, "accept_uniforms", accept_uniforms, n)
+    _need_f32(tree.device, "sample_uniforms", sample_uniforms, bs)
     if not (accept_uniforms.is_contiguous() and sample_uniforms.is_contiguous()):
         raise CsgmvError(-1, "the uniform numbers must be contiguous")
     if n > tree.max_nodes:
@@ -702,9 +712,9 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
         accept_index = _empty(stream, (bs, width), **new) if accept_index is None else accept_index
         accept_len = _empty(stream, bs, **new) if accept_len is None else accept_len
         next_token = _empty(stream, bs, **new) if next_token is None else next_token
-        _need_i32("accept_index", accept_index, bs, width)
-        _need_i32("accept_len", accept_len, bs)
-        _need_i32("next_token", next_token, bs)
+        _need_i32(tree.device, "accept_index", accept_index, bs, width)
+        _need_i32(tree.device, "accept_len", accept_len, bs)
+        _need_i32(tree.device, "next_token", next_token, bs)
     rc = lib().csgmv_verify_drafts(
         target_probs.data_ptr(), ts, _at(draft_probs), ds, draft_tokens.data_ptr(), tree_indptr.data_ptr(), tree._at[2],
         tree._at[3], accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), bs, n, vocab, accept_index.data_ptr(), width,
