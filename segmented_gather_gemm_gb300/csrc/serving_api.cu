@@ -1,6 +1,7 @@
 // C ABI of the serving step's operators: argument checks on the host, then
 // the launches of each call on the caller's stream.  Nothing here allocates,
 // frees or synchronizes.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 
@@ -30,6 +31,23 @@ bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
     if (!a || !b || !abytes || !bbytes) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return a0 < b0 + bbytes && b0 < a0 + abytes;
+}
+
+struct Dim {
+    int64_t extent, stride;
+};
+// Whether no two elements of an array of dense rows of `row` share a place:
+// each dimension steps over all that those of shorter strides reach.
+template <int N>
+bool apart(int64_t row, Dim (&&dims)[N]) {
+    std::sort(dims, dims + N, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    int64_t span = row;
+    for (const Dim &d : dims) {
+        if (d.extent <= 1) continue;
+        if (d.stride < span || d.stride > (INT64_MAX - span) / (d.extent - 1)) return false;
+        span += (d.extent - 1) * d.stride;
+    }
+    return true;
 }
 
 // The cache's bookkeeping steers every kernel's addresses: nothing a call
@@ -75,7 +93,11 @@ int check_kv(const csgmv_kv_cache *kv) {
                            kv->page_stride >= (H - 1) * kv->head_stride + (P - 1) * kv->token_stride + D;
     const bool heads_in = kv->head_stride >= D && kv->token_stride >= (H - 1) * kv->head_stride + D &&
                           kv->page_stride >= (P - 1) * kv->token_stride + (H - 1) * kv->head_stride + D;
-    if (!heads_out && !heads_in) return fail(CSGMV_ERR_INVALID_ARG, "kv cache strides overlap");
+    if ((!heads_out && !heads_in) || !apart(D, {{kv->num_layers, kv->layer_stride},
+                                                {kv->num_pages, kv->page_stride},
+                                                {H, kv->head_stride},
+                                                {P, kv->token_stride}}))
+        return fail(CSGMV_ERR_INVALID_ARG, "kv cache strides overlap");
     return CSGMV_OK;
 }
 

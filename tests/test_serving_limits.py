@@ -3,7 +3,7 @@ kernels' arithmetic holds, and buffers that steer a kernel apart from what it
 writes.  CPU only: no kernel runs."""
 import pytest
 
-from tests.test_serving_abi import INVALID, P, UNSUPPORTED, attend, cache, lib  # noqa: F401
+from tests.test_serving_abi import INVALID, UNSUPPORTED, attend, cache, commit, lib  # noqa: F401
 
 
 def test_rows_of_a_kv_head_fit_30_bits(lib):  # noqa: F811
@@ -13,3 +13,22 @@ def test_rows_of_a_kv_head_fit_30_bits(lib):  # noqa: F811
     assert attend(lib, cache(), n=most, hq=2 * 65) == UNSUPPORTED and b"2^30" in lib.csgmv_last_error()
     # 64 of them fit: refused for the next thing that is wrong
     assert attend(lib, cache(), n=most, hq=2 * 64, q=None) == INVALID and b"NULL" in lib.csgmv_last_error()
+
+
+@pytest.mark.parametrize("kw,ok", [
+    (dict(layer_stride=0), False), (dict(layer_stride=8), False), (dict(layer_stride=2048), False),
+    (dict(layer_stride=15 * 2048), False), (dict(layer_stride=16 * 2048), True), (dict(layer_stride=17 * 2048 + 8), True),
+    (dict(layer_stride=2048, page_stride=4 * 2048), True),  # layers inside pages
+    (dict(layer_stride=2048, page_stride=3 * 2048), False), (dict(layer_stride=2040, page_stride=4 * 2048), False),
+    (dict(layer_stride=1024, head_stride=4 * 1024, page_stride=8 * 1024), True),  # inside heads
+    (dict(layer_stride=64, token_stride=4 * 64, head_stride=4096, page_stride=8192), True),  # inside tokens
+    (dict(layer_stride=0, num_layers=1), True), (dict(layer_stride=8, num_layers=1), True),
+    (dict(layer_stride=1 << 62), False),  # past 64 bits
+])
+def test_layers_of_a_cache_keep_to_themselves(lib, kw, ok):  # noqa: F811
+    """Calls copy all layers at once: two layers that share memory would leave
+    there whichever comes last."""
+    c = cache(**kw)
+    # what is right is refused for the next thing: a negative number of requests
+    assert commit(lib, c, bs=-1) == INVALID
+    assert (b"overlap" in lib.csgmv_last_error()) is not ok
