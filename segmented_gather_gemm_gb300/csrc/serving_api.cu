@@ -231,14 +231,23 @@ int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     const size_t need = csgmv::attn_workspace_bytes(kv->head_dim);
     if (need && (!workspace || !aligned16(workspace)))
         return fail(CSGMV_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
-    if (workspace_bytes < need)
-        return fail(CSGMV_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (!apart(kv->head_dim, {{num_tokens, out_token_stride}, {num_q_heads, out_head_stride}}))
+        return fail(CSGMV_ERR_INVALID_ARG, "out strides overlap");
+    // what steers the kernels' addresses and barriers, and what they write
+    const size_t lse_bytes = 4 * (size_t)num_tokens * num_q_heads, ptr_bytes = 4 * (size_t)(bs + 1), slot_bytes = 4 * (size_t)bs;
     const size_t out_bytes =
         2 * ((size_t)(num_tokens - 1) * out_token_stride + (size_t)(num_q_heads - 1) * out_head_stride + kv->head_dim);
-    if (overlaps_meta(kv, out, out_bytes) || overlaps_meta(kv, lse, 4 * (size_t)num_tokens * num_q_heads) ||
-        overlaps_meta(kv, workspace, need) || overlaps(tree_indptr, 4 * (size_t)(bs + 1), out, out_bytes) ||
-        overlaps(workspace, need, out, out_bytes))
-        return fail(CSGMV_ERR_INVALID_ARG, "out / lse / workspace overlaps the cache's bookkeeping, tree_indptr or each other");
+    const struct { const void *at; size_t bytes; } written[] = {{out, out_bytes}, {lse, lse_bytes}, {workspace, need}};
+    bool over = overlaps(out, out_bytes, lse, lse_bytes) || overlaps(out, out_bytes, workspace, need) ||
+                overlaps(lse, lse_bytes, workspace, need);
+    for (const auto &w : written)
+        over = over || overlaps_meta(kv, w.at, w.bytes) || overlaps(tree_indptr, ptr_bytes, w.at, w.bytes) ||
+               overlaps(seq_slots, slot_bytes, w.at, w.bytes);
+    if (over)
+        return fail(CSGMV_ERR_INVALID_ARG,
+                    "out / lse / workspace overlaps the cache's bookkeeping, tree_indptr, seq_slots or each other");
+    if (workspace_bytes < need)
+        return fail(CSGMV_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     csgmv::AttnParams p = {};
     p.q = static_cast<const uint16_t *>(q);
     p.k_new = static_cast<const uint16_t *>(k_new);

@@ -1,9 +1,11 @@
 """Host checks of the serving operators' C calls that keep sizes within what the
 kernels' arithmetic holds, and buffers that steer a kernel apart from what it
 writes.  CPU only: no kernel runs."""
+import ctypes
+
 import pytest
 
-from tests.test_serving_abi import INVALID, UNSUPPORTED, attend, cache, commit, lib  # noqa: F401
+from tests.test_serving_abi import CAPACITY, INVALID, P, UNSUPPORTED, attend, cache, commit, lib  # noqa: F401
 
 
 def test_rows_of_a_kv_head_fit_30_bits(lib):  # noqa: F811
@@ -31,4 +33,28 @@ def test_layers_of_a_cache_keep_to_themselves(lib, kw, ok):  # noqa: F811
     c = cache(**kw)
     # what is right is refused for the next thing: a negative number of requests
     assert commit(lib, c, bs=-1) == INVALID
+    assert (b"overlap" in lib.csgmv_last_error()) is not ok
+
+
+@pytest.mark.parametrize("kw,ok", [
+    (dict(), True),
+    # written over by one another, or over what the kernels find their way by
+    (dict(lse=0x80000000), False), (dict(lse=0x80000000 - 64), False), (dict(lse=0x40000000 + 512), False),
+    (dict(lse=P), False), (dict(ws=P - 4096), False), (dict(out=P - 128), False),
+    (dict(out=0x50000000 - 64), False), (dict(lse=0x50000000), False), (dict(ws=0x50000000 - 65536), False),
+    (dict(lse=0x50000010), True),  # right behind the four slots
+    # rows of the output in one another
+    (dict(ots=0), False), (dict(ohs=0), False), (dict(ohs=56), False), (dict(ots=504), False), (dict(ots=64, ohs=2048), True),
+    (dict(ots=64, ohs=2040), False), (dict(n=1, ots=0), True), (dict(ots=1 << 62), False),
+])
+def test_attention_writes_apart_from_what_steers_it(lib, kw, ok):  # noqa: F811
+    a = dict(q=P, qts=512, qhs=64, hq=8, k=P, v=P, nts=128, nhs=64, layer=0, indptr=P, slots=0x50000000, bs=4, n=32, mask=P,
+             words=1, scale=0.125, out=0x40000000, ots=512, ohs=64, lse=0x60000000, ws=0x80000000)
+    a.update(kw)
+    c = cache()
+    short = lib.csgmv_tree_attention_workspace_bytes(ctypes.byref(c), 8) - 1  # refused last: nothing is launched here
+    rc = lib.csgmv_tree_attention(a["q"], a["qts"], a["qhs"], a["hq"], a["k"], a["v"], a["nts"], a["nhs"], ctypes.byref(c),
+                                  a["layer"], a["indptr"], a["slots"], a["bs"], a["n"], a["mask"], a["words"], a["scale"],
+                                  a["out"], a["ots"], a["ohs"], a["lse"], a["ws"], short, None)
+    assert rc == (CAPACITY if ok else INVALID)
     assert (b"overlap" in lib.csgmv_last_error()) is not ok
