@@ -322,6 +322,17 @@ int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const 
         return fail(CSGMV_ERR_INVALID_ARG, "target_probs / draft_probs must be 4-byte aligned");
     if (target_stride < vocab_size || (draft_probs && draft_stride < vocab_size))
         return fail(CSGMV_ERR_INVALID_ARG, "target_stride / draft_stride below vocab_size");
+    // a request's CTAs walk its tree each by itself and meet at cluster barriers: what they read must not change
+    const size_t n4 = 4 * (size_t)num_nodes, b4 = 4 * (size_t)bs;
+    auto rows = [&](int64_t stride) { return num_nodes ? 4 * ((size_t)(num_nodes - 1) * stride + vocab_size) : 0; };
+    const struct { const void *at; size_t bytes; } read[] = {
+        {target_probs, rows(target_stride)}, {draft_probs, rows(draft_stride)}, {draft_tokens, n4}, {tree_indptr, b4 + 4},
+        {first_child, n4}, {next_sibling, n4}, {accept_uniforms, n4}, {sample_uniforms, b4}},
+        written[] = {{accept_index, b4 * accept_width}, {accept_len, b4}, {next_token, b4}, {status, 4}};
+    for (const auto &r : read)
+        for (const auto &w : written)
+            if (overlaps(r.at, r.bytes, w.at, w.bytes))
+                return fail(CSGMV_ERR_INVALID_ARG, "an output overlaps an input");
     csgmv::VerifyParams p = {target_probs, draft_probs,  target_stride, draft_stride,    num_nodes,       draft_tokens,
                              tree_indptr,  first_child,  next_sibling,  accept_uniforms, sample_uniforms, bs,
                              vocab_size,   accept_width, accept_index,  accept_len,      next_token,      status};

@@ -58,3 +58,20 @@ def test_attention_writes_apart_from_what_steers_it(lib, kw, ok):  # noqa: F811
                                   a["out"], a["ots"], a["ohs"], a["lse"], a["ws"], short, None)
     assert rc == (CAPACITY if ok else INVALID)
     assert (b"overlap" in lib.csgmv_last_error()) is not ok
+
+
+AT = {name: 0x1000000 * (i + 1) for i, name in enumerate(
+    ("target", "draft", "tokens", "indptr", "first", "next", "au", "su", "path", "len", "token", "status"))}
+
+
+@pytest.mark.parametrize("out,size", [("path", 4 * 2 * 5), ("len", 8), ("token", 8), ("status", 4)])
+@pytest.mark.parametrize("inp,size_in", [("target", 4 * (7 * 1000 + 900)), ("draft", 4 * (7 * 904 + 900)), ("tokens", 32),
+                                         ("indptr", 12), ("first", 32), ("next", 32), ("au", 32), ("su", 8)])
+def test_verification_writes_apart_from_what_it_reads(lib, out, size, inp, size_in):  # noqa: F811
+    """8 nodes of 2 requests, 900 tokens; the output's first and last bytes on the input's last and first."""
+    for at in (AT[inp] + size_in - 4, AT[inp] - size + 4):
+        a = dict(AT)
+        a[out] = at
+        rc = lib.csgmv_verify_drafts(a["target"], 1000, a["draft"], 904, a["tokens"], a["indptr"], a["first"], a["next"],
+                                     a["au"], a["su"], 2, 8, 900, a["path"], 5, a["len"], a["token"], a["status"], None)
+        assert rc == INVALID and b"overlaps" in lib.csgmv_last_error()
