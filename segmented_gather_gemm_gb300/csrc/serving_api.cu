@@ -58,6 +58,13 @@ bool overlaps_meta(const csgmv_kv_cache *kv, const void *p, size_t bytes) {
            overlaps(p, bytes, kv->page_refs, 4 * (size_t)kv->num_pages) || overlaps(p, bytes, kv->status, 4);
 }
 
+// A plan and the move behind it both read a call's lists; the plan checks them,
+// and writes the bookkeeping and scratch: no list may lie there.
+bool overlaps_plan(const csgmv_kv_cache *kv, const int32_t *list, size_t n) {
+    return overlaps_meta(kv, list, 4 * n) ||
+           overlaps(list, 4 * n, kv->scratch, 4 * (size_t)csgmv::kv_scratch_ints(kv->num_pages, kv->max_seqs));
+}
+
 int check_kv(const csgmv_kv_cache *kv) {
     if (!kv) return fail(CSGMV_ERR_INVALID_ARG, "kv cache is NULL");
     if (!kv->k_pages || !kv->v_pages || !kv->page_table || !kv->seq_lens || !kv->page_refs || !kv->scratch || !kv->status)
@@ -136,6 +143,9 @@ int csgmv_kv_commit(const csgmv_kv_cache *kv, const void *k_new, const void *v_n
     if ((rc = check_new(k_new, v_new, new_token_stride, new_head_stride))) return rc;
     if (new_layer_stride % 8 || new_layer_stride < 0)
         return fail(CSGMV_ERR_INVALID_ARG, "new_layer_stride must be a non-negative multiple of 8");
+    if (overlaps_plan(kv, accept_index, (size_t)bs * accept_width) || overlaps_plan(kv, accept_len, bs) ||
+        overlaps_plan(kv, tree_indptr, (size_t)bs + 1) || overlaps_plan(kv, seq_slots, bs))
+        return fail(CSGMV_ERR_INVALID_ARG, "a list of the call overlaps the cache's bookkeeping or scratch");
     csgmv::CommitParams p;
     p.k_new = static_cast<const uint16_t *>(k_new);
     p.v_new = static_cast<const uint16_t *>(v_new);
@@ -160,6 +170,8 @@ int csgmv_kv_fork(const csgmv_kv_cache *kv, const int32_t *parents, const int32_
     if (n > kv->max_seqs) return fail(CSGMV_ERR_CAPACITY, "n %d exceeds max_seqs %d", n, kv->max_seqs);
     if (n == 0) return CSGMV_OK;
     if (!parents || !children) return fail(CSGMV_ERR_INVALID_ARG, "parents / children is NULL");
+    if (overlaps_plan(kv, parents, n) || overlaps_plan(kv, children, n))
+        return fail(CSGMV_ERR_INVALID_ARG, "a list of the call overlaps the cache's bookkeeping or scratch");
     return launched(csgmv::launch_kv_fork(*kv, parents, children, n, st(stream)), "csgmv_kv_fork");
 }
 

@@ -75,3 +75,19 @@ def test_verification_writes_apart_from_what_it_reads(lib, out, size, inp, size_
         rc = lib.csgmv_verify_drafts(a["target"], 1000, a["draft"], 904, a["tokens"], a["indptr"], a["first"], a["next"],
                                      a["au"], a["su"], 2, 8, 900, a["path"], 5, a["len"], a["token"], a["status"], None)
         assert rc == INVALID and b"overlaps" in lib.csgmv_last_error()
+
+
+@pytest.mark.parametrize("name", ["page_table", "seq_lens", "page_refs", "scratch", "status"])
+def test_lists_of_a_cache_call_lie_apart_from_what_its_plan_writes(lib, name):  # noqa: F811
+    c = cache()
+    for i, n in enumerate(("page_table", "seq_lens", "page_refs", "scratch", "status")):
+        setattr(c, n, 0x1000000 * (i + 1))
+    size = dict(page_table=4 * 8 * 4, seq_lens=4 * 8, page_refs=4 * 16, scratch=4 * lib.csgmv_kv_scratch_ints(16, 8), status=4)
+    ref = ctypes.byref(c)
+    for at in (getattr(c, name), getattr(c, name) + size[name] - 4):
+        for kw in (dict(idx=at), dict(lens=at), dict(indptr=at), dict(lens=at - 12), dict(idx=at - 60)):
+            assert commit(lib, c, **kw) == INVALID and b"overlaps" in lib.csgmv_last_error()
+        slots = lib.csgmv_kv_commit(ref, P, P, 1 << 20, 128, 64, 32, P, 4, P, P, at, 4, None)
+        assert slots == INVALID and b"overlaps" in lib.csgmv_last_error()
+        for a, b in ((at, P), (P, at), (P, at - 28)):
+            assert lib.csgmv_kv_fork(ref, a, b, 8, None) == INVALID and b"overlaps" in lib.csgmv_last_error()
