@@ -426,7 +426,8 @@ enum {
     CSGMV_KV_STATUS_BAD_PAGE = 2,  /* page number out of range, or a reference count that would go below zero */
     CSGMV_KV_STATUS_CAPACITY = 4,  /* no free pages left, or a row of the page table is full */
     CSGMV_KV_STATUS_BAD_LENS = 8,  /* negative or inconsistent lengths */
-    CSGMV_KV_STATUS_BAD_TREE = 16, /* a parent that does not come before its child, or a bad node number */
+    CSGMV_KV_STATUS_BAD_TREE = 16, /* a parent that does not come before its child, a bad node number, or a node
+                                      under two parents */
     CSGMV_KV_STATUS_BAD_TOKEN = 32, /* a drafted token outside the vocabulary, or a distribution without mass */
     CSGMV_KV_STATUS_TIMEOUT = 1 << 30 /* csgmv_tree_attention: a bounded wait inside the kernel ran out, the call's
                                          results are meaningless; while the bit is set its calls give no output */
@@ -605,15 +606,17 @@ CSGMV_API int csgmv_build_draft_tree(const int32_t *parents, const int32_t *tree
  *   target_probs, draft_probs   f32, row of a node at target_stride / draft_stride
  *                  elements; draft_probs may be NULL
  *   draft_tokens   [num_nodes] (the root's is not used)
- *   first_child, next_sibling   from csgmv_build_draft_tree
+ *   first_child, next_sibling   from csgmv_build_draft_tree (a number that is
+ *                  not above its node's own, or past the request, ends a list)
  *   accept_uniforms [num_nodes], sample_uniforms [bs]   in [0, 1)
  *   accept_index   [bs][accept_width]: node numbers of the accepted path, the
  *                  root first, then -1
  *   accept_len     [bs]: nodes on the path (1 when no draft was accepted)
  *   next_token     [bs]
- * A request without nodes, or whose path is longer than accept_width
- * (CSGMV_KV_STATUS_CAPACITY), gets accept_len = 0 and next_token = -1, as does
- * one whose last distribution has no mass (BAD_TOKEN: next_token = -1 only).
+ * A request without nodes, with a node in two nodes' lists (BAD_TREE), or whose
+ * path is longer than accept_width (CSGMV_KV_STATUS_CAPACITY), gets accept_len
+ * = 0 and next_token = -1; one whose last distribution has no mass (BAD_TOKEN)
+ * next_token = -1 only.
  * 1 <= vocab_size <= 2^18.
  */
 CSGMV_API int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const float *draft_probs,

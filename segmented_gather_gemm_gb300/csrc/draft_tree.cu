@@ -127,17 +127,16 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify(VerifyParams v, int per
     int n = hi - lo;
     if (tid == 0) sm.ngone = 0;
     const bool sound = lo >= 0 && hi >= lo && hi <= v.num_nodes && n <= kMaxNodes;
-    if (!sound || n == 0) {  // the same in every CTA of the cluster
-        if (rank == 0) {
-            for (int j = tid; j < v.width; j += kVerThreads) v.accept_index[(int64_t)b * v.width + j] = -1;
-            if (tid == 0) {
-                v.accept_len[b] = 0;
-                v.next_token[b] = -1;
-                if (!sound) atomicOr(v.status, CSGMV_KV_STATUS_BAD_TREE);
-            }
+    auto leave_out = [&](bool bad) {
+        if (rank != 0) return;
+        for (int j = tid; j < v.width; j += kVerThreads) v.accept_index[(int64_t)b * v.width + j] = -1;
+        if (tid == 0) {
+            v.accept_len[b] = 0;
+            v.next_token[b] = -1;
+            if (bad) atomicOr(v.status, CSGMV_KV_STATUS_BAD_TREE);
         }
-        return;
-    }
+    };
+    if (!sound || n == 0) return leave_out(!sound);  // the same in every CTA of the cluster
     for (int i = tid; i < n; i += kVerThreads) {
         // numbers that do not increase would let the walk go in circles
         const int f = v.first_child[lo + i], s = v.next_sibling[lo + i];
@@ -153,9 +152,12 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify(VerifyParams v, int per
         sm.parent[i] = -1;
     }
     __syncthreads();
+    // (A node in two lists would have whichever parent comes last, not the same one in every CTA, and
+    // CTAs that walk differently would wait for one another at the cluster's barriers.)
+    bool twice = false;
     for (int i = tid; i < n; i += kVerThreads)
-        for (int k = sm.first[i]; k >= 0; k = sm.next[k]) sm.parent[k] = i;
-    __syncthreads();
+        for (int k = sm.first[i]; k >= 0; k = sm.next[k]) twice |= atomicExch(&sm.parent[k], i) >= 0;
+    if (__syncthreads_or(twice)) return leave_out(true);
     for (int i = tid; i < n; i += kVerThreads) {
         const int c = sm.parent[i], t = sm.token[i];
         const bool on = c >= 0 && t >= 0;
