@@ -544,7 +544,10 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  * head_dim 64 or 128; num_q_heads a multiple of num_kv_heads, at most 128
  * times it; page_size a power of two >= 8.  One row for each request is plain
  * decoding.  Sums are fp32; before they meet V the softmax weights are
- * rounded to half, or to a bfloat16 pair of 16 bits.  Results do not depend on
+ * rounded: bfloat16's to a pair of 16 bits, half's to one half of 11 bits, as
+ * many as out has.  (The rows of a request and kv head, tokens times query heads,
+ * are taken 128 at a time: where that leaves 16 or fewer, plain decoding for
+ * instance, half's weights are a pair of 22 bits.)  Results do not depend on
  * timing.  A page number out of range sets CSGMV_KV_STATUS_BAD_PAGE and makes
  * its request's rows meaningless; other bad requests are left out (their rows
  * of out and lse stay as they are).  bs <= 16000;

@@ -114,7 +114,7 @@ struct VerSmem {
 // instead of 36), and a cluster is as large as leaves the batch two CTAs an SM
 // (launch_verify; four an SM, in turns: 41 us).  256 trees over 128256 tokens,
 // one pass each: 37 us, the pass 22 us of it at 6 TB/s; one chain of 5 over
-// 32000: 9 us.  In both the rest is dependent loads: lists, parents, the drafted
+// 32000: 9.5 us.  In both the rest is dependent loads: lists, parents, the drafted
 // tokens' probabilities, the draw.
 __global__ void __launch_bounds__(kVerThreads, 2) verify(VerifyParams v, int per, int vec) {
     __shared__ VerSmem sm;

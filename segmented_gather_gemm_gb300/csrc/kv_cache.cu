@@ -6,12 +6,14 @@
 // are given out) from page_refs alone, with prefix sums and no atomic whose
 // order could show, so the same state gives the same pages.  The move kernel
 // is launched behind it (programmatic dependent launch) and streams the data
-// with 16-byte loads, several in flight a thread; it is bound by HBM.
+// with 16-byte loads, several in flight a thread.  Whole pages go at HBM's rate;
+// a commit's rows do not (DRAM 52 to 63 % busy): a warp's unit is one row in one
+// layer, and for each it finds the request and follows four dependent loads.
 //
 // Measured (device time): a commit of 256 requests' accepted tokens into 32
-// layers of 8 heads of 128 (292 MB) 58.5 us, of which the plan 8 us and the
-// move 5 TB/s; of 4 requests 10.6 us, the chain of loads of both.  Fork, free
-// and compaction of 512 sequences (4.3 GB) 677 us, 6.4 TB/s; of 16 small ones
+// layers of 8 heads of 128 (292 MB) 58.7 us, of which the plan 8 us and the
+// move 5 TB/s; of 4 requests 10.8 us, the chain of loads of both.  Fork, free
+// and compaction of 512 sequences (4.3 GB) 678 us, 6.4 TB/s; of 16 small ones
 // 20 us, five launches one behind the other.
 #include "serving.cuh"
 

@@ -48,7 +48,11 @@
 // Rounding.  Half inputs round P to half, scaled by 2^4 so that small weights
 // keep their bits; bfloat16 would keep 8 bits, as coarse as the output's own
 // rounding, so there P goes in as a high part (its upper 16 bits) and what that
-// leaves, rounded, in two products, which the tensor core has time for.
+// leaves, rounded, in two products, which the tensor core has time for.  Half
+// weights have 11 bits, as the output has; turned over their low part costs
+// nothing and goes in as well, above 16 rows it would cost a quarter: the trees
+// below 192 us instead of 152 (called one by one), for a largest error of
+// 8.3e-4, the output's rounding alone, instead of 1.07e-3.
 //
 // One CTA: a warp each fills a ring of K tiles and one of V tiles with TMA, a
 // warp issues S = Q K^T up to three tiles ahead (three S buffers, each P in its
@@ -58,9 +62,13 @@
 // and held everything up (bfloat16, head_dim 64, 128 rows a kv head over 100003
 // and 131072 tokens: 73 us, with two warps 63.5 us).
 //
-// Measured now: that case 57 us; 256 requests of one token, 64 to 4096 cached, 8
-// kv heads of 128, 330 us (6.6 TB/s, 97 % of a plain copy's rate); a tree of 12
-// over 1021 tokens 12.2 us.
+// Waits are bounded.  After one has run out nothing of the call's results holds,
+// but its warps meet at all barriers and wait for their own copies and products;
+// calls that find the status bit do nothing (what this takes: trees 145 to 147 us).
+//
+// Measured now: that case 58 to 60 us; 256 requests of one token, 64 to 4096
+// cached, 8 kv heads of 128, 328 us (6.7 TB/s, 98 % of a plain copy's rate); a
+// tree of 12 over 1021 tokens 12.6 us.
 
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -357,8 +365,9 @@ constexpr int kFewRows = 16;  // up to so many rows the products are turned over
 // What the parts of the axis are weighed by, in units of 64 clocks.  Measured
 // on long axes: a tile's K and V of head_dim 128 come in 2870 clocks of an SM's
 // share of HBM, half of that when two CTAs read them together (of head_dim 64 in
-// less than the softmax takes); its softmax takes 1000 clocks turned over,
-// otherwise 1400 (half) or 1700 (bfloat16).  Beginning and ending an item costs
+// 1430); its softmax takes 1000 clocks turned over, otherwise 1400 (half) or 1700
+// (bfloat16).  (Bytes of head_dim 64 are weighed as the turned-over softmax, which
+// is too little where that is all there is: no such batch has been measured.)  Beginning and ending an item costs
 // 5800 turned over (its tiles' loads start anew), 10200 otherwise.  With equal
 // tile counts instead, 256 requests of 64 to 4096 tokens take 340 us (328), the
 // trees above 218 us (145).
