@@ -433,8 +433,9 @@ def _raw_stream(stream, device: int):
     if torch.cuda.current_device() != device:
         raise CsgmvError(-1, f"the operands are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is not None:
-        if stream.device_index != device:
-            raise CsgmvError(-1, f"the operands are on cuda:{device}, the stream is on cuda:{stream.device_index}")
+        at = getattr(stream, "device_index", device)  # (a bare handle's holder need not say)
+        if at != device:
+            raise CsgmvError(-1, f"the operands are on cuda:{device}, the stream is on cuda:{at}")
         return stream.cuda_stream
     if _current_raw_stream is not None:
         return _current_raw_stream(device)

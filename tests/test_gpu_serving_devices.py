@@ -86,3 +86,18 @@ def test_host_tensors_and_workspaces_that_are_not_memory():
         call()
     torch.cuda.synchronize()
     assert cache.device_status() == 0 and tree.device_status() == 0
+
+
+def test_a_stream_that_is_only_a_handle():
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+
+    cache, tree = make()
+    s = torch.cuda.Stream()
+    todo = calls(cache, tree, Handle(s))[:7]  # (what allocates outputs needs torch's own)
+    s.wait_stream(torch.cuda.current_stream())
+    for call in todo:
+        call()
+    torch.cuda.synchronize()
+    assert cache.device_status() == 0 and tree.device_status() == 0
