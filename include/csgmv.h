@@ -438,8 +438,9 @@ enum {
  * handed out to at most max_seqs sequences.  Element (layer l, page p, head
  * h, token slot t, d) of k_pages and of v_pages is at
  *     l * layer_stride + p * page_stride + h * head_stride + t * token_stride + d
- * (strides in elements, multiples of 8).  Token i of sequence s is in slot
- * i % page_size of page page_table[s * max_pages_per_seq + i / page_size].
+ * (strides in elements, multiples of 8; no two elements share a place).  Token i
+ * of sequence s is in slot i % page_size of page
+ * page_table[s * max_pages_per_seq + i / page_size].
  * page_refs[p] counts the sequences that hold page p; a page is free when it
  * is 0, and pages are given out lowest first.  The caller allocates every
  * buffer; an empty cache has seq_lens = 0, page_refs = 0 and page_table = -1.
@@ -475,7 +476,8 @@ CSGMV_API int64_t csgmv_kv_scratch_ints(int num_pages, int max_seqs);
  * A request with a bad slot, length or node number, or without room in its
  * row of the page table, is left out; when the free pages do not suffice for
  * the whole batch nothing is appended at all (CSGMV_KV_STATUS_CAPACITY).
- * A sequence may appear once in a batch.  bs <= max_seqs.
+ * A sequence may appear once in a batch.  bs <= max_seqs.  The lists may not lie
+ * in the cache's bookkeeping or scratch (nor csgmv_kv_fork's).
  */
 CSGMV_API int csgmv_kv_commit(const csgmv_kv_cache *kv, const void *k_new, const void *v_new, int64_t new_layer_stride,
                               int64_t new_token_stride, int64_t new_head_stride, int64_t num_tokens,
@@ -556,6 +558,8 @@ CSGMV_API int csgmv_kv_copy_pages(const csgmv_kv_cache *kv, const int32_t *src, 
  * of which 128 rows against 128 tokens take 16 to 45, so at least 4 * 10^14
  * pairs of a row and a token) sets CSGMV_KV_STATUS_CAPACITY and gives no output.
  *   workspace      csgmv_tree_attention_workspace_bytes(); contents do not matter
+ * out, lse and workspace may not overlap one another, tree_indptr, seq_slots or
+ * the cache's bookkeeping, nor rows of out each other.
  */
 CSGMV_API int csgmv_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads,
                                    const void *k_new, const void *v_new, int64_t new_token_stride,
@@ -620,7 +624,7 @@ CSGMV_API int csgmv_build_draft_tree(const int32_t *parents, const int32_t *tree
  * path is longer than accept_width (CSGMV_KV_STATUS_CAPACITY), gets accept_len
  * = 0 and next_token = -1; one whose last distribution has no mass (BAD_TOKEN)
  * next_token = -1 only.
- * 1 <= vocab_size <= 2^18.
+ * 1 <= vocab_size <= 2^18.  No output may overlap an input.
  */
 CSGMV_API int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const float *draft_probs,
                                   int64_t draft_stride, const int32_t *draft_tokens, const int32_t *tree_indptr,

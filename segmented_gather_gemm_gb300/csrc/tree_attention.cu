@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend(const __grid_constant_
             }
             w = wn;
         } while (more && on);
-        // each place's last load (of this round, or of the one before)
+        // each place's last load (from the place before s on back, once around the ring)
         for (int i = 0; i < slots; ++i) within(&full[i], i < s ? phase : phase ^ 1, kDrain);
     } else if (warp == kWarpS) {
         // ------------------------------------------------ products: S = Q K^T
