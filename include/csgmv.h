@@ -428,7 +428,8 @@ enum {
     CSGMV_KV_STATUS_BAD_LENS = 8,  /* negative or inconsistent lengths */
     CSGMV_KV_STATUS_BAD_TREE = 16, /* a parent that does not come before its child, a bad node number, or a node
                                       under two parents */
-    CSGMV_KV_STATUS_BAD_TOKEN = 32, /* a drafted token outside the vocabulary, or a distribution without mass */
+    CSGMV_KV_STATUS_BAD_TOKEN = 32, /* a token outside the vocabulary, or a distribution without mass */
+    CSGMV_KV_STATUS_BAD_VALUE = 64, /* csgmv_process_logits: a request's factor, list of biases or mask that is not one */
     CSGMV_KV_STATUS_TIMEOUT = 1 << 30 /* csgmv_tree_attention: a bounded wait inside the kernel ran out, the call's
                                          results are meaningless; while the bit is set its calls give no output */
 };
@@ -632,6 +633,50 @@ CSGMV_API int csgmv_verify_drafts(const float *target_probs, int64_t target_stri
                                   const float *accept_uniforms, const float *sample_uniforms, int bs,
                                   int64_t num_nodes, int vocab_size, int32_t *accept_index, int accept_width,
                                   int32_t *accept_len, int32_t *next_token, int32_t *status, csgmv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What a decoder does between the projections, the attention and the
+ * verification (additions of this library as well): residual and norms,
+ * rotary positions, appending to the cache layer by layer, logits to
+ * probabilities.  The conventions above hold, except that pointers need only
+ * their elements' alignment (16 bytes are faster).
+ * ------------------------------------------------------------------------ */
+
+/* Kinds of norm: none, root mean square, and centred ("layer"). */
+enum { CSGMV_NORM_NONE = 0, CSGMV_NORM_RMS = 1, CSGMV_NORM_LAYER = 2 };
+
+/* A norm over a row v of `hidden` elements:
+ *     RMS    v * rsqrt(mean(v^2) + eps) * weight + bias
+ *     LAYER  (v - mean(v)) * rsqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ * weight and bias have the row's type (dtype of the call); NULL: 1 and 0. */
+typedef struct csgmv_norm {
+    const void *weight, *bias;
+    float eps;
+    int32_t kind; /* CSGMV_NORM_* */
+} csgmv_norm;
+
+/*
+ * Adds a block's output x to the residual stream and norms the sum for the
+ * next block: for every row t,
+ *     r'[t] = residual_scale * r[t] + gate[t] * post(x[t]),   out[t] = pre(r'[t]).
+ *   x, out, gate   dtype (CSGMV_DTYPE_BF16, _F16 or _F32); rows of `hidden`
+ *                  dense elements, *_stride elements apart
+ *   gate           NULL: 1; gate_stride 0: one row for all
+ *   residual, residual_out   dtype or f32 (residual_dtype); residual NULL: r = 0;
+ *                  residual_out NULL: r' is not written
+ *   pre            NULL or kind NONE with out NULL: only r' is made
+ *   post           NULL: x as it is
+ * r' enters pre with 32 bits, not as it is rounded for residual_out.  Sums are
+ * f32.  out and residual_out may each be x, residual or gate (same address and
+ * stride, types of one size); otherwise no output overlaps an input or the other
+ * output.
+ * 1 <= hidden <= 16384.
+ */
+CSGMV_API int csgmv_add_norm(const void *x, int64_t x_stride, int dtype, const void *residual, int64_t residual_stride,
+                             int residual_dtype, const void *gate, int64_t gate_stride, const csgmv_norm *post,
+                             const csgmv_norm *pre, float residual_scale, int64_t num_tokens, int hidden,
+                             void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
+                             csgmv_stream_t stream);
 
 #ifdef __cplusplus
 }

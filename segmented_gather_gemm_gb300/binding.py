@@ -25,7 +25,8 @@ STATUS_BITS = {
 # bits of KvCache.status and DraftTree.status (CSGMV_KV_STATUS_*; 1 << 30: a
 # bounded wait inside a kernel ran out)
 KV_STATUS_BITS = {
-    1: "BAD_SEQ", 2: "BAD_PAGE", 4: "CAPACITY", 8: "BAD_LENS", 16: "BAD_TREE", 32: "BAD_TOKEN", 1 << 30: "TIMEOUT",
+    1: "BAD_SEQ", 2: "BAD_PAGE", 4: "CAPACITY", 8: "BAD_LENS", 16: "BAD_TREE", 32: "BAD_TOKEN",
+    64: "BAD_VALUE", 1 << 30: "TIMEOUT",
 }
 
 EXPORTED = ["csgmv_last_error", "csgmv_version", "csgmv_chunk_size", "csgmv_batch_info_capacity",
@@ -35,7 +36,7 @@ EXPORTED = ["csgmv_last_error", "csgmv_version", "csgmv_chunk_size", "csgmv_batc
             "embedding_lora_a_transposed", "csgmv_transpose_embedding",
             "csgmv_kv_scratch_ints", "csgmv_kv_commit", "csgmv_kv_fork", "csgmv_kv_free", "csgmv_kv_compact",
             "csgmv_kv_copy_pages", "csgmv_tree_attention", "csgmv_tree_attention_workspace_bytes",
-            "csgmv_build_draft_tree", "csgmv_verify_drafts"]
+            "csgmv_build_draft_tree", "csgmv_verify_drafts", "csgmv_add_norm"]
 
 # csgmv_qkv_path results (CSGMV_PATH_*)
 PATHS = {0: "fused", 1: "decode", 2: "small_split", 3: "stream"}
@@ -64,6 +65,10 @@ class _KvCacheC(ctypes.Structure):
         (n, ctypes.c_int32) for n in (
             "dtype", "num_layers", "num_pages", "page_size", "num_kv_heads", "head_dim", "max_seqs",
             "max_pages_per_seq")]
+
+
+class _NormC(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float), ("kind", ctypes.c_int32)]
 
 
 _lib = None
@@ -117,6 +122,8 @@ def lib():
         "csgmv_build_draft_tree": (i32, [vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp]),
         "csgmv_verify_drafts": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, vp, i32, vp, vp, vp,
                                       vp]),
+        "csgmv_add_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, i64, ctypes.POINTER(_NormC), ctypes.POINTER(_NormC), f32,
+                                 i64, i32, vp, i64, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -723,3 +730,100 @@ def csgmv_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, 
     if rc:
         _check(rc)
     return accept_index, accept_len, next_token
+
+
+# ---------------------------------------------------------------------------
+# What a decoder does between the projections, the attention and the
+# verification: residual and norms, rotary positions, appending to the cache
+# layer by layer, logits to probabilities.
+
+_DTYPES = {torch.bfloat16: CSGMV_DTYPE_BF16, torch.float16: CSGMV_DTYPE_F16, torch.float32: CSGMV_DTYPE_F32}
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+
+
+class Norm:
+    """A norm over rows of `hidden` elements, and the C struct of it: kind "rms"
+    or "layer", weight and bias dense vectors of the rows' type or None."""
+
+    def __init__(self, kind: str = "rms", weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-6):
+        _need(kind in NORM_KINDS, f"kind {kind!r} must be one of {', '.join(NORM_KINDS)}")
+        of = [t for t in (weight, bias) if t is not None]
+        _need(all(t.is_cuda and t.dim() == 1 and t.is_contiguous() for t in of),
+              "a norm's weight and bias must be dense CUDA vectors")
+        _need(len(of) < 2 or (of[0].shape == of[1].shape and of[0].dtype is of[1].dtype and of[0].device == of[1].device),
+              "a norm's weight and bias must be alike")
+        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, eps
+        self.hidden = of[0].shape[0] if of else None
+        self.dtype = of[0].dtype if of else None
+        self.device = of[0].get_device() if of else None
+        self.c = _NormC(_at(weight), _at(bias), eps, NORM_KINDS[kind])
+        self._ref = ctypes.byref(self.c)
+
+
+def _norm_for(norm: Norm | None, x: torch.Tensor, hidden: int):
+    if norm is None:
+        return None
+    if norm.hidden is not None and not (norm.hidden == hidden and norm.dtype is x.dtype and norm.device == x.get_device()):
+        raise CsgmvError(-1, f"a norm's weight is {norm.dtype} ({norm.hidden},) on cuda:{norm.device}, the rows are {x.dtype} "
+                             f"of {hidden} on {x.device}")
+    return norm._ref
+
+
+def _row_stride(name: str, t: torch.Tensor, n: int, hidden: int, device: int) -> int:
+    """t is (n, hidden) on that GPU, its rows dense; their stride."""
+    st = t.stride()
+    if t.shape != (n, hidden) or t.get_device() != device or hidden > 1 and st[1] != 1:
+        raise CsgmvError(-1, f"{name} must be ({n}, {hidden}) on cuda:{device}, its rows dense, not {tuple(t.shape)} on {t.device}")
+    return st[0] if n > 1 else hidden
+
+
+def csgmv_add_norm(x: torch.Tensor, norm: Norm | None, out: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                   post_norm: Norm | None = None, gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                   stream=None) -> torch.Tensor | None:
+    """r' = residual_scale * residual + gate * post_norm(x); out = norm(r').
+
+    x, out and gate (tokens, hidden) in one type (gate may be a single row);
+    residual in that type or f32.  residual_out None: the residual is updated in
+    place (without one, r' is not kept).  out None: allocated on the call's
+    stream, unless norm is None too: then only r' is made."""
+    if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda:
+        raise CsgmvError(-1, "x must be a CUDA tensor (tokens, hidden) of bf16, f16 or f32")
+    n, hidden = x.shape
+    device, rtype = x.get_device(), x.dtype
+    xs, rs, ros, gs, os_ = _row_stride("x", x, n, hidden, device), 0, 0, 0, 0
+    if residual is not None:
+        rtype = residual.dtype
+        rs = _row_stride("residual", residual, n, hidden, device)
+        if residual_out is None:
+            residual_out = residual
+    if residual_out is not None:
+        ros = _row_stride("residual_out", residual_out, n, hidden, device)
+        if residual is None:
+            rtype = residual_out.dtype
+        elif residual_out.dtype is not rtype:
+            raise CsgmvError(-1, "residual_out must have the residual's type")
+    if rtype is not x.dtype and rtype is not torch.float32:
+        raise CsgmvError(-1, f"the residual must be {x.dtype} or float32, not {rtype}")
+    if gate is not None:
+        if gate.dtype is not x.dtype:
+            raise CsgmvError(-1, f"gate must be {x.dtype}, not {gate.dtype}")
+        one = gate.shape[0] == 1
+        gs = _row_stride("gate", gate, 1 if one else n, hidden, device)
+        if one:
+            gs = 0
+    if out is None:
+        if norm is not None:
+            out = _empty(stream, (n, hidden), dtype=x.dtype, device=x.device)
+            os_ = hidden
+    else:
+        if out.dtype is not x.dtype:
+            raise CsgmvError(-1, f"out must be {x.dtype}, not {out.dtype}")
+        os_ = _row_stride("out", out, n, hidden, device)
+    rc = lib().csgmv_add_norm(x.data_ptr(), xs, _DTYPES[x.dtype], _at(residual), rs, _DTYPES[rtype], _at(gate), gs,
+                              _norm_for(post_norm, x, hidden), _norm_for(norm, x, hidden), residual_scale, n, hidden,
+                              _at(residual_out), ros, _at(out), os_, _raw_stream(stream, device))
+    if rc:
+        _check(rc)
+    return out

@@ -1,0 +1,65 @@
+"""Plain references, in 64 bits, of what a decoder does between the projections,
+the attention and the verification.  No code of the package runs here."""
+from __future__ import annotations
+
+import math
+
+import torch
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}  # half a step, relative
+TINY = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -25, torch.float32: 0.0}  # half a step of subnormal numbers
+
+
+def norm(v, kind, w, b, eps):
+    """(normed v, how much of each value's terms an error of one part can move):
+    for a relative error e of each operation the result is off by at most a few
+    e times the second."""
+    if kind == "none":
+        return v, v.abs()
+    off = v.abs().mean(-1, keepdim=True)
+    if kind == "layer":
+        v = v - v.mean(-1, keepdim=True)
+    f = 1 / torch.sqrt((v * v).mean(-1, keepdim=True) + eps)
+    w = torch.ones_like(v[:1]) if w is None else w.double()
+    b = torch.zeros_like(v[:1]) if b is None else b.double()
+    y = v * f * w + b
+    return y, y.abs() + b.abs() + w.abs() * f * (off if kind == "layer" else 0.0) + (v * f * w).abs()
+
+
+def add_norm(x, residual, gate, post, pre, scale):
+    """((r', its tolerance), (out, its tolerance)) in float64, but for the
+    rounding to the outputs' types.  post, pre: (kind, w, b, eps).
+
+    Every value is a chain of less than 2^7 operations of f32 (sums: up to 32
+    elements a thread and ten steps of a tree; a reciprocal root of two units in
+    the last place): each moves it by 2^-24 of the terms it is made of."""
+    e = 2.0 ** -17
+    v, terms = norm(x.double(), *post)
+    if gate is not None:
+        v, terms = v * gate.double(), terms * gate.double().abs()
+    if residual is not None:
+        v, terms = v + scale * residual.double(), terms + (scale * residual.double()).abs()
+    kind, w, b, eps = pre
+    out, more = norm(v, *pre)
+    if kind == "none":
+        return (v, e * terms), (out, e * terms)
+    c = v - v.mean(-1, keepdim=True) if kind == "layer" else v
+    f = 1 / torch.sqrt((c * c).mean(-1, keepdim=True) + eps)
+    wa = 1.0 if w is None else w.double().abs()
+    # an error of r' moves its own value, the mean, and the root mean square
+    rms = torch.sqrt((terms * terms).mean(-1, keepdim=True))
+    return (v, e * terms), (out, e * (more + wa * f * (terms + rms * (1 + (c * f).abs()))))
+
+
+def close(got, want, tol, dtype=None):
+    """got within tol plus its type's rounding of want; NaN and infinities alike."""
+    dtype = got.dtype if dtype is None else dtype
+    got, want, tol = got.double().cpu(), want.double().cpu(), torch.as_tensor(tol, dtype=torch.float64).cpu()
+    finite = torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), "NaN in other places"
+    inf = ~finite & ~torch.isnan(want)
+    assert torch.equal(got[inf], want[inf]), "infinities differ"
+    bound = tol + HALF[dtype] * (want.abs() + tol) + TINY[dtype]
+    bound = bound.expand_as(want) if bound.dim() else bound.repeat(want.shape)
+    over = ((got - want).abs() - bound)[finite]
+    assert not bool((over > 0).any()), f"{int((over > 0).sum())} of {over.numel()} too far off, by up to {float(over.max()):.3g}"
