@@ -678,6 +678,92 @@ CSGMV_API int csgmv_add_norm(const void *x, int64_t x_stride, int dtype, const v
                              void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
                              csgmv_stream_t stream);
 
+/*
+ * Rotary positions.  Elements u, v of pair i (0 <= i < rotary_dim / 2) of a head
+ * at position p become
+ *     scale * (u cos a - v sin a),  scale * (u sin a + v cos a),  a = p * f_i
+ * (f_i radians a position); the other elements of the head stay as they are.
+ *   interleaved  1: pair i is elements 2 i and 2 i + 1; 0: elements i and
+ *                i + rotary_dim / 2
+ *   turns        device, [rotary_dim / 2]: f_i in units of 2^-64 turns, from
+ *                csgmv_rope_turns().  p * turns[i] in 64 bits wraps at whole turns, so
+ *                angles of far positions keep all their bits.
+ */
+typedef struct csgmv_rope {
+    const uint64_t *turns;
+    float scale;
+    int32_t rotary_dim; /* even, at most head_dim */
+    int32_t interleaved;
+} csgmv_rope;
+
+/* turns[i] = round(2^64 * freq[i] / (2 pi)) modulo 2^64 (freq in radians a
+ * position, finite).  Host only. */
+CSGMV_API int csgmv_rope_turns(const double *freq, int n, uint64_t *turns);
+
+/*
+ * Turns the heads of queries and keys by the positions of their tokens.
+ *   dtype       CSGMV_DTYPE_BF16, _F16 or _F32
+ *   q, k        element (t, h, d) at t * token_stride + h * head_stride + d; k (with
+ *               num_k_heads 0) or q (with num_q_heads 0) may be NULL
+ *   positions   [num_tokens], any int32
+ *   q_out, k_out  may be q and k (same address and strides); otherwise no
+ *               output overlaps an input, nor the other output
+ *   inverse     1: by the negative angles, times scale: the gradient of the
+ *               inputs from that of the outputs
+ * Products are f32, rounded once.  1 <= head_dim <= 1024.
+ */
+CSGMV_API int csgmv_rotary(const csgmv_rope *rope, int dtype, int head_dim, const int32_t *positions,
+                           int64_t num_tokens, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                           int num_q_heads, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                           int num_k_heads, void *q_out, int64_t qo_token_stride, int64_t qo_head_stride, void *k_out,
+                           int64_t ko_token_stride, int64_t ko_head_stride, int inverse, csgmv_stream_t stream);
+
+/*
+ * Makes room for add_lens[b] more tokens (all of its rows when add_lens is
+ * NULL) in sequence seq_slots[b] (b when NULL) of the cache: takes pages, copies
+ * a partly filled last page that another sequence holds too, raises seq_lens.
+ * What csgmv_kv_commit does but for the contents, which csgmv_kv_append brings
+ * layer by layer.  Request b owns rows [tree_indptr[b], tree_indptr[b+1]); its
+ * first add_lens[b] rows are the tokens, in order.
+ *   slots        int64 [num_tokens]: page * page_size + slot of a row's token; -1
+ *                for a row that is not appended
+ *   positions    [num_tokens]: the token's index in its sequence; 0 where slots is -1
+ *   lens_before  [max_seqs] or NULL: seq_lens as they were.  With them in place of
+ *                seq_lens, csgmv_tree_attention sees the cache without the new
+ *                tokens, which it takes from k_new and v_new (prompts).  With
+ *                seq_lens and a mask of zeros, a single new token is seen from the
+ *                cache (plain decoding).
+ * Requests are left out as by csgmv_kv_commit.  A tree_indptr that decreases or
+ * leaves [0, num_tokens] (CSGMV_KV_STATUS_BAD_LENS), or too few free pages
+ * (CSGMV_KV_STATUS_CAPACITY): nothing is extended, all slots are -1.  bs <=
+ * max_seqs.  No two of the call's buffers overlap one another or the cache's.
+ */
+CSGMV_API int csgmv_kv_extend(const csgmv_kv_cache *kv, const int32_t *add_lens, const int32_t *tree_indptr,
+                              const int32_t *seq_slots, int bs, int64_t num_tokens, int64_t *slots, int32_t *positions,
+                              int32_t *lens_before, csgmv_stream_t stream);
+
+/*
+ * Writes the rows of k and v into their slots of one layer of the cache, k
+ * turned by its positions on the way, and turns q beside them.
+ *   rope        NULL: nothing is turned (positions may then be NULL)
+ *   q, k, v     dtype of the cache, strided as in csgmv_rotary; k and v have
+ *               the cache's heads and head_dim; q may be NULL (num_q_heads 0)
+ *   slots       [num_tokens], from csgmv_kv_extend; rows of a slot outside
+ *               [0, num_pages * page_size) are left out (-1 without a word, others with
+ *               CSGMV_KV_STATUS_BAD_PAGE): nothing is written for them
+ *   q_out       the turned queries; may be q
+ *   k_out       the turned keys, or NULL; may be k
+ * A slot that is listed twice holds one of its rows' elements, which is not said.
+ * No output overlaps an input (but q_out and k_out as said), another output, the
+ * cache's pages or its bookkeeping.
+ */
+CSGMV_API int csgmv_kv_append(const csgmv_kv_cache *kv, int layer, const csgmv_rope *rope, const int32_t *positions,
+                              const int64_t *slots, int64_t num_tokens, const void *q, int64_t q_token_stride,
+                              int64_t q_head_stride, int num_q_heads, const void *k, int64_t k_token_stride,
+                              int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                              void *q_out, int64_t qo_token_stride, int64_t qo_head_stride, void *k_out,
+                              int64_t ko_token_stride, int64_t ko_head_stride, csgmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@ fallback: if the library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -36,7 +37,8 @@ EXPORTED = ["csgmv_last_error", "csgmv_version", "csgmv_chunk_size", "csgmv_batc
             "embedding_lora_a_transposed", "csgmv_transpose_embedding",
             "csgmv_kv_scratch_ints", "csgmv_kv_commit", "csgmv_kv_fork", "csgmv_kv_free", "csgmv_kv_compact",
             "csgmv_kv_copy_pages", "csgmv_tree_attention", "csgmv_tree_attention_workspace_bytes",
-            "csgmv_build_draft_tree", "csgmv_verify_drafts", "csgmv_add_norm"]
+            "csgmv_build_draft_tree", "csgmv_verify_drafts", "csgmv_add_norm", "csgmv_rope_turns",
+            "csgmv_rotary", "csgmv_kv_extend", "csgmv_kv_append"]
 
 # csgmv_qkv_path results (CSGMV_PATH_*)
 PATHS = {0: "fused", 1: "decode", 2: "small_split", 3: "stream"}
@@ -69,6 +71,11 @@ class _KvCacheC(ctypes.Structure):
 
 class _NormC(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float), ("kind", ctypes.c_int32)]
+
+
+class _RopeC(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("scale", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -124,6 +131,12 @@ def lib():
                                       vp]),
         "csgmv_add_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, i64, ctypes.POINTER(_NormC), ctypes.POINTER(_NormC), f32,
                                  i64, i32, vp, i64, vp, i64, vp]),
+        "csgmv_rope_turns": (i32, [vp, i32, vp]),
+        "csgmv_rotary": (i32, [ctypes.POINTER(_RopeC), i32, i32, vp, i64, vp, i64, i64, i32, vp, i64, i64, i32, vp, i64, i64,
+                               vp, i64, i64, i32, vp]),
+        "csgmv_kv_extend": (i32, [kvp, vp, vp, vp, i32, i64, vp, vp, vp, vp]),
+        "csgmv_kv_append": (i32, [kvp, i32, ctypes.POINTER(_RopeC), vp, vp, i64, vp, i64, i64, i32, vp, i64, i64, vp, i64, i64,
+                                  vp, i64, i64, vp, i64, i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -526,6 +539,19 @@ class KvCache:
                    torch.full((max_seqs, max_pages_per_seq), -1, **i32), torch.zeros(max_seqs, **i32),
                    torch.zeros(num_pages, **i32), layout=layout)
 
+    def with_lens(self, seq_lens: torch.Tensor) -> "KvCache":
+        """The same cache (pages, table, counts, scratch, status) seen with other
+        lengths, e.g. those before csgmv_kv_extend: for calls that read it."""
+        _need_i32(self.device, "seq_lens", seq_lens, self.max_seqs)
+        other = object.__new__(KvCache)
+        other.__dict__.update(self.__dict__)
+        other.seq_lens = seq_lens
+        other.c = _KvCacheC()
+        ctypes.pointer(other.c)[0] = self.c
+        other.c.seq_lens = seq_lens.data_ptr()
+        other._ref = ctypes.byref(other.c)
+        return other
+
     def device_status(self) -> int:
         return int(self.status.item())
 
@@ -827,3 +853,199 @@ def csgmv_add_norm(x: torch.Tensor, norm: Norm | None, out: torch.Tensor | None 
     if rc:
         _check(rc)
     return out
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | None = None):
+    """(radians a position of each pair, float64 on the CPU; the factor of the
+    turned part) of rotary positions: base ** (-2 i / rotary_dim), stretched for
+    contexts longer than the trained one by scaling:
+
+      ("linear", factor)      every angle divided by factor
+      ("ntk", factor)         base * factor ** (rotary_dim / (rotary_dim - 2)) in
+                              place of base
+      ("wavelength", factor, low, high, original)
+                              a pair that makes fewer than low turns in the original
+                              context is divided by factor, one that makes more than
+                              high is kept, others are blended in between
+      ("yarn", factor, original[, fast = 32, slow = 1])
+                              pairs from the one that makes `fast` turns in the
+                              original context to the one that makes `slow` are
+                              blended along their index; the turned part is
+                              multiplied by 0.1 ln(factor) + 1"""
+    _need(rotary_dim >= 0 and rotary_dim % 2 == 0, f"rotary_dim {rotary_dim} must be even and not negative")
+    _need(base > 0, "base must be positive")
+    n = rotary_dim // 2
+    i = torch.arange(n, dtype=torch.float64)
+    if n == 0:
+        return i, 1.0
+    f = base ** (-2.0 * i / rotary_dim)
+    if scaling is None:
+        return f, 1.0
+    kind, more = scaling[0], scaling[1:]
+    lengths = {"linear": (1,), "ntk": (1,), "wavelength": (4,), "yarn": (2, 4)}
+    _need(kind in lengths and len(more) in lengths[kind] and all(v > 0 for v in more),
+          f"scaling {scaling!r} is none of those that are known, or not positive")
+    factor = float(more[0])
+    if kind == "linear":
+        return f / factor, 1.0
+    if kind == "ntk":
+        _need(rotary_dim > 2, "ntk scaling needs a rotary_dim above 2")
+        return (base * factor ** (rotary_dim / (rotary_dim - 2.0))) ** (-2.0 * i / rotary_dim), 1.0
+    if kind == "wavelength":
+        _, low, high, original = more
+        _need(high > low, "wavelength scaling needs low < high")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        return f * (keep + (1 - keep) / factor), 1.0
+    _need(base != 1.0, "yarn scaling needs a base other than 1")
+    original, (fast, slow) = more[1], more[2:] or (32.0, 1.0)
+
+    def pair(turns):
+        return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), n - 1)
+    blend = ((i - lo) / max(hi - lo, 0.001)).clamp(0.0, 1.0)
+    return f * (1 - blend) + f / factor * blend, 0.1 * math.log(factor) + 1.0
+
+
+def csgmv_rope_turns(freq) -> torch.Tensor:
+    """Frequencies (radians a position) in 2^-64 turns, as an int64 tensor that
+    holds the unsigned numbers' bits."""
+    freq = torch.as_tensor(freq, dtype=torch.float64).cpu().contiguous()
+    turns = torch.empty(freq.shape, dtype=torch.int64)
+    _check(lib().csgmv_rope_turns(freq.data_ptr(), freq.numel(), turns.data_ptr()))
+    return turns
+
+
+class Rope:
+    """Rotary positions of heads of head_dim: the first rotary_dim elements
+    (None: all), pairs (2 i, 2 i + 1) if interleaved, else (i, i + rotary_dim / 2).
+    freq (radians a position of each pair) and scale take the place of what
+    rope_frequencies(rotary_dim, base, scaling) gives."""
+
+    def __init__(self, head_dim: int, rotary_dim: int | None = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: tuple | None = None, freq=None, scale: float | None = None, device="cuda"):
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        _need(rotary_dim <= head_dim, f"rotary_dim {rotary_dim} exceeds head_dim {head_dim}")
+        own, factor = rope_frequencies(rotary_dim, base, scaling)
+        self.freq = own if freq is None else torch.as_tensor(freq, dtype=torch.float64).cpu()
+        _need(self.freq.shape == own.shape, f"freq must have {rotary_dim // 2} entries")
+        self.scale = factor if scale is None else scale
+        self.head_dim, self.rotary_dim, self.interleaved = head_dim, rotary_dim, bool(interleaved)
+        self.turns = csgmv_rope_turns(self.freq).to(device)
+        _need(self.turns.is_cuda, "a rope's device must be a CUDA device")
+        self.device = self.turns.get_device()
+        self.c = _RopeC(self.turns.data_ptr(), self.scale, rotary_dim, int(interleaved))
+        self._ref = ctypes.byref(self.c)
+
+
+def _head_strides(name: str, t: torch.Tensor, n: int, heads, d: int, dtype, device: int):
+    """t is (n, heads, d) in that type on that GPU, its heads dense; its strides."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or heads is not None and shape[1] != heads or shape[2] != d or \
+            t.dtype is not dtype or t.get_device() != device or n and d > 1 and st[2] != 1:
+        raise CsgmvError(-1, f"{name} must be ({n}, {'heads' if heads is None else heads}, {d}) of {dtype} on cuda:{device}, "
+                             f"its heads dense, not {tuple(shape)} of {t.dtype} on {t.device}")
+    return st
+
+
+def csgmv_rotary(rope: Rope, positions: torch.Tensor, q: torch.Tensor, k: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, inverse: bool = False, stream=None):
+    """q and k (tokens, heads, head_dim; bf16, f16 or f32) turned by positions
+    (int32, (tokens,)) into q_out and k_out (None: in place); returns those.
+    inverse: by the negative angles (the gradient of the inputs from that of the
+    outputs)."""
+    n, d, dtype, device = q.shape[0], rope.head_dim, q.dtype, rope.device
+    if dtype not in _DTYPES:
+        raise CsgmvError(-1, f"q must be bf16, f16 or f32, not {dtype}")
+    _need_i32(device, "positions", positions, n)
+    qs = _head_strides("q", q, n, None, d, dtype, device)
+    hq, hk = q.shape[1], 0
+    if q_out is None or q_out is q:
+        q_out, qos = q, qs
+    else:
+        qos = _head_strides("q_out", q_out, n, hq, d, dtype, device)
+    if k is None:
+        if k_out is not None:
+            raise CsgmvError(-1, "k_out without k")
+        ks = kos = (0, 0)
+    else:
+        ks = _head_strides("k", k, n, None, d, dtype, device)
+        hk = k.shape[1]
+        if k_out is None or k_out is k:
+            k_out, kos = k, ks
+        else:
+            kos = _head_strides("k_out", k_out, n, hk, d, dtype, device)
+    rc = lib().csgmv_rotary(rope._ref, _DTYPES[dtype], d, positions.data_ptr(), n, q.data_ptr(), qs[0], qs[1], hq, _at(k), ks[0],
+                            ks[1], hk, q_out.data_ptr(), qos[0], qos[1], _at(k_out), kos[0], kos[1], inverse,
+                            _raw_stream(stream, device))
+    if rc:
+        _check(rc)
+    return q_out, k_out
+
+
+def csgmv_kv_extend(cache: KvCache, tree_indptr: torch.Tensor, num_tokens: int, add_lens: torch.Tensor | None = None,
+                    seq_slots: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                    positions: torch.Tensor | None = None, lens_before: torch.Tensor | None = None, stream=None):
+    """Room for add_lens[b] (None: all) of request b's rows of a batch of
+    num_tokens rows in its sequence: (slots int64, positions int32), one of each a
+    row, allocated on the call's stream unless given.  lens_before (int32,
+    (max_seqs,)) gets the lengths as they were (KvCache.with_lens)."""
+    device = cache.device
+    bs = tree_indptr.shape[0] - 1 if tree_indptr.dim() else -1
+    _need_i32(device, "tree_indptr", tree_indptr, bs + 1)
+    if add_lens is not None:
+        _need_i32(device, "add_lens", add_lens, bs)
+    if seq_slots is not None:
+        _need_i32(device, "seq_slots", seq_slots, bs)
+    if lens_before is not None:
+        _need_i32(device, "lens_before", lens_before, cache.max_seqs)
+    if slots is None:
+        slots = _empty(stream, num_tokens, dtype=torch.int64, device=cache.k_pages.device)
+    elif slots.dtype is not torch.int64 or slots.shape != (num_tokens,) or not slots.is_contiguous() or slots.get_device() != device:
+        raise CsgmvError(-1, f"slots must be a contiguous int64 tensor of shape ({num_tokens},) on cuda:{device}")
+    if positions is None:
+        positions = _empty(stream, num_tokens, dtype=torch.int32, device=cache.k_pages.device)
+    else:
+        _need_i32(device, "positions", positions, num_tokens)
+    rc = lib().csgmv_kv_extend(cache._ref, _at(add_lens), tree_indptr.data_ptr(), _at(seq_slots), bs, num_tokens,
+                               slots.data_ptr(), positions.data_ptr(), _at(lens_before), _raw_stream(stream, device))
+    if rc:
+        _check(rc)
+    return slots, positions
+
+
+def csgmv_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    positions: torch.Tensor | None = None, rope: Rope | None = None, q: torch.Tensor | None = None,
+                    q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None) -> None:
+    """Rows of k (turned by positions if there is a rope) and v (tokens,
+    kv_heads, head_dim) into their slots of a layer of the cache, and q
+    (tokens, heads, head_dim) turned into q_out (None: in place).  k_out, which
+    may be k, gets the turned keys too."""
+    n, d, dtype, device = k.shape[0], cache.head_dim, cache.dtype, cache.device
+    ks = _head_strides("k", k, n, cache.num_kv_heads, d, dtype, device)
+    vs = _head_strides("v", v, n, cache.num_kv_heads, d, dtype, device)
+    if slots.dtype is not torch.int64 or slots.shape != (n,) or not slots.is_contiguous() or slots.get_device() != device:
+        raise CsgmvError(-1, f"slots must be a contiguous int64 tensor of shape ({n},) on cuda:{device}")
+    if rope is not None:
+        if rope.head_dim != d or rope.device != device or positions is None:
+            raise CsgmvError(-1, f"a rope for heads of {rope.head_dim} on cuda:{rope.device} and no or some positions, for heads "
+                                 f"of {d} on cuda:{device}")
+        _need_i32(device, "positions", positions, n)
+    qs = qos = kos = (0, 0)
+    hq = 0
+    if q is not None:
+        qs = _head_strides("q", q, n, None, d, dtype, device)
+        hq = q.shape[1]
+        if q_out is None or q_out is q:
+            q_out, qos = q, qs
+        else:
+            qos = _head_strides("q_out", q_out, n, hq, d, dtype, device)
+    elif q_out is not None:
+        raise CsgmvError(-1, "q_out without q")
+    if k_out is not None:
+        kos = _head_strides("k_out", k_out, n, cache.num_kv_heads, d, dtype, device)
+    rc = lib().csgmv_kv_append(
+        cache._ref, layer, None if rope is None else rope._ref, _at(positions), slots.data_ptr(), n, _at(q), qs[0], qs[1], hq,
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _at(q_out), qos[0], qos[1], _at(k_out), kos[0], kos[1],
+        _raw_stream(stream, device))
+    if rc:
+        _check(rc)

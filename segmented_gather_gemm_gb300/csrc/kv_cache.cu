@@ -15,6 +15,8 @@
 // move 5 TB/s; of 4 requests 10.8 us, the chain of loads of both.  Fork, free
 // and compaction of 512 sequences (4.3 GB) 678 us, 6.4 TB/s; of 16 small ones
 // 20 us, five launches one behind the other.
+#include <algorithm>
+
 #include "serving.cuh"
 
 namespace csgmv {
@@ -169,8 +171,12 @@ __device__ __forceinline__ int pages_of(const Kv &c, int tokens) { return (token
 // sequence slot; pa: the pages given out.  A warp of the cluster a request: what
 // the plan takes is a chain of dependent loads, so it is kept as short as the
 // requests allow.
+// EXTEND: the same for rows whose contents come later: lengths may be those of
+// tree_indptr, which has to be sound as a whole (a row is then one request's at
+// most); lens_before (or NULL) gets the lengths as they are.
+template <bool EXTEND>
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-commit_plan(Kv c, CommitParams p) {
+commit_plan(Kv c, CommitParams p, int32_t *lens_before) {
     __shared__ PlanSmem sm;
     griddep_launch_dependents();
     griddep_wait();
@@ -180,6 +186,8 @@ commit_plan(Kv c, CommitParams p) {
     const Stretch s = stretch(c.pages);
     auto slot_of = [&](int b) { return p.seq_slots ? p.seq_slots[b] : b; };
     auto in = [&](int q) { return q >= 0 && q < c.seqs; };
+    if (EXTEND && lens_before)
+        for (int q = gt; q < c.seqs; q += kAllThreads) lens_before[q] = c.lens[q];
     if (p.seq_slots) {  // (without slots none can come twice)
         for (int b = gt; b < p.bs; b += kAllThreads)
             if (in(slot_of(b))) c.mark[slot_of(b)] = INT32_MAX;
@@ -190,8 +198,8 @@ commit_plan(Kv c, CommitParams p) {
     }
     // is the request sound?  sa: its rows, sb: the length before, sd: pages it needs
     for (int b = gw; b < p.bs; b += kAllWarps) {
-        const int q = slot_of(b), add = p.accept_len[b];
-        const int lo = p.tree_indptr[b], hi = p.tree_indptr[b + 1];
+        const int q = slot_of(b), lo = p.tree_indptr[b], hi = p.tree_indptr[b + 1];
+        const int add = EXTEND && !p.accept_len ? hi - lo : p.accept_len[b];
         int bad = 0, old = 0;
         bool wrong = false;
         if (p.accept_index)  // read beside the rest: a bad count is cut to what is there
@@ -228,8 +236,13 @@ commit_plan(Kv c, CommitParams p) {
     cluster_sync();
     if (rank == 0) {  // running sums of rows and of pages over the requests
         long long sum = 0;
+        bool torn = false;
         for (int b0 = 0; b0 < p.bs; b0 += kPlanThreads) {
             const int b = b0 + tid;
+            if (EXTEND && b < p.bs) {
+                const int lo = p.tree_indptr[b], hi = p.tree_indptr[b + 1];
+                torn |= lo < 0 || hi < lo || hi > p.num_tokens;
+            }
             long long t;
             const long long own = b < p.bs ? (long long)c.sa[b] << 32 | (unsigned)c.sd[b] : 0;
             const long long pre = sum + block_scan_ex(own, sm.scan, &t);
@@ -239,21 +252,22 @@ commit_plan(Kv c, CommitParams p) {
             }
             sum += t;
         }
+        if (EXTEND) torn = __syncthreads_or(torn);
         if (tid == 0) {
             c.sa[p.bs] = (int)(sum >> 32);
-            sm.a = (int)sum;
+            sm.a = torn ? -1 : (int)sum;
         }
     }
     int nfree;
     const int before = count_before(sm, &nfree);
     cluster_sync();
     const int need = dsmem_ld_i32(dsmem_addr(&sm.a, 0));
-    const bool fits = need <= nfree;
+    const bool fits = need >= 0 && need <= nfree;
     if (fits) list_free(c, s, before, need, c.pa);
     __threadfence();
     cluster_sync();
     if (gt == 0) {
-        if (!fits) atomicOr(c.status, CSGMV_KV_STATUS_CAPACITY);
+        if (!fits) atomicOr(c.status, need < 0 ? CSGMV_KV_STATUS_BAD_LENS : CSGMV_KV_STATUS_CAPACITY);
         c.head[kHRows] = fits ? c.sa[p.bs] : 0;
     }
     if (!fits) return;
@@ -281,6 +295,20 @@ commit_plan(Kv c, CommitParams p) {
             c.refs[pg] = 1;
         }
         if (lane == 0) c.lens[q] = old + add;
+    }
+}
+
+// CTAs copy the pages that were shared (sc, sd of the plan) in every layer.
+__device__ void copy_shared(const Kv &c, int bs) {
+    for (int b = blockIdx.x; b < bs; b += gridDim.x) {
+        const int from = c.sc[b];
+        if (from < 0) continue;
+        const int to = c.sd[b], ntok = c.sb[b] & (c.ps - 1);
+        for (int l = 0; l < c.layers; ++l) {
+            const int64_t a = l * c.layer_stride + from * c.page_stride, z = l * c.layer_stride + to * c.page_stride;
+            copy_page<2>(c, c.k + a, c.k + z, ntok, threadIdx.x, kMoveThreads);
+            copy_page<2>(c, c.v + a, c.v + z, ntok, threadIdx.x, kMoveThreads);
+        }
     }
 }
 
@@ -328,16 +356,37 @@ __global__ void __launch_bounds__(kMoveThreads, 4) commit_move(Kv c, CommitParam
             }
         }
     }
-    for (int b = blockIdx.x; b < p.bs; b += gridDim.x) {
-        const int from = c.sc[b];
-        if (from < 0) continue;
-        const int to = c.sd[b], ntok = c.sb[b] & (c.ps - 1);
-        for (int l = 0; l < c.layers; ++l) {
-            const int64_t a = l * c.layer_stride + from * c.page_stride, z = l * c.layer_stride + to * c.page_stride;
-            copy_page<2>(c, c.k + a, c.k + z, ntok, threadIdx.x, kMoveThreads);
-            copy_page<2>(c, c.v + a, c.v + z, ntok, threadIdx.x, kMoveThreads);
+    copy_shared(c, p.bs);
+}
+
+// What csgmv_kv_extend leaves: the slot and position of every row; and the
+// copies of shared pages.  A thread a row: its request is the last one that
+// begins at or before it (the plan found tree_indptr sound).
+__global__ void __launch_bounds__(kMoveThreads) extend_fill(Kv c, ExtendParams e) {
+    griddep_wait();
+    const CommitParams &p = e.plan;
+    const bool any = c.head[kHRows] != 0;
+    for (int64_t t = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; t < p.num_tokens; t += (int64_t)gridDim.x * kMoveThreads) {
+        int64_t slot = -1;
+        int pos = 0;
+        if (any && t >= p.tree_indptr[0]) {
+            int b = 0;
+            for (int len = p.bs; len > 1;) {
+                const int half = len >> 1;
+                if (p.tree_indptr[b + half] <= t) b += half, len -= half;
+                else len = half;
+            }
+            const int64_t j = t - p.tree_indptr[b];
+            if (j < c.sa[b + 1] - c.sa[b]) {
+                const int q = p.seq_slots ? p.seq_slots[b] : b;
+                pos = c.sb[b] + (int)j;
+                slot = ((int64_t)c.table[(int64_t)q * c.max_pages + (pos >> c.ps_shift)] << c.ps_shift) + (pos & (c.ps - 1));
+            }
         }
+        e.slots[t] = slot;
+        e.positions[t] = pos;
     }
+    if (any) copy_shared(c, p.bs);
 }
 
 // --------------------------------------------------------------------- fork
@@ -571,11 +620,19 @@ dim3 grid_for(int64_t units) {
 
 cudaError_t launch_kv_commit(const csgmv_kv_cache &kv, const CommitParams &p, cudaStream_t stream) {
     const Kv c = view(kv);
-    cudaError_t e = launch_kernel(commit_plan, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c, p);
+    cudaError_t e = launch_kernel(commit_plan<false>, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c, p, (int32_t *)nullptr);
     if (e != cudaSuccess) return e;
     // at most every row of the batch, eight (row, layer) pairs a block
     return launch_kernel(commit_move, grid_for((p.num_tokens * c.layers + 7) / 8), kMoveThreads, 0, stream, 0, true, c,
                          p);
+}
+
+cudaError_t launch_kv_extend(const csgmv_kv_cache &kv, const ExtendParams &p, cudaStream_t stream) {
+    const Kv c = view(kv);
+    cudaError_t e = launch_kernel(commit_plan<true>, dim3(kPlanCtas), kPlanThreads, 0, stream, 0, true, c, p.plan, p.lens_before);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (p.plan.num_tokens + kMoveThreads - 1) / kMoveThreads;
+    return launch_kernel(extend_fill, grid_for(std::max<int64_t>(blocks, p.plan.bs)), kMoveThreads, 0, stream, 0, true, c, p);
 }
 
 cudaError_t launch_kv_fork(const csgmv_kv_cache &kv, const int32_t *parents, const int32_t *children, int n,

@@ -25,6 +25,12 @@ struct CommitParams {
     int bs;
 };
 cudaError_t launch_kv_commit(const csgmv_kv_cache &kv, const CommitParams &p, cudaStream_t stream);
+struct ExtendParams {
+    CommitParams plan;  // num_tokens, accept_len (NULL: all rows), tree_indptr, seq_slots, bs
+    int64_t *slots;
+    int32_t *positions, *lens_before;
+};
+cudaError_t launch_kv_extend(const csgmv_kv_cache &kv, const ExtendParams &p, cudaStream_t stream);
 cudaError_t launch_kv_fork(const csgmv_kv_cache &kv, const int32_t *parents, const int32_t *children, int n,
                            cudaStream_t stream);
 cudaError_t launch_kv_free(const csgmv_kv_cache &kv, const int32_t *seqs, const int32_t *keep, int n,

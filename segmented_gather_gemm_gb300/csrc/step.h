@@ -28,4 +28,28 @@ struct AddNormParams {
 };
 cudaError_t launch_add_norm(const AddNormParams &p, cudaStream_t stream);
 
+// Heads of one tensor: element (t, h, d) at at + t * ts + h * hs + d.
+struct Heads {
+    const void *in;
+    void *out;  // or NULL
+    int64_t ts, hs, o_ts, o_hs;
+    int n;
+};
+struct RotaryParams {
+    const uint64_t *turns;  // [rot / 2]
+    const int32_t *positions;
+    float scale, sign;      // sign -1: by the negative angles
+    int rot, interleaved, d, dtype;
+    int64_t num_tokens;
+    Heads q, k;
+    // appending to a layer of the cache (v, slots); slots NULL: only turning
+    Heads v;
+    const int64_t *slots;
+    void *k_pages, *v_pages;  // of the layer
+    int64_t page_stride, head_stride, token_stride, num_slots;
+    int page_shift;
+    int32_t *status;
+};
+cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream);
+
 }  // namespace csgmv

@@ -1,6 +1,8 @@
 // C ABI of what a decoder does between the projections, the attention and the
 // verification: argument checks on the host, then the launches of each call
 // on the caller's stream.  Nothing here allocates, frees or synchronizes.
+#include <cmath>
+
 #include "serving_checks.h"
 #include "elements.cuh"
 #include "step.h"
@@ -20,7 +22,7 @@ Rows rows_of(const void *at, int bytes, int64_t n, int64_t ts, int64_t heads, in
     if (!at || n <= 0 || heads <= 0) return {nullptr, 0, 0, 0, 0, 0};
     return {at, n, ts * bytes, heads, hs * bytes, row * bytes};
 }
-Rows plain(const void *at, size_t bytes) { return {bytes ? at : nullptr, 1, 0, 1, 0, (int64_t)bytes}; }
+Rows plain(const void *at, size_t bytes) { return {bytes ? at : nullptr, 1, 0, 1, 0, (int64_t)std::min<size_t>(bytes, INT64_MAX)}; }
 
 bool same(const Rows &a, const Rows &b) {
     return a.at == b.at && a.n == b.n && a.heads == b.heads && a.row == b.row && (a.n == 1 || a.ts == b.ts) &&
@@ -56,8 +58,42 @@ bool meet(const Rows &a, const Rows &b) {
 // An output may be the input of the same place, element by element, or apart from it.
 bool in_place_or_apart(const Rows &out, const Rows &in) { return same(out, in) || !meet(out, in); }
 
+// turns and the rest of a rope for heads of head_dim elements; 0 or an error.
+int check_rope(const csgmv_rope *rope, int head_dim) {
+    if (rope->rotary_dim < 0 || rope->rotary_dim % 2 || rope->rotary_dim > head_dim)
+        return fail(CSGMV_ERR_INVALID_ARG, "rotary_dim %d must be even and at most head_dim %d", rope->rotary_dim, head_dim);
+    if (rope->rotary_dim && (!rope->turns || !aligned_to(rope->turns, 8)))
+        return fail(CSGMV_ERR_INVALID_ARG, "turns is NULL or not 8-byte aligned");
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+        return fail(CSGMV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+    if (!(rope->scale - rope->scale == 0.0f)) return fail(CSGMV_ERR_INVALID_ARG, "a rope's scale must be finite");
+    return CSGMV_OK;
+}
+
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements; a row's offset stays within 64 bits
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
+
+// From the first element of k_pages or v_pages to the last, all layers.
+size_t kv_pool_bytes(const csgmv_kv_cache *kv) {
+    return 2 * ((size_t)(kv->num_layers - 1) * kv->layer_stride + (size_t)(kv->num_pages - 1) * kv->page_stride +
+                (size_t)(kv->num_kv_heads - 1) * kv->head_stride + (size_t)(kv->page_size - 1) * kv->token_stride + kv->head_dim);
+}
+
+// Queries or keys of a call, and their outputs: 0 or an error.
+int check_heads(const char *name, const csgmv::Heads &h, int64_t n, int d, int bytes, bool need_out) {
+    if (h.n < 0 || h.n > 4096) return fail(CSGMV_ERR_UNSUPPORTED, "%d heads of %s outside 0..4096", h.n, name);
+    if (h.n == 0) return CSGMV_OK;
+    if (!h.in || (need_out && !h.out)) return fail(CSGMV_ERR_INVALID_ARG, "%s or its output is NULL", name);
+    if (!aligned_to(h.in, bytes) || !aligned_to(h.out, bytes))
+        return fail(CSGMV_ERR_INVALID_ARG, "%s or its output is not aligned to its type", name);
+    if (!stride_ok(h.ts) || !stride_ok(h.hs) || !stride_ok(h.o_ts) || !stride_ok(h.o_hs))
+        return fail(CSGMV_ERR_INVALID_ARG, "a stride of %s or its output is negative or above 2^40", name);
+    if (h.out && !apart(d, {{n, h.o_ts}, {h.n, h.o_hs}}))
+        return fail(CSGMV_ERR_INVALID_ARG, "rows of the output of %s overlap", name);
+    return CSGMV_OK;
+}
+Rows in_rows(const csgmv::Heads &h, int64_t n, int d, int bytes) { return rows_of(h.in, bytes, n, h.ts, h.n, h.hs, d); }
+Rows out_rows(const csgmv::Heads &h, int64_t n, int d, int bytes) { return rows_of(h.out, bytes, n, h.o_ts, h.n, h.o_hs, d); }
 
 }  // namespace
 
@@ -126,6 +162,162 @@ int csgmv_add_norm(const void *x, int64_t x_stride, int dtype, const void *resid
     p.dtype = dtype;
     p.r_dtype = residual_dtype;
     return launched(csgmv::launch_add_norm(p, st(stream)), "csgmv_add_norm");
+}
+
+int csgmv_rope_turns(const double *freq, int n, uint64_t *turns) {
+    if (n < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative n");
+    if (n > 0 && (!freq || !turns)) return fail(CSGMV_ERR_INVALID_ARG, "freq / turns is NULL");
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(freq[i])) return fail(CSGMV_ERR_INVALID_ARG, "freq[%d] is not finite", i);
+    for (int i = 0; i < n; ++i) {
+        const double turn = freq[i] / 6.283185307179586476925;
+        const double steps = std::nearbyint(std::ldexp(turn - std::floor(turn), 64));
+        turns[i] = steps < 0x1p64 ? (uint64_t)steps : 0;  // (a whole turn is none)
+    }
+    return CSGMV_OK;
+}
+
+int csgmv_rotary(const csgmv_rope *rope, int dtype, int head_dim, const int32_t *positions, int64_t num_tokens,
+                 const void *q, int64_t q_token_stride, int64_t q_head_stride, int num_q_heads, const void *k,
+                 int64_t k_token_stride, int64_t k_head_stride, int num_k_heads, void *q_out, int64_t qo_token_stride,
+                 int64_t qo_head_stride, void *k_out, int64_t ko_token_stride, int64_t ko_head_stride, int inverse,
+                 csgmv_stream_t stream) {
+    if (!known_type(dtype)) return fail(CSGMV_ERR_INVALID_ARG, "dtype %d must be bf16, f16 or f32", dtype);
+    if (head_dim < 1 || head_dim > 1024) return fail(CSGMV_ERR_UNSUPPORTED, "head_dim %d outside 1..1024", head_dim);
+    if (!rope) return fail(CSGMV_ERR_INVALID_ARG, "rope is NULL");
+    int rc = check_rope(rope, head_dim);
+    if (rc) return rc;
+    if (num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative num_tokens");
+    if (num_tokens > INT32_MAX) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds int32");
+    if (inverse != 0 && inverse != 1) return fail(CSGMV_ERR_INVALID_ARG, "inverse must be 0 or 1");
+    csgmv::RotaryParams p = {};
+    p.q = {q, q_out, q_token_stride, q_head_stride, qo_token_stride, qo_head_stride, num_q_heads};
+    p.k = {k, k_out, k_token_stride, k_head_stride, ko_token_stride, ko_head_stride, num_k_heads};
+    const int e = csgmv::dtype_bytes(dtype);
+    if (num_tokens == 0) return CSGMV_OK;
+    if ((rc = check_heads("q", p.q, num_tokens, head_dim, e, true)) || (rc = check_heads("k", p.k, num_tokens, head_dim, e, true)))
+        return rc;
+    if (num_q_heads == 0 && num_k_heads == 0) return CSGMV_OK;
+    if (!positions || !aligned4(positions)) return fail(CSGMV_ERR_INVALID_ARG, "positions is NULL or not 4-byte aligned");
+    const Rows qi = in_rows(p.q, num_tokens, head_dim, e), ki = in_rows(p.k, num_tokens, head_dim, e);
+    const Rows qo = out_rows(p.q, num_tokens, head_dim, e), ko = out_rows(p.k, num_tokens, head_dim, e);
+    const Rows steer[] = {plain(positions, 4 * (size_t)num_tokens), plain(rope->turns, 4 * (size_t)rope->rotary_dim)};
+    bool bad = !in_place_or_apart(qo, qi) || !in_place_or_apart(ko, ki) || meet(qo, ki) || meet(ko, qi) || meet(qo, ko);
+    for (const Rows &s : steer) bad = bad || meet(qo, s) || meet(ko, s);
+    if (bad) return fail(CSGMV_ERR_INVALID_ARG, "an output overlaps an input that it is not, or the other output");
+    p.turns = rope->turns;
+    p.positions = positions;
+    p.scale = rope->scale;
+    p.sign = inverse ? -1.0f : 1.0f;
+    p.rot = rope->rotary_dim;
+    p.interleaved = rope->interleaved;
+    p.d = head_dim;
+    p.dtype = dtype;
+    p.num_tokens = num_tokens;
+    return launched(csgmv::launch_rotary(p, st(stream)), "csgmv_rotary");
+}
+
+int csgmv_kv_extend(const csgmv_kv_cache *kv, const int32_t *add_lens, const int32_t *tree_indptr,
+                    const int32_t *seq_slots, int bs, int64_t num_tokens, int64_t *slots, int32_t *positions,
+                    int32_t *lens_before, csgmv_stream_t stream) {
+    int rc = check_kv(kv);
+    if (rc) return rc;
+    if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
+    if (bs > kv->max_seqs) return fail(CSGMV_ERR_CAPACITY, "bs %d exceeds max_seqs %d", bs, kv->max_seqs);
+    if (num_tokens > INT32_MAX) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds int32");
+    if (bs > 0 && !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "tree_indptr is NULL");
+    if (num_tokens > 0 && (!slots || !positions)) return fail(CSGMV_ERR_INVALID_ARG, "slots / positions is NULL");
+    if (!aligned4(add_lens) || !aligned4(tree_indptr) || !aligned4(seq_slots) || !aligned_to(slots, 8) || !aligned4(positions) ||
+        !aligned4(lens_before))
+        return fail(CSGMV_ERR_INVALID_ARG, "a buffer is not aligned to its type");
+    const size_t pool = kv_pool_bytes(kv);
+    const struct { const void *at; size_t bytes; } all[] = {
+        {slots, 8 * (size_t)num_tokens}, {positions, 4 * (size_t)num_tokens}, {lens_before, 4 * (size_t)kv->max_seqs},
+        {add_lens, 4 * (size_t)bs}, {tree_indptr, bs ? 4 * (size_t)bs + 4 : 0}, {seq_slots, 4 * (size_t)bs}};
+    for (int i = 0; i < 6; ++i) {
+        bool bad = overlaps_plan(kv, static_cast<const int32_t *>(all[i].at), all[i].bytes / 4) ||
+                   overlaps(all[i].at, all[i].bytes, kv->k_pages, pool) || overlaps(all[i].at, all[i].bytes, kv->v_pages, pool);
+        for (int j = 0; j < i && j < 3; ++j) bad = bad || overlaps(all[i].at, all[i].bytes, all[j].at, all[j].bytes);
+        if (bad) return fail(CSGMV_ERR_INVALID_ARG, "a buffer of the call overlaps another one or the cache");
+    }
+    if (bs == 0 && num_tokens == 0 && !lens_before) return CSGMV_OK;
+    csgmv::ExtendParams p = {};
+    p.plan.num_tokens = num_tokens;
+    p.plan.accept_len = add_lens;
+    p.plan.tree_indptr = tree_indptr;
+    p.plan.seq_slots = seq_slots;
+    p.plan.bs = bs;
+    p.slots = slots;
+    p.positions = positions;
+    p.lens_before = lens_before;
+    return launched(csgmv::launch_kv_extend(*kv, p, st(stream)), "csgmv_kv_extend");
+}
+
+int csgmv_kv_append(const csgmv_kv_cache *kv, int layer, const csgmv_rope *rope, const int32_t *positions,
+                    const int64_t *slots, int64_t num_tokens, const void *q, int64_t q_token_stride,
+                    int64_t q_head_stride, int num_q_heads, const void *k, int64_t k_token_stride,
+                    int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride, void *q_out,
+                    int64_t qo_token_stride, int64_t qo_head_stride, void *k_out, int64_t ko_token_stride,
+                    int64_t ko_head_stride, csgmv_stream_t stream) {
+    int rc = check_kv(kv);
+    if (rc) return rc;
+    if (layer < 0 || layer >= kv->num_layers)
+        return fail(CSGMV_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, kv->num_layers);
+    if (rope && (rc = check_rope(rope, kv->head_dim))) return rc;
+    if (num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative num_tokens");
+    if (num_tokens > INT32_MAX) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds int32");
+    if (num_tokens == 0) return CSGMV_OK;
+    const int d = kv->head_dim, e = 2;
+    csgmv::RotaryParams p = {};
+    p.q = {q, q_out, q_token_stride, q_head_stride, qo_token_stride, qo_head_stride, num_q_heads};
+    p.k = {k, k_out, k_token_stride, k_head_stride, ko_token_stride, ko_head_stride, kv->num_kv_heads};
+    p.v = {v, nullptr, v_token_stride, v_head_stride, 0, 0, kv->num_kv_heads};
+    if ((rc = check_heads("q", p.q, num_tokens, d, e, true)) || (rc = check_heads("k", p.k, num_tokens, d, e, false)) ||
+        (rc = check_heads("v", p.v, num_tokens, d, e, false)))
+        return rc;
+    if (!slots || !aligned_to(slots, 8)) return fail(CSGMV_ERR_INVALID_ARG, "slots is NULL or not 8-byte aligned");
+    if (rope && (!positions || !aligned4(positions)))
+        return fail(CSGMV_ERR_INVALID_ARG, "positions is NULL or not 4-byte aligned");
+    const Rows qi = in_rows(p.q, num_tokens, d, e), ki = in_rows(p.k, num_tokens, d, e), vi = in_rows(p.v, num_tokens, d, e);
+    const Rows qo = out_rows(p.q, num_tokens, d, e), ko = out_rows(p.k, num_tokens, d, e);
+    bool bad = !in_place_or_apart(qo, qi) || !in_place_or_apart(ko, ki) || meet(qo, ki) || meet(qo, vi) || meet(ko, qi) ||
+               meet(ko, vi) || meet(qo, ko);
+    // the pages of the cache, all layers of them, are an output too
+    const size_t pool = kv_pool_bytes(kv);
+    const Rows pools[] = {plain(kv->k_pages, pool), plain(kv->v_pages, pool)};
+    const Rows steer[] = {plain(slots, 8 * (size_t)num_tokens), plain(rope ? positions : nullptr, 4 * (size_t)num_tokens),
+                          plain(rope ? rope->turns : nullptr, rope ? 4 * (size_t)rope->rotary_dim : 0),
+                          plain(kv->page_table, 4 * (size_t)kv->max_seqs * kv->max_pages_per_seq),
+                          plain(kv->seq_lens, 4 * (size_t)kv->max_seqs), plain(kv->page_refs, 4 * (size_t)kv->num_pages),
+                          plain(kv->status, 4)};
+    for (const Rows &x : {qo, ko}) {
+        for (const Rows &s : steer) bad = bad || meet(x, s);
+        for (const Rows &s : pools) bad = bad || meet(x, s);
+    }
+    for (const Rows &x : {qi, ki, vi, steer[0], steer[1], steer[2]})
+        for (const Rows &s : pools) bad = bad || meet(x, s);
+    if (bad) return fail(CSGMV_ERR_INVALID_ARG, "an output overlaps an input that it is not, another output or the cache");
+    if (rope) {
+        p.turns = rope->turns;
+        p.scale = rope->scale;
+        p.rot = rope->rotary_dim;
+        p.interleaved = rope->interleaved;
+    }
+    p.sign = 1.0f;
+    p.positions = positions;
+    p.d = d;
+    p.dtype = kv->dtype;
+    p.num_tokens = num_tokens;
+    p.slots = slots;
+    p.k_pages = static_cast<uint16_t *>(kv->k_pages) + (int64_t)layer * kv->layer_stride;
+    p.v_pages = static_cast<uint16_t *>(kv->v_pages) + (int64_t)layer * kv->layer_stride;
+    p.page_stride = kv->page_stride;
+    p.head_stride = kv->head_stride;
+    p.token_stride = kv->token_stride;
+    p.num_slots = (int64_t)kv->num_pages * kv->page_size;
+    p.page_shift = __builtin_ctz((unsigned)kv->page_size);
+    p.status = kv->status;
+    return launched(csgmv::launch_rotary(p, st(stream)), "csgmv_kv_append");
 }
 
 }  // extern "C"

@@ -63,3 +63,55 @@ def close(got, want, tol, dtype=None):
     bound = bound.expand_as(want) if bound.dim() else bound.repeat(want.shape)
     over = ((got - want).abs() - bound)[finite]
     assert not bool((over > 0).any()), f"{int((over > 0).sum())} of {over.numel()} too far off, by up to {float(over.max()):.3g}"
+
+
+def rotary(x, positions, freq, rot, interleaved, scale=1.0, inverse=False):
+    """(x turned, tolerance) in float64; x (n, heads, d).
+
+    The angle enters the sine as a number of at most one half turn with 24 bits
+    (2^-22.3 radians) and cosine and sine are off by two units in the last place:
+    less than 2^-21 together.  Two products and their sum: 2^-22 more.  The
+    reference's own angle is off by 2^-53 of itself."""
+    x = x.double().cpu()
+    a = positions.double().cpu()[:, None] * freq.double().cpu()
+    off = (a.abs().amax(-1) if a.numel() else a.sum(-1)) * 2.0 ** -52 + 2.0 ** -20
+    a = (-a if inverse else a)[:, None, :]
+    u, v = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
+    c, s = a.cos() * scale, a.sin() * scale
+    pair, size = [u * c - v * s, u * s + v * c], abs(scale) * (u.abs() + v.abs())
+    join = (lambda p: torch.stack(p, -1).flatten(-2)) if interleaved else (lambda p: torch.cat(p, -1))
+    y, tol = torch.cat([join(pair), x[..., rot:]], -1), torch.zeros_like(x)
+    tol[..., :rot] = join([size, size]) * off[:, None, None]
+    return y, tol
+
+
+class Cache:
+    """A paged cache as csgmv.h describes it, as lists of Python numbers: pages
+    are given out lowest first, a shared page that is not full is copied before
+    it is appended to."""
+
+    def __init__(self, cache):
+        self.ps, self.width = cache.page_size, cache.max_pages_per_seq
+        self.table = cache.page_table.tolist()
+        self.lens = cache.seq_lens.tolist()
+        self.refs = cache.page_refs.tolist()
+
+    def extend(self, seq, n):
+        """[(slot)] of n more tokens, [(from page, to page, tokens)] of the copies."""
+        old, copies = self.lens[seq], []
+        need = math.ceil((old + n) / self.ps) - math.ceil(old / self.ps)
+        free = [p for p, c in enumerate(self.refs) if c == 0]
+        if n and old % self.ps:
+            last = self.table[seq][old // self.ps]
+            if self.refs[last] > 1:
+                to = free.pop(0)
+                self.refs[last] -= 1
+                self.refs[to] = 1
+                self.table[seq][old // self.ps] = to
+                copies.append((last, to, old % self.ps))
+        for i in range(need):
+            page = free.pop(0)
+            self.refs[page] = 1
+            self.table[seq][math.ceil(old / self.ps) + i] = page
+        self.lens[seq] = old + n
+        return [self.table[seq][p // self.ps] * self.ps + p % self.ps for p in range(old, old + n)], copies
