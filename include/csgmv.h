@@ -764,6 +764,101 @@ CSGMV_API int csgmv_kv_append(const csgmv_kv_cache *kv, int layer, const csgmv_r
                               void *q_out, int64_t qo_token_stride, int64_t qo_head_stride, void *k_out,
                               int64_t ko_token_stride, int64_t ko_head_stride, csgmv_stream_t stream);
 
+/*
+ * How often each sequence holds each token.  counts[s * vocab_size + v] is the
+ * number of times that sequence s gave token v, plus 2^30 if its prompt has it;
+ * seen[s * vocab_size + i], i < num_seen[s], lists the tokens whose count is not
+ * zero, each once, in no certain order.  The caller allocates the buffers; all
+ * zero (seen: anything) is empty.
+ */
+typedef struct csgmv_token_counts {
+    int32_t *counts, *seen; /* [max_seqs][vocab_size] */
+    int32_t *num_seen;      /* [max_seqs] */
+    int32_t *status;        /* [1] CSGMV_KV_STATUS_* bits */
+    int32_t max_seqs, vocab_size;
+} csgmv_token_counts;
+
+/*
+ * Counts tokens of request b for sequence seq_slots[b] (b when NULL): the first
+ * accept_len[b] (NULL: all) of rows tree_indptr[b] + accept_index[b * accept_width
+ * + j] (NULL: j) of tokens: what csgmv_kv_commit appends for the same lists.
+ * prompt 1: they are the sequence's prompt.  A sequence may come several times,
+ * and so may a token.  A request with a bad sequence, length or node is left out;
+ * a token outside the vocabulary is (CSGMV_KV_STATUS_BAD_TOKEN).  A sequence may
+ * give a token at most 2^30 - 1 times.
+ */
+CSGMV_API int csgmv_count_tokens(const csgmv_token_counts *counts, const int32_t *tokens, int64_t num_tokens,
+                                 const int32_t *tree_indptr, const int32_t *accept_index, int accept_width,
+                                 const int32_t *accept_len, const int32_t *seq_slots, int bs, int prompt,
+                                 csgmv_stream_t stream);
+
+/* Empties the sequences seqs[i], i < n. */
+CSGMV_API int csgmv_count_reset(const csgmv_token_counts *counts, const int32_t *seqs, int n, csgmv_stream_t stream);
+
+/* children[i] becomes a copy of parents[i], i < n.  A child must be empty, may
+ * appear once, and may not be a parent in the same call; an entry that breaks
+ * this is left out (CSGMV_KV_STATUS_BAD_SEQ).  n <= max_seqs. */
+CSGMV_API int csgmv_count_fork(const csgmv_token_counts *counts, const int32_t *parents, const int32_t *children,
+                               int n, csgmv_stream_t stream);
+
+/*
+ * What csgmv_process_logits does to a row of request b.  Any pointer may be
+ * NULL: then that step is left out.
+ *   repetition, frequency, presence, temperature   [bs]; repetition > 0 and
+ *                 temperature >= 0, both finite, none NaN
+ *   bias_tokens, bias_values   entries [bias_indptr[b], bias_indptr[b+1]) are
+ *                 request b's, in increasing order of their tokens (a token may
+ *                 come again: the values are added in turn); bias_total entries in all
+ *   allow         [num_allow][allow_words]: bit v % 32 of word v / 32 lets token v
+ *                 through; allow_words >= vocab_size / 32, rounded up
+ *   allow_index   [num_tokens]: the row of allow for each row of logits, or -1
+ *                 for none
+ */
+typedef struct csgmv_logit_rules {
+    const csgmv_token_counts *counts; /* host pointer; NULL: only a row's own branch counts */
+    const float *repetition, *frequency, *presence, *temperature;
+    const int32_t *bias_indptr, *bias_tokens;
+    const float *bias_values;
+    const int32_t *allow, *allow_index;
+    int64_t bias_total;
+    int32_t num_allow, allow_words;
+    int32_t *status; /* [1] CSGMV_KV_STATUS_* bits */
+} csgmv_logit_rules;
+
+/*
+ * Logits of drafted tokens to what csgmv_verify_drafts takes.  Request b owns
+ * rows [tree_indptr[b], tree_indptr[b+1]) and sequence seq_slots[b] (b when
+ * NULL) of the counts.  With c_v the number of times that the sequence gave v
+ * (counts), plus those that the row's own branch has it (rows j of the request
+ * whose bit is set in the row's mask: draft_tokens), for every token v of row t
+ *     z = logits[t][v]
+ *     z = z > 0 ? z / repetition : z * repetition   if c_v > 0 or v is in the prompt
+ *     z = z - frequency * c_v - presence * [c_v > 0]
+ *     z = z + biases of v
+ *     z = -infinity                                 if v is not allowed
+ * and, with softmax, out[t] = exp((z - max z) / temperature) / sum of these; where
+ * the temperature is 0, 1 at the lowest v with the largest z and 0 elsewhere.
+ * Each step of z is rounded to f32.  A row with nothing but -infinity gives zeros
+ * (verification draws nothing from it); one with a NaN, or whose largest z is
+ * infinite (but at temperature 0), NaN everywhere.  What is not allowed has no
+ * influence, whatever it holds.
+ *   logits      dtype (CSGMV_DTYPE_BF16, _F16 or _F32); rows of vocab_size, logits_stride
+ *               elements apart
+ *   out         f32, rows out_stride elements apart; may be logits when those are f32
+ *               (same address and stride), else it overlaps no input
+ *   mask        [num_tokens][mask_words] as csgmv_build_draft_tree writes it; NULL,
+ *               like draft_tokens NULL: no branch
+ * A request with a bad sequence, length, factor or list of biases, and a row
+ * with a bad allow_index, is left out: its rows of out stay as they are, and so do
+ * those of no request.  A drafted token or a bias outside the vocabulary counts
+ * for nothing (CSGMV_KV_STATUS_BAD_TOKEN).
+ * 1 <= vocab_size <= 2^18, mask_words <= 8, num_tokens < 2^24.
+ */
+CSGMV_API int csgmv_process_logits(const void *logits, int dtype, int64_t logits_stride, const int32_t *tree_indptr,
+                                   const int32_t *seq_slots, int bs, int64_t num_tokens, int vocab_size,
+                                   const csgmv_logit_rules *rules, const int32_t *draft_tokens, const int32_t *mask,
+                                   int mask_words, int softmax, float *out, int64_t out_stride, csgmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

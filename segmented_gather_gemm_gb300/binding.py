@@ -38,7 +38,8 @@ EXPORTED = ["csgmv_last_error", "csgmv_version", "csgmv_chunk_size", "csgmv_batc
             "csgmv_kv_scratch_ints", "csgmv_kv_commit", "csgmv_kv_fork", "csgmv_kv_free", "csgmv_kv_compact",
             "csgmv_kv_copy_pages", "csgmv_tree_attention", "csgmv_tree_attention_workspace_bytes",
             "csgmv_build_draft_tree", "csgmv_verify_drafts", "csgmv_add_norm", "csgmv_rope_turns",
-            "csgmv_rotary", "csgmv_kv_extend", "csgmv_kv_append"]
+            "csgmv_rotary", "csgmv_kv_extend", "csgmv_kv_append", "csgmv_count_tokens", "csgmv_count_reset",
+            "csgmv_count_fork", "csgmv_process_logits"]
 
 # csgmv_qkv_path results (CSGMV_PATH_*)
 PATHS = {0: "fused", 1: "decode", 2: "small_split", 3: "stream"}
@@ -76,6 +77,18 @@ class _NormC(ctypes.Structure):
 class _RopeC(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("scale", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class _TokenCountsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("counts", "seen", "num_seen", "status")] + [
+        ("max_seqs", ctypes.c_int32), ("vocab_size", ctypes.c_int32)]
+
+
+class _LogitRulesC(ctypes.Structure):
+    _fields_ = [("counts", ctypes.POINTER(_TokenCountsC))] + [(n, ctypes.c_void_p) for n in (
+        "repetition", "frequency", "presence", "temperature", "bias_indptr", "bias_tokens", "bias_values", "allow",
+        "allow_index")] + [("bias_total", ctypes.c_int64), ("num_allow", ctypes.c_int32), ("allow_words", ctypes.c_int32),
+                           ("status", ctypes.c_void_p)]
 
 
 _lib = None
@@ -137,6 +150,11 @@ def lib():
         "csgmv_kv_extend": (i32, [kvp, vp, vp, vp, i32, i64, vp, vp, vp, vp]),
         "csgmv_kv_append": (i32, [kvp, i32, ctypes.POINTER(_RopeC), vp, vp, i64, vp, i64, i64, i32, vp, i64, i64, vp, i64, i64,
                                   vp, i64, i64, vp, i64, i64, vp]),
+        "csgmv_count_tokens": (i32, [ctypes.POINTER(_TokenCountsC), vp, i64, vp, vp, i32, vp, vp, i32, i32, vp]),
+        "csgmv_count_reset": (i32, [ctypes.POINTER(_TokenCountsC), vp, i32, vp]),
+        "csgmv_count_fork": (i32, [ctypes.POINTER(_TokenCountsC), vp, vp, i32, vp]),
+        "csgmv_process_logits": (i32, [vp, i32, i64, vp, vp, i32, i64, i32, ctypes.POINTER(_LogitRulesC), vp, vp, i32, i32, vp,
+                                       i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -1049,3 +1067,162 @@ def csgmv_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor
         _raw_stream(stream, device))
     if rc:
         _check(rc)
+
+
+class TokenCounts:
+    """How often each of max_seqs sequences holds each token, empty at first.
+
+      counts    int32 (max_seqs, vocab_size): times given, plus 2^30 if the prompt
+                has it
+      seen      int32 (max_seqs, vocab_size): its first num_seen[s] entries are the
+                tokens that sequence s holds, in no certain order
+      num_seen  int32 (max_seqs,)"""
+
+    def __init__(self, max_seqs: int, vocab_size: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.counts = torch.zeros((max_seqs, vocab_size), **i32)
+        self.seen = torch.zeros((max_seqs, vocab_size), **i32)
+        self.num_seen = torch.zeros(max_seqs, **i32)
+        self.status = torch.zeros(1, **i32)
+        self.max_seqs, self.vocab_size, self.device = int(max_seqs), int(vocab_size), self.status.get_device()
+        self.c = _TokenCountsC(self.counts.data_ptr(), self.seen.data_ptr(), self.num_seen.data_ptr(), self.status.data_ptr(),
+                               max_seqs, vocab_size)
+        self._ref = ctypes.byref(self.c)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
+
+
+def csgmv_count_tokens(counts: TokenCounts, tokens: torch.Tensor, tree_indptr: torch.Tensor,
+                       accept_index: torch.Tensor | None = None, accept_len: torch.Tensor | None = None,
+                       seq_slots: torch.Tensor | None = None, prompt: bool = False, stream=None) -> None:
+    """Counts the tokens of request b's rows (its first accept_len[b], or its
+    rows accept_index[b, j]) for its sequence; prompt: as its prompt."""
+    device, bs = counts.device, tree_indptr.shape[0] - 1 if tree_indptr.dim() else -1
+    n, width = tokens.numel(), 0
+    _need_i32(device, "tokens", tokens, n)
+    _need_i32(device, "tree_indptr", tree_indptr, bs + 1)
+    if accept_index is not None:
+        width = accept_index.shape[-1]
+        _need_i32(device, "accept_index", accept_index, bs, width)
+    if accept_len is not None:
+        _need_i32(device, "accept_len", accept_len, bs)
+    if seq_slots is not None:
+        _need_i32(device, "seq_slots", seq_slots, bs)
+    rc = lib().csgmv_count_tokens(counts._ref, tokens.data_ptr(), n, tree_indptr.data_ptr(), _at(accept_index), width,
+                                  _at(accept_len), _at(seq_slots), bs, prompt, _raw_stream(stream, device))
+    if rc:
+        _check(rc)
+
+
+def csgmv_count_reset(counts: TokenCounts, seqs: torch.Tensor, stream=None) -> None:
+    """Empties sequences."""
+    n = seqs.numel()
+    _need_i32(counts.device, "seqs", seqs, n)
+    _check(lib().csgmv_count_reset(counts._ref, seqs.data_ptr(), n, _raw_stream(stream, counts.device)))
+
+
+def csgmv_count_fork(counts: TokenCounts, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
+    """Sequence children[i] becomes a copy of sequence parents[i]."""
+    n = parents.numel()
+    _need_i32(counts.device, "parents", parents, n)
+    _need_i32(counts.device, "children", children, n)
+    _check(lib().csgmv_count_fork(counts._ref, parents.data_ptr(), children.data_ptr(), n, _raw_stream(stream, counts.device)))
+
+
+class LogitRules:
+    """What csgmv_process_logits does to the rows of a batch of requests, over
+    caller-owned tensors whose contents may change from call to call; each part
+    may be None.
+
+      counts       TokenCounts that the penalties go by (None: a row's own branch)
+      repetition, frequency, presence, temperature   f32 (bs,)
+      bias         (indptr int32 (bs + 1,), tokens int32 (total,), values f32
+                   (total,)): entries of request b in increasing order of tokens
+      allow        int32 (masks, words): bit v % 32 of word v / 32 lets token v through
+      allow_index  int32 (rows,): each row's mask, or -1"""
+
+    def __init__(self, counts: TokenCounts | None = None, repetition: torch.Tensor | None = None,
+                 frequency: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                 temperature: torch.Tensor | None = None, bias: tuple | None = None, allow: torch.Tensor | None = None,
+                 allow_index: torch.Tensor | None = None, device="cuda"):
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = at = self.status.get_device()
+        _need(self.status.is_cuda, "the rules' device must be a CUDA device")
+        _need(counts is None or counts.device == at, f"the counts are on another device than cuda:{at}")
+        self.counts, self.bias, self.allow, self.allow_index = counts, bias, allow, allow_index
+        self.repetition, self.frequency, self.presence, self.temperature = repetition, frequency, presence, temperature
+        self.bs = None
+        c = _LogitRulesC()
+        if counts is not None:
+            c.counts = ctypes.pointer(counts.c)
+        for name in ("repetition", "frequency", "presence", "temperature"):
+            t = getattr(self, name)
+            if t is None:
+                continue
+            self.bs = t.shape[0] if self.bs is None and t.dim() else self.bs
+            _need_f32(at, name, t, self.bs)
+            _need(t.is_contiguous(), f"{name} must be contiguous")
+            setattr(c, name, t.data_ptr())
+        if bias is not None:
+            indptr, tokens, values = bias
+            total = tokens.numel()
+            self.bs = indptr.shape[0] - 1 if self.bs is None and indptr.dim() else self.bs
+            _need_i32(at, "bias indptr", indptr, self.bs + 1)
+            _need_i32(at, "bias tokens", tokens, total)
+            _need_f32(at, "bias values", values, total)
+            _need(values.is_contiguous(), "bias values must be contiguous")
+            c.bias_indptr, c.bias_tokens, c.bias_values, c.bias_total = indptr.data_ptr(), tokens.data_ptr(), values.data_ptr(), total
+        self.rows = None
+        _need((allow is None) == (allow_index is None), "allow and allow_index go together")
+        if allow is not None:
+            _need_i32(at, "allow", allow, None, None)
+            _need_i32(at, "allow_index", allow_index, None)
+            self.rows = allow_index.shape[0]
+            c.allow, c.allow_index = allow.data_ptr(), allow_index.data_ptr()
+            c.num_allow, c.allow_words = allow.shape
+        c.status = self.status.data_ptr()
+        self.c = c
+        self._ref = ctypes.byref(c)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
+
+
+def csgmv_process_logits(logits: torch.Tensor, tree_indptr: torch.Tensor, rules: LogitRules, out: torch.Tensor | None = None,
+                         draft_tokens: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                         seq_slots: torch.Tensor | None = None, softmax: bool = True, stream=None) -> torch.Tensor:
+    """out (rows, vocab; f32, allocated on the call's stream unless given; may be
+    logits): logits (rows, vocab; bf16, f16 or f32) of request b's rows after the
+    rules, as probabilities, or as they are without softmax.  draft_tokens (int32,
+    (rows,)) and mask (int32, (rows, words), of csgmv_build_draft_tree): the tokens
+    of a row's own branch count as given."""
+    device, dtype = rules.device, logits.dtype
+    if len(logits.shape) != 2 or dtype not in _DTYPES or logits.get_device() != device or logits.shape[0] and logits.stride(1) != 1:
+        raise CsgmvError(-1, f"logits must be (rows, vocab) of bf16, f16 or f32 on cuda:{device}, the rows dense")
+    n, vocab = logits.shape
+    bs = tree_indptr.shape[0] - 1 if tree_indptr.dim() else -1
+    _need_i32(device, "tree_indptr", tree_indptr, bs + 1)
+    if rules.bs is not None and rules.bs != bs or rules.rows is not None and rules.rows != n:
+        raise CsgmvError(-1, f"rules for {rules.bs} requests and {rules.rows} rows, a batch of {bs} and {n}")
+    if seq_slots is not None:
+        _need_i32(device, "seq_slots", seq_slots, bs)
+    words = 0
+    if (mask is None) != (draft_tokens is None):
+        raise CsgmvError(-1, "draft_tokens and mask go together")
+    if mask is not None:
+        words = mask.shape[-1]
+        _need_i32(device, "mask", mask, n, words)
+        _need_i32(device, "draft_tokens", draft_tokens, n)
+    if out is None:
+        out = _empty(stream, (n, vocab), dtype=torch.float32, device=logits.device)
+    else:
+        _need_f32(device, "out", out, n, vocab)
+        if n and out.stride(1) != 1:
+            raise CsgmvError(-1, "out must have dense rows")
+    rc = lib().csgmv_process_logits(logits.data_ptr(), _DTYPES[dtype], logits.stride(0) if n > 1 else vocab, tree_indptr.data_ptr(),
+                                    _at(seq_slots), bs, n, vocab, rules._ref, _at(draft_tokens), _at(mask), words, softmax,
+                                    out.data_ptr(), out.stride(0) if n > 1 else vocab, _raw_stream(stream, device))
+    if rc:
+        _check(rc)
+    return out

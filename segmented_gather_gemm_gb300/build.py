@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libcsgmv.so")
 SOURCES = ["api.cu", "builder.cu", "embedding.cu", "lora_launch.cu", "lora_fused.cu", "lora_shrink.cu", "lora_expand.cu",
            "lora_small.cu", "lora_stream.cu", "lora_sshrink.cu", "lora_decode.cu", "lora_wide.cu",
            "qkv_static.cu", "serving_api.cu", "kv_cache.cu", "draft_tree.cu", "tree_attention.cu",
-           "step_api.cu", "norm.cu", "rotary.cu"]
+           "step_api.cu", "norm.cu", "rotary.cu", "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -52,4 +52,31 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream);
 
+struct LogitParams {
+    const void *logits;
+    float *out;
+    int64_t logits_s, out_s, num_tokens, bias_total;
+    const int32_t *indptr, *slots;
+    const int32_t *counts, *seen, *num_seen;  // or NULL
+    const float *repetition, *frequency, *presence, *temperature;
+    const int32_t *bias_indptr, *bias_tokens;
+    const float *bias_values;
+    const int32_t *allow, *allow_index;
+    const int32_t *drafts, *mask;  // both or neither
+    int32_t *status;
+    int bs, vocab, max_seqs, num_allow, allow_words, mask_words, softmax, dtype;
+    int chunk;  // of a row, to a CTA
+};
+cudaError_t launch_process_logits(const LogitParams &p, cudaStream_t stream);
+
+struct CountParams {
+    int32_t *counts, *seen, *num_seen, *status;
+    int max_seqs, vocab, prompt, accept_width;
+    int64_t num_tokens;
+    const int32_t *tokens, *indptr, *accept_index, *accept_len, *slots;
+};
+cudaError_t launch_count_tokens(const CountParams &p, int bs, cudaStream_t stream);
+cudaError_t launch_count_reset(const CountParams &p, int n, cudaStream_t stream);
+cudaError_t launch_count_fork(const CountParams &p, const int32_t *parents, const int32_t *children, int n, cudaStream_t stream);
+
 }  // namespace csgmv

@@ -79,6 +79,37 @@ size_t kv_pool_bytes(const csgmv_kv_cache *kv) {
                 (size_t)(kv->num_kv_heads - 1) * kv->head_stride + (size_t)(kv->page_size - 1) * kv->token_stride + kv->head_dim);
 }
 
+int check_counts(const csgmv_token_counts *c) {
+    if (!c) return fail(CSGMV_ERR_INVALID_ARG, "counts is NULL");
+    if (c->max_seqs <= 0 || c->vocab_size <= 0) return fail(CSGMV_ERR_INVALID_ARG, "sizes of the counts must be positive");
+    if (c->vocab_size > (1 << 18) || c->max_seqs > (1 << 20))
+        return fail(CSGMV_ERR_UNSUPPORTED, "counts of at most 2^18 tokens and 2^20 sequences");
+    const size_t table = 4 * (size_t)c->max_seqs * c->vocab_size, seqs = 4 * (size_t)c->max_seqs;
+    const struct { const void *at; size_t bytes; } all[] = {{c->counts, table}, {c->seen, table}, {c->num_seen, seqs}, {c->status, 4}};
+    for (int i = 0; i < 4; ++i) {
+        if (!all[i].at || !aligned4(all[i].at)) return fail(CSGMV_ERR_INVALID_ARG, "a buffer of the counts is NULL or not 4-byte aligned");
+        for (int j = 0; j < i; ++j)
+            if (overlaps(all[i].at, all[i].bytes, all[j].at, all[j].bytes))
+                return fail(CSGMV_ERR_INVALID_ARG, "buffers of the counts overlap");
+    }
+    return CSGMV_OK;
+}
+bool overlaps_counts(const csgmv_token_counts *c, const void *at, size_t bytes) {
+    const size_t table = 4 * (size_t)c->max_seqs * c->vocab_size;
+    return overlaps(at, bytes, c->counts, table) || overlaps(at, bytes, c->seen, table) ||
+           overlaps(at, bytes, c->num_seen, 4 * (size_t)c->max_seqs) || overlaps(at, bytes, c->status, 4);
+}
+csgmv::CountParams count_params(const csgmv_token_counts *c) {
+    csgmv::CountParams p = {};
+    p.counts = c->counts;
+    p.seen = c->seen;
+    p.num_seen = c->num_seen;
+    p.status = c->status;
+    p.max_seqs = c->max_seqs;
+    p.vocab = c->vocab_size;
+    return p;
+}
+
 // Queries or keys of a call, and their outputs: 0 or an error.
 int check_heads(const char *name, const csgmv::Heads &h, int64_t n, int d, int bytes, bool need_out) {
     if (h.n < 0 || h.n > 4096) return fail(CSGMV_ERR_UNSUPPORTED, "%d heads of %s outside 0..4096", h.n, name);
@@ -318,6 +349,157 @@ int csgmv_kv_append(const csgmv_kv_cache *kv, int layer, const csgmv_rope *rope,
     p.page_shift = __builtin_ctz((unsigned)kv->page_size);
     p.status = kv->status;
     return launched(csgmv::launch_rotary(p, st(stream)), "csgmv_kv_append");
+}
+
+int csgmv_count_tokens(const csgmv_token_counts *counts, const int32_t *tokens, int64_t num_tokens,
+                       const int32_t *tree_indptr, const int32_t *accept_index, int accept_width,
+                       const int32_t *accept_len, const int32_t *seq_slots, int bs, int prompt, csgmv_stream_t stream) {
+    int rc = check_counts(counts);
+    if (rc) return rc;
+    if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
+    if (num_tokens > INT32_MAX) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds int32");
+    if (prompt != 0 && prompt != 1) return fail(CSGMV_ERR_INVALID_ARG, "prompt must be 0 or 1");
+    if (bs == 0 || num_tokens == 0) return CSGMV_OK;
+    if (!tokens || !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "tokens / tree_indptr is NULL");
+    if (accept_index && (accept_width <= 0 || !accept_len))
+        return fail(CSGMV_ERR_INVALID_ARG, "accept_index needs a positive accept_width and accept_len");
+    const size_t b4 = 4 * (size_t)bs;
+    const struct { const void *at; size_t bytes; } lists[] = {{tokens, 4 * (size_t)num_tokens},
+                                                              {tree_indptr, b4 + 4},
+                                                              {accept_index, b4 * (accept_index ? accept_width : 0)},
+                                                              {accept_len, b4},
+                                                              {seq_slots, b4}};
+    for (const auto &l : lists)
+        if (!aligned4(l.at) || overlaps_counts(counts, l.at, l.bytes))
+            return fail(CSGMV_ERR_INVALID_ARG, "a list of the call is not 4-byte aligned or overlaps the counts");
+    csgmv::CountParams p = count_params(counts);
+    p.prompt = prompt;
+    p.accept_width = accept_width;
+    p.num_tokens = num_tokens;
+    p.tokens = tokens;
+    p.indptr = tree_indptr;
+    p.accept_index = accept_index;
+    p.accept_len = accept_len;
+    p.slots = seq_slots;
+    return launched(csgmv::launch_count_tokens(p, bs, st(stream)), "csgmv_count_tokens");
+}
+
+int csgmv_count_reset(const csgmv_token_counts *counts, const int32_t *seqs, int n, csgmv_stream_t stream) {
+    int rc = check_counts(counts);
+    if (rc) return rc;
+    if (n < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative n");
+    if (n == 0) return CSGMV_OK;
+    if (!seqs || !aligned4(seqs) || overlaps_counts(counts, seqs, 4 * (size_t)n))
+        return fail(CSGMV_ERR_INVALID_ARG, "seqs is NULL, not 4-byte aligned or overlaps the counts");
+    csgmv::CountParams p = count_params(counts);
+    p.slots = seqs;
+    return launched(csgmv::launch_count_reset(p, n, st(stream)), "csgmv_count_reset");
+}
+
+int csgmv_count_fork(const csgmv_token_counts *counts, const int32_t *parents, const int32_t *children, int n,
+                     csgmv_stream_t stream) {
+    int rc = check_counts(counts);
+    if (rc) return rc;
+    if (n < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative n");
+    if (n > counts->max_seqs) return fail(CSGMV_ERR_CAPACITY, "n %d exceeds max_seqs %d", n, counts->max_seqs);
+    if (n == 0) return CSGMV_OK;
+    for (const int32_t *l : {parents, children})
+        if (!l || !aligned4(l) || overlaps_counts(counts, l, 4 * (size_t)n))
+            return fail(CSGMV_ERR_INVALID_ARG, "parents / children is NULL, not 4-byte aligned or overlaps the counts");
+    return launched(csgmv::launch_count_fork(count_params(counts), parents, children, n, st(stream)), "csgmv_count_fork");
+}
+
+int csgmv_process_logits(const void *logits, int dtype, int64_t logits_stride, const int32_t *tree_indptr,
+                         const int32_t *seq_slots, int bs, int64_t num_tokens, int vocab_size,
+                         const csgmv_logit_rules *rules, const int32_t *draft_tokens, const int32_t *mask, int mask_words,
+                         int softmax, float *out, int64_t out_stride, csgmv_stream_t stream) {
+    if (!known_type(dtype)) return fail(CSGMV_ERR_INVALID_ARG, "dtype %d must be bf16, f16 or f32", dtype);
+    if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
+    if (num_tokens >= (1 << 24)) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds 2^24 - 1");
+    if (vocab_size < 1 || vocab_size > (1 << 18))
+        return fail(CSGMV_ERR_UNSUPPORTED, "vocab_size %d outside 1..2^18", vocab_size);
+    if (!rules || !rules->status || !aligned4(rules->status))
+        return fail(CSGMV_ERR_INVALID_ARG, "rules or its status is NULL or not 4-byte aligned");
+    const csgmv_logit_rules &r = *rules;
+    const csgmv_token_counts *counts = r.counts;
+    if (counts) {
+        int rc = check_counts(counts);
+        if (rc) return rc;
+        if (counts->vocab_size != vocab_size)
+            return fail(CSGMV_ERR_INVALID_ARG, "counts of %d tokens, logits of %d", counts->vocab_size, vocab_size);
+    }
+    if (r.bias_total < 0 || r.bias_total > INT32_MAX) return fail(CSGMV_ERR_INVALID_ARG, "bias_total outside [0, 2^31)");
+    if (r.bias_indptr && r.bias_total > 0 && (!r.bias_tokens || !r.bias_values))
+        return fail(CSGMV_ERR_INVALID_ARG, "bias_tokens / bias_values is NULL");
+    if (r.num_allow < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative num_allow");
+    if (r.allow_index && r.num_allow > 0 && (!r.allow || r.allow_words < (vocab_size + 31) / 32))
+        return fail(CSGMV_ERR_INVALID_ARG, "allow is NULL or allow_words %d below %d", r.allow_words, (vocab_size + 31) / 32);
+    if (softmax != 0 && softmax != 1) return fail(CSGMV_ERR_INVALID_ARG, "softmax must be 0 or 1");
+    const bool branch = draft_tokens && mask;
+    if (branch && (mask_words < 1 || mask_words > csgmv::kTreeMaxWords))
+        return fail(CSGMV_ERR_UNSUPPORTED, "mask_words %d outside 1..%d", mask_words, csgmv::kTreeMaxWords);
+    if (bs == 0 || num_tokens == 0) return CSGMV_OK;
+    if (!logits || !out || !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "NULL tensor");
+    const int e = csgmv::dtype_bytes(dtype);
+    if (!aligned_to(logits, e) || !aligned4(out)) return fail(CSGMV_ERR_INVALID_ARG, "logits or out is not aligned to its type");
+    if (!stride_ok(logits_stride) || !stride_ok(out_stride) || (num_tokens > 1 && out_stride < vocab_size))
+        return fail(CSGMV_ERR_INVALID_ARG, "a stride is negative or above 2^40, or rows of out overlap");
+    const Rows in = rows_of(logits, e, num_tokens, logits_stride, 1, 0, vocab_size);
+    const Rows to = rows_of(out, 4, num_tokens, out_stride, 1, 0, vocab_size);
+    if (!in_place_or_apart(to, in)) return fail(CSGMV_ERR_INVALID_ARG, "out overlaps logits");
+    const size_t b4 = 4 * (size_t)bs, n4 = 4 * (size_t)num_tokens;
+    const struct { const void *at; size_t bytes; } read[] = {
+        {tree_indptr, b4 + 4}, {seq_slots, b4}, {r.repetition, b4}, {r.frequency, b4}, {r.presence, b4}, {r.temperature, b4},
+        {r.bias_indptr, b4 + 4}, {r.bias_tokens, 4 * (size_t)r.bias_total}, {r.bias_values, 4 * (size_t)r.bias_total},
+        {r.allow, r.allow_index ? 4 * (size_t)r.num_allow * (size_t)std::max(r.allow_words, 0) : 0}, {r.allow_index, n4},
+        {draft_tokens, branch ? n4 : 0}, {mask, branch ? n4 * mask_words : 0}};
+    for (const auto &l : read)
+        if (!aligned4(l.at) || meet(to, plain(l.at, l.bytes)) || overlaps(l.at, l.bytes, r.status, 4))
+            return fail(CSGMV_ERR_INVALID_ARG, "a list of the call is not 4-byte aligned or overlaps out or the status");
+    if (meet(to, plain(r.status, 4)) || meet(in, plain(r.status, 4)) ||
+        (counts && (overlaps_counts(counts, r.status, 4) && r.status != counts->status)))
+        return fail(CSGMV_ERR_INVALID_ARG, "the status overlaps a tensor");
+    if (counts) {
+        const size_t table = 4 * (size_t)counts->max_seqs * vocab_size;
+        if (meet(to, plain(counts->counts, table)) || meet(to, plain(counts->seen, table)) ||
+            meet(to, plain(counts->num_seen, 4 * (size_t)counts->max_seqs)))
+            return fail(CSGMV_ERR_INVALID_ARG, "out overlaps the counts");
+    }
+    csgmv::LogitParams p = {};
+    p.logits = logits;
+    p.out = out;
+    p.logits_s = logits_stride;
+    p.out_s = out_stride;
+    p.num_tokens = num_tokens;
+    p.bias_total = r.bias_total;
+    p.indptr = tree_indptr;
+    p.slots = seq_slots;
+    if (counts) {
+        p.counts = counts->counts;
+        p.seen = counts->seen;
+        p.num_seen = counts->num_seen;
+        p.max_seqs = counts->max_seqs;
+    }
+    p.repetition = r.repetition;
+    p.frequency = r.frequency;
+    p.presence = r.presence;
+    p.temperature = r.temperature;
+    p.bias_indptr = r.bias_indptr;
+    p.bias_tokens = r.bias_tokens;
+    p.bias_values = r.bias_values;
+    p.allow = r.allow;
+    p.allow_index = r.allow_index;
+    p.num_allow = r.num_allow;
+    p.allow_words = r.allow_words;
+    p.drafts = branch ? draft_tokens : nullptr;
+    p.mask = branch ? mask : nullptr;
+    p.mask_words = branch ? mask_words : 0;
+    p.status = r.status;
+    p.bs = bs;
+    p.vocab = vocab_size;
+    p.softmax = softmax;
+    p.dtype = dtype;
+    return launched(csgmv::launch_process_logits(p, st(stream)), "csgmv_process_logits");
 }
 
 }  // extern "C"

@@ -115,3 +115,71 @@ class Cache:
             self.table[seq][math.ceil(old / self.ps) + i] = page
         self.lens[seq] = old + n
         return [self.table[seq][p // self.ps] * self.ps + p % self.ps for p in range(old, old + n)], copies
+
+
+class Counts:
+    """What a sequence's tokens are: times given, and which its prompt has."""
+
+    def __init__(self):
+        self.given, self.prompt = {}, set()
+
+    def add(self, tokens, prompt=False):
+        for v in tokens:
+            if prompt:
+                self.prompt.add(v)
+            else:
+                self.given[v] = self.given.get(v, 0) + 1
+
+    def word(self, v):
+        return self.given.get(v, 0) + (2 ** 30 if v in self.prompt else 0)
+
+    def row(self, vocab):
+        out = [0] * vocab
+        for v in set(self.given) | self.prompt:
+            out[v] = self.word(v)
+        return out
+
+
+def scores(logits, counts, branch, rho, alpha, beta, bias, allowed):
+    """(z of one row in float64, how far rounding each step to f32 can move it).
+    counts: Counts or None; branch: tokens; bias: [(token, value)]; allowed: bool
+    (vocab,) or None."""
+    z = logits.double().clone()
+    size = torch.zeros_like(z)
+    given, prompt = (dict(counts.given), counts.prompt) if counts else ({}, set())
+    for v in branch:
+        given[v] = given.get(v, 0) + 1
+    for v in set(given) | set(prompt):
+        x = float(z[v])
+        x = x / rho if x > 0 else x * rho
+        c = given.get(v, 0)
+        s = 2 * abs(x) + (2 * abs(alpha) * c + abs(beta) + abs(x - alpha * c - beta) if c else 0.0)
+        z[v], size[v] = x - (alpha * c + beta if c else 0.0), s
+    for v, b in bias:
+        z[v] += b
+        size[v] += abs(float(z[v])) + abs(b)
+    if allowed is not None:
+        z[~allowed] = float("-inf")
+    size[~torch.isfinite(z)] = 0.0
+    return z, size.nan_to_num(0.0, 0.0, 0.0) * 2.0 ** -24
+
+
+def distribution(z, off, temperature):
+    """(probabilities, tolerance) of one row.  A relative error of a probability:
+    of z and of the largest z over the temperature; of their difference and two
+    factors (2^-22 of it); of the exponential and the division (2^-20); of the
+    sum, weighted, of some 60 additions (2^-18)."""
+    none = float("-inf")
+    top = float(z.max())
+    if bool(torch.isnan(z).any()) or (top == float("inf") and temperature > 0):
+        return torch.full_like(z, float("nan")), 0.0
+    if top == none:
+        return torch.zeros_like(z), 0.0
+    if temperature == 0:
+        p = torch.zeros_like(z)
+        p[int((z == top).nonzero()[0])] = 1.0
+        return p, 0.0
+    arg = (z - top) / temperature
+    p = torch.softmax(z / temperature, -1)
+    rel = (off + off.max()) / temperature + torch.where(torch.isfinite(arg), arg.abs(), 0.0) * 2.0 ** -22 + 2.0 ** -20
+    return p, p * (rel + float((p * rel).sum()) + 2.0 ** -18) + 2.0 ** -140

@@ -192,3 +192,92 @@ def test_append_calls_that_are_refused(lib, kw, rc, msg):  # noqa: F811
 def test_append_of_nothing(lib):  # noqa: F811
     assert append(lib, None) == INVALID
     assert append(lib, far(), n=0, k=None, slots=None) == OK
+
+
+def counts(**kw):
+    from segmented_gather_gemm_gb300 import binding
+    c = binding._TokenCountsC(0x1000000, 0x2000000, 0x3000000, 0x3100000, 8, 1000)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def count(lib, c, tokens=0x5000000, n=50, indptr=0x5100000, idx=None, width=0, lens=None, seqs=None, bs=4, prompt=0):
+    return lib.csgmv_count_tokens(None if c is None else ctypes.byref(c), tokens, n, indptr, idx, width, lens, seqs, bs, prompt, None)
+
+
+BAD_COUNTS = [(dict(counts=None), INVALID, b"NULL"), (dict(status=0x3100002), INVALID, b"aligned"), (dict(max_seqs=0), INVALID, b"positive"),
+              (dict(vocab_size=-1), INVALID, b"positive"), (dict(vocab_size=(1 << 18) + 1), UNSUPPORTED, b"2^18"),
+              (dict(max_seqs=(1 << 20) + 1), UNSUPPORTED, b"2^20"), (dict(seen=0x1000010), INVALID, b"overlap"),
+              (dict(num_seen=0x1000000 + 31996), INVALID, b"overlap"), (dict(status=0x3000004), INVALID, b"overlap")]
+
+
+@pytest.mark.parametrize("kw,rc,msg", BAD_COUNTS)
+def test_counts_that_are_refused(lib, kw, rc, msg):  # noqa: F811
+    c = counts(**kw)
+    for call in (lambda: count(lib, c), lambda: lib.csgmv_count_reset(ctypes.byref(c), P, 1, None),
+                 lambda: lib.csgmv_count_fork(ctypes.byref(c), P, P + 64, 1, None), lambda: process(lib, counts=c)):
+        assert call() == rc and msg in lib.csgmv_last_error()
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(bs=-1), b"negative"), (dict(n=-1), b"negative"), (dict(prompt=2), b"prompt"), (dict(tokens=None), b"NULL"),
+    (dict(indptr=None), b"NULL"), (dict(idx=P, width=0, lens=P), b"accept_index"), (dict(idx=P, width=4), b"accept_index"),
+    (dict(tokens=0x5000002), b"aligned"), (dict(tokens=0x1000000), b"overlaps"), (dict(seqs=0x3000000), b"overlaps"),
+    (dict(lens=0x3100000), b"overlaps"), (dict(idx=0x2000000, width=4, lens=P), b"overlaps")])
+def test_count_calls_that_are_refused(lib, kw, msg):  # noqa: F811
+    assert count(lib, counts(), **kw) == INVALID and msg in lib.csgmv_last_error()
+
+
+def test_other_count_calls_that_are_refused(lib):  # noqa: F811
+    c = ctypes.byref(counts())
+    assert count(lib, None) == INVALID and count(lib, counts(), n=1 << 31) == UNSUPPORTED
+    assert lib.csgmv_count_reset(c, P, -1, None) == INVALID and lib.csgmv_count_reset(c, None, 1, None) == INVALID
+    assert lib.csgmv_count_reset(c, 0x1000000, 1, None) == INVALID and lib.csgmv_count_reset(None, P, 1, None) == INVALID
+    assert lib.csgmv_count_fork(c, P, P, -1, None) == INVALID and lib.csgmv_count_fork(c, P, P, 9, None) == CAPACITY
+    assert lib.csgmv_count_fork(c, P, None, 1, None) == INVALID and lib.csgmv_count_fork(c, 0x3000000, P, 1, None) == INVALID
+    # nothing to do
+    assert count(lib, counts(), bs=0, tokens=None) == OK and count(lib, counts(), n=0, tokens=None) == OK
+    assert lib.csgmv_count_reset(c, None, 0, None) == OK and lib.csgmv_count_fork(c, None, None, 0, None) == OK
+
+
+def process(lib, counts=None, rules=True, logits=0x40000000, dtype=0, ls=1000, indptr=0x5000000, seqs=None, bs=4, n=20, vocab=1000,
+            drafts=None, mask=None, words=1, softmax=1, out=0x50000000, os=1000, status=0x6000000, **kw):
+    from segmented_gather_gemm_gb300 import binding
+    r = binding._LogitRulesC()
+    if counts is not None:
+        r.counts = ctypes.pointer(counts)
+    r.status = status
+    for k, v in kw.items():
+        setattr(r, k, v)
+    return lib.csgmv_process_logits(logits, dtype, ls, indptr, seqs, bs, n, vocab, ctypes.byref(r) if rules else None, drafts, mask,
+                                    words, softmax, out, os, None)
+
+
+@pytest.mark.parametrize("kw,rc,msg", [
+    (dict(dtype=3), INVALID, b"dtype"), (dict(bs=-1), INVALID, b"negative"), (dict(n=-1), INVALID, b"negative"),
+    (dict(n=1 << 24), UNSUPPORTED, b"2^24"), (dict(vocab=0), UNSUPPORTED, b"vocab"), (dict(vocab=(1 << 18) + 1), UNSUPPORTED, b"vocab"),
+    (dict(rules=False), INVALID, b"rules"), (dict(status=None), INVALID, b"status"), (dict(status=0x6000002), INVALID, b"status"),
+    (dict(bias_total=-1), INVALID, b"bias_total"), (dict(bias_indptr=P, bias_total=4), INVALID, b"bias_tokens"),
+    (dict(num_allow=-1), INVALID, b"num_allow"), (dict(allow_index=P, num_allow=1), INVALID, b"allow is NULL"),
+    (dict(allow_index=P, allow=P + 4096, num_allow=1, allow_words=31), INVALID, b"allow_words"), (dict(softmax=2), INVALID, b"softmax"),
+    (dict(drafts=P, mask=P + 4096, words=9), UNSUPPORTED, b"mask_words"), (dict(drafts=P, mask=P + 4096, words=0), UNSUPPORTED, b"mask_words"),
+    (dict(logits=None), INVALID, b"NULL"), (dict(out=None), INVALID, b"NULL"), (dict(indptr=None), INVALID, b"NULL"),
+    (dict(logits=0x40000001), INVALID, b"aligned"), (dict(out=0x50000002), INVALID, b"aligned"), (dict(ls=-1), INVALID, b"stride"),
+    (dict(os=999), INVALID, b"overlap"), (dict(os=1 << 41), INVALID, b"stride"),
+    # out over what is read
+    (dict(out=0x40000000), INVALID, b"overlaps logits"), (dict(out=0x40000000, dtype=1, os=1004), INVALID, b"overlaps logits"),
+    (dict(indptr=0x50000000), INVALID, b"overlaps"), (dict(temperature=0x50000100), INVALID, b"overlaps"),
+    (dict(seqs=0x50000100), INVALID, b"overlaps"), (dict(repetition=0x50000002), INVALID, b"aligned"),
+    (dict(drafts=0x50000100, mask=P), INVALID, b"overlaps"), (dict(drafts=P, mask=0x50000100), INVALID, b"overlaps"),
+    (dict(allow_index=P, allow=0x50000000, num_allow=1, allow_words=32), INVALID, b"overlaps"), (dict(status=0x50000000), INVALID, b"status"),
+    (dict(status=0x40000000), INVALID, b"status"), (dict(indptr=0x6000000), INVALID, b"status")])
+def test_process_calls_that_are_refused(lib, kw, rc, msg):  # noqa: F811
+    assert process(lib, **kw) == rc and msg in lib.csgmv_last_error()
+
+
+def test_process_with_counts_that_do_not_fit(lib):  # noqa: F811
+    assert process(lib, counts=counts(vocab_size=999)) == INVALID and b"999" in lib.csgmv_last_error()
+    assert process(lib, counts=counts(), out=0x1000000) == INVALID and b"counts" in lib.csgmv_last_error()
+    assert process(lib, counts=counts(), status=0x1000000) == INVALID and b"status" in lib.csgmv_last_error()
+    assert process(lib, bs=0, logits=None) == OK and process(lib, n=0, logits=None) == OK
