@@ -5,10 +5,9 @@
 // A pair (u, v) becomes scale (u cos a - v sin a, u sin a + v cos a) with a = p f.
 // f is held in 2^-64 turns: p f in 64-bit whole numbers wraps at whole turns by
 // itself, so no angle loses bits however far its position is, and no table of
-// cosines is read.  A thread owns W neighbouring pairs of a head (two vectors of
-// W elements, or one of 2 W where pairs lie side by side) of one token: it takes
-// their sines and cosines once and turns that part of several heads, four at a
-// time so that their loads are in flight together.
+// cosines is read.  A CTA takes the sines and cosines of its tokens once, into
+// shared memory.  A thread owns W neighbouring pairs (two vectors of W elements, or
+// one of 2 W where pairs lie side by side) of one token in some of its heads.
 #include "elements.cuh"
 #include "serving.cuh"
 #include "step.h"
@@ -26,93 +25,89 @@ struct Shape {
 };
 
 template <typename T, int W, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rotary(RotaryParams p, Shape s) {
+__global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams p, Shape s) {
+    extern __shared__ float4 angles4[];
+    float *cosines = reinterpret_cast<float *>(angles4), *sines = cosines + s.tokens * s.pairs * W;
     griddep_launch_dependents();
     griddep_wait();
     const int local = threadIdx.x / s.slots, slot0 = threadIdx.x - local * s.slots;
-    const int64_t t = (int64_t)blockIdx.x * s.tokens + local;
-    if (local >= s.tokens || t >= p.num_tokens) return;
+    const int64_t t0 = (int64_t)blockIdx.x * s.tokens, t = t0 + local;
+    bool mine = local < s.tokens && t < p.num_tokens;
     int64_t to = 0;  // of the token, in a head of the pages
-    if (APPEND) {
+    if (APPEND && mine) {
         const int64_t at = p.slots[t];
         if (at < 0 || at >= p.num_slots) {
             if (at != -1 && slot0 == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
-            return;
+            mine = false;
         }
         to = (at >> p.page_shift) * p.page_stride + (at & ((1 << p.page_shift) - 1)) * p.token_stride;
     }
-    const T *q = static_cast<const T *>(p.q.in) + t * p.q.ts, *k = static_cast<const T *>(p.k.in) + t * p.k.ts;
-    T *qo = static_cast<T *>(p.q.out) + t * p.q.o_ts;
-    T *ko = p.k.out ? static_cast<T *>(p.k.out) + t * p.k.o_ts : nullptr;
-    T *kc = APPEND ? static_cast<T *>(p.k_pages) + to : nullptr;
-    const int heads = p.q.n + p.k.n;
+    for (int i = threadIdx.x; i < s.tokens * s.pairs * W; i += kThreads) {
+        const int token = i / (s.pairs * W);
+        if (t0 + token >= p.num_tokens) break;
+        const uint64_t pos = (uint64_t)(int64_t)p.positions[t0 + token];
+        const int64_t turn = (int64_t)(pos * p.turns[i - token * (s.pairs * W)]);  // 2^-64 turns, modulo a whole one
+        float sn, cs;
+        sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
+        cosines[i] = cs * p.scale;
+        sines[i] = sn * p.scale * p.sign;
+    }
+    __syncthreads();
+    if (!mine) return;
     for (int slot = slot0; slot < s.units * s.lanes; slot += s.slots) {
-        const int lane = slot / s.units, unit = slot - lane * s.units;
+        // the thread's unit: its first element and, of pairs apart, how far their second ones are
+        const int lane = slot / s.units, unit = slot - lane * s.units, apart = IL ? W : p.rot / 2;
         const bool turned = unit < s.pairs;
-        // the unit's first element and, of pairs apart, how far their second ones are
-        const int e = turned ? unit * (IL ? 2 * W : W) : p.rot + (unit - s.pairs) * W, apart = IL ? W : p.rot / 2;
+        const int e = turned ? unit * (IL ? 2 * W : W) : p.rot + (unit - s.pairs) * W;
         float c[W], z[W];
         if (turned) {
-            const uint64_t pos = (uint64_t)(int64_t)p.positions[t];
+            const int first = (local * s.pairs + unit) * W;
+            if constexpr (W % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const int64_t turn = (int64_t)(pos * p.turns[unit * W + i]);  // 2^-64 turns, modulo a whole one
-                float sn, cs;
-                sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
-                c[i] = cs * p.scale;
-                z[i] = sn * p.scale * p.sign;
+                for (int i = 0; i < W; i += 4) {
+                    *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(cosines + first + i);
+                    *reinterpret_cast<float4 *>(z + i) = *reinterpret_cast<const float4 *>(sines + first + i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) c[i] = cosines[first + i], z[i] = sines[first + i];
             }
         }
-        constexpr int U = 4;
-        for (int h0 = lane; h0 < heads; h0 += U * s.lanes) {
-            Vec<T, W> a[U], b[U];
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int h = h0 + x * s.lanes;
-                if (h >= heads) continue;
-                const T *at = (h < p.q.n ? q + h * p.q.hs : k + (h - p.q.n) * p.k.hs) + e;
-                a[x] = ld_vec<T, W>(at);
-                if (turned) b[x] = ld_vec<T, W>(at + apart);
-            }
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int h = h0 + x * s.lanes;
-                if (h >= heads) continue;
-                if (turned) {
+        // the unit in heads lane, lane + lanes, ... of a tensor, to up to two places
+        auto heads = [&](const Heads &x, bool turn, T *page) {
+            const T *in = static_cast<const T *>(x.in) + t * x.ts + lane * x.hs + e;
+            T *out = x.out ? static_cast<T *>(x.out) + t * x.o_ts + lane * x.o_hs + e : nullptr;
+            if (APPEND && page) page += to + lane * p.head_stride + e;
+            for (int h = lane; h < x.n; h += s.lanes) {
+                Vec<T, W> a = ld_vec<T, W>(in), b;
+                if (turned) b = ld_vec<T, W>(in + apart);
+                in += s.lanes * x.hs;
+                if (turn && turned) {
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
                         // pair i: elements i of both, or neighbours in the two vectors laid end to end
-                        T &u = IL ? (2 * i < W ? a[x].e[(2 * i) % W] : b[x].e[(2 * i) % W]) : a[x].e[i];
-                        T &v = IL ? (2 * i + 1 < W ? a[x].e[(2 * i + 1) % W] : b[x].e[(2 * i + 1) % W]) : b[x].e[i];
+                        T &u = IL ? (2 * i < W ? a.e[(2 * i) % W] : b.e[(2 * i) % W]) : a.e[i];
+                        T &v = IL ? (2 * i + 1 < W ? a.e[(2 * i + 1) % W] : b.e[(2 * i + 1) % W]) : b.e[i];
                         const float uf = to_f32(u), vf = to_f32(v);
                         u = from_f32<T>(uf * c[i] - vf * z[i]);
                         v = from_f32<T>(uf * z[i] + vf * c[i]);
                     }
                 }
-                T *out[2] = {nullptr, nullptr};
-                if (h < p.q.n) {
-                    out[0] = qo + h * p.q.o_hs;
-                } else {
-                    if (ko) out[0] = ko + (h - p.q.n) * p.k.o_hs;
-                    if (APPEND) out[1] = kc + (h - p.q.n) * p.head_stride;
+                if (out) {
+                    st_vec<T, W>(out, a);
+                    if (turned) st_vec<T, W>(out + apart, b);
+                    out += s.lanes * x.o_hs;
                 }
-#pragma unroll
-                for (int o = 0; o < (APPEND ? 2 : 1); ++o) {
-                    if (!out[o]) continue;
-                    st_vec<T, W>(out[o] + e, a[x]);
-                    if (turned) st_vec<T, W>(out[o] + e + apart, b[x]);
+                if (APPEND && page) {
+                    st_vec<T, W>(page, a);
+                    if (turned) st_vec<T, W>(page + apart, b);
+                    page += s.lanes * p.head_stride;
                 }
             }
-        }
-    }
-    if (APPEND) {
-        const T *v = static_cast<const T *>(p.v.in) + t * p.v.ts;
-        T *vc = static_cast<T *>(p.v_pages) + to;
-        const int chunks = p.d / W, n = p.v.n * chunks;
-        for (int i = slot0; i < n; i += s.slots) {
-            const int h = i / chunks, e = (i - h * chunks) * W;
-            st_vec<T, W>(vc + h * p.head_stride + e, ld_vec<T, W>(v + h * p.v.hs + e));
-        }
+        };
+        heads(p.q, true, nullptr);
+        heads(p.k, true, APPEND ? static_cast<T *>(p.k_pages) : nullptr);
+        if (APPEND) heads(p.v, false, static_cast<T *>(p.v_pages));
     }
 }
 
@@ -142,28 +137,28 @@ cudaError_t go(const RotaryParams &p, cudaStream_t stream) {
     Shape s;
     s.pairs = p.rot / 2 / W;
     s.units = s.pairs + (p.d - p.rot) / W;
-    const int heads = std::max(1, p.q.n + p.k.n);
-    // Four heads a thread share its sines; few tokens spread over all lanes instead.
-    const int64_t wide = p.num_tokens * heads * s.units;
-    const int each = wide >= 152 * 1024 * 4 ? 4 : 1;
-    s.lanes = std::max(1, std::min((heads + each - 1) / each, kThreads / s.units));
+    const int heads = std::max(1, p.q.n + p.k.n + p.v.n);
+    // A warp a token where there are enough of them to fill the GPU (35507 tokens of 40
+    // heads of 128: 117 us; twice as many threads a token 123, half as many 128); with
+    // fewer, more threads share a token's heads (12 of them: 3.0 us, with a warp each 4).
+    const int64_t fill = 152 * 5 * kThreads / (p.num_tokens * s.units);
+    s.lanes = (int)std::max<int64_t>(1, std::min<int64_t>({std::max<int64_t>(fill, 32 / s.units), heads, kThreads / s.units}));
     s.slots = std::min(kThreads, s.units * s.lanes);
     s.tokens = kThreads / s.slots;
     const int64_t blocks = (p.num_tokens + s.tokens - 1) / s.tokens;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
-    return p.interleaved ? launch_kernel(rotary<T, W, true, APPEND>, grid, kThreads, 0, stream, 0, true, p, s)
-                         : launch_kernel(rotary<T, W, false, APPEND>, grid, kThreads, 0, stream, 0, true, p, s);
+    const size_t smem = 8 * (size_t)s.tokens * s.pairs * W;
+    return p.interleaved ? launch_kernel(rotary<T, W, true, APPEND>, grid, kThreads, smem, stream, 0, true, p, s)
+                         : launch_kernel(rotary<T, W, false, APPEND>, grid, kThreads, smem, stream, 0, true, p, s);
 }
 
 template <typename T, bool APPEND>
 cudaError_t pick(const RotaryParams &p, cudaStream_t stream) {
     constexpr int kWide = 16 / (int)sizeof(T);
-    switch (width_for(p, (int)sizeof(T))) {
-        case kWide: return go<T, kWide, APPEND>(p, stream);
-        case 2: return go<T, 2, APPEND>(p, stream);
-        default: return go<T, 1, APPEND>(p, stream);
-    }
+    const int w = width_for(p, (int)sizeof(T));
+    if (w == kWide) return go<T, kWide, APPEND>(p, stream);
+    return w == 2 ? go<T, 2, APPEND>(p, stream) : go<T, 1, APPEND>(p, stream);
 }
 
 }  // namespace
