@@ -2,17 +2,18 @@
 // masks, temperature, softmax; and the counts of tokens that penalties go by.
 // See include/csgmv.h (csgmv_process_logits, csgmv_count_*).
 //
-// A cluster of up to eight CTAs has a row, a stretch each, that it copies to
-// shared memory as it is, before it knows whose it is.  What is sparse is put
-// right while that arrives: the tokens that a sequence holds (they come as a list
-// beside the dense counts, so a row costs as many gathers as it has tokens, not a
-// pass over the vocabulary), the row's branch, biases; each such token has one
-// thread (a bit for each, the number of bits before it: a list in the order of
-// the vocabulary, whatever that of the counts' list, so results do not depend on
-// it).  f32 scores go back to their places; those of 16-bit logits are kept beside, and
-// their places become -infinity.  Two passes over the stretch follow, both in shared memory: the
-// maximum and the sum of exponentials together, then the probabilities.  The
-// CTAs of a row exchange one pair of numbers in between.
+// A cluster of up to eight CTAs has a row, every eighth block of it a CTA (low
+// numbers are frequent tokens: they are everyone's), that it copies to shared
+// memory as it is, before it knows whose it is.  What is sparse is found
+// while that arrives: the tokens that a sequence holds (they come as a list beside
+// the dense counts, so a row costs as many gathers as it has tokens, not a pass
+// over the vocabulary), the row's branch, biases.  Whoever finds a token first (a bit
+// for each) takes its logit out of there, into a list, and leaves -infinity.  Two
+// passes follow, both in shared memory: the maximum and the sum
+// of exponentials together, then the probabilities; the list's counts come
+// during the first.  The list is in no certain order, so its exponentials are summed in
+// whole steps of 2^-40 of the CTA's largest: results do not depend on timing.
+// The CTAs of a row exchange one pair of numbers between the passes.
 #include <algorithm>
 #include <atomic>
 
@@ -28,7 +29,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBranch = 32 * kTreeMaxWords;
 constexpr int kPrompt = 1 << 30;
 constexpr int kMaxVocab = 1 << 18, kMaxCtas = 8;
-constexpr int kKept = 1024;  // scores beside a stretch of 16-bit logits; further ones wait in out
+constexpr int kBlock = 512;  // elements; blocks of a row go to its CTAs in turn
+constexpr int kKept = 1024;  // scores in a CTA's list; further ones wait in out
 constexpr float kLargest = 3.402823466e+38f;
 
 // A part of a row: its largest score, and the sum of 2^((z - top) heat), which
@@ -41,18 +43,18 @@ struct Smem {
     int branch[kMaxBranch];
     float kept[kKept];
     uint16_t place[kKept];
-    int n_branch;
-    int scan[33];
-    Part warp[kWarps];
-    Part ctas[kMaxCtas];
+    int n_branch, n_kept;
+    uint32_t drawn[32], biased[32];  // bits of the branch's and the biases' places modulo 1024
+    float most[kWarps];
+    unsigned long long steps;
+    int list_at, lost;
+    Part parts[kMaxCtas * (kWarps + 1)];  // of the row: each CTA's warps, and its list
 };
-// Shared memory of a stretch of up to `chunk` elements, which begins up to 15
-// bytes behind a 16-byte boundary: the elements; a bit for each of those whose score
-// is another; how many of these are set before each word.
-struct Stretch {
+// Shared memory of a CTA's blocks of a row: the elements, and a bit for each.
+struct Share {
     int elements, words;  // bytes, and words of bits
 };
-__host__ __device__ inline Stretch stretch_of(int chunk, int bytes) { return {(chunk * bytes + 16 + 15) & ~15, (chunk + 16 + 31) >> 5}; }
+__host__ __device__ inline Share share_of(int chunk, int bytes) { return {chunk * bytes, chunk >> 5}; }
 
 // 2^x to two units in the last place, what is below 2^-126 as 0.
 __device__ __forceinline__ float ex2(float x) {
@@ -60,7 +62,7 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// What a sum about `top` counts about `about` (equal infinities are no difference).
+// What a sum about `top` counts about another (equal infinities are no difference).
 __device__ __forceinline__ float shifted(float sum, float top, float about, float heat) {
     return top == about ? sum : sum * ex2((top - about) * heat);
 }
@@ -98,33 +100,37 @@ __device__ __forceinline__ void store(float *p, const float (&x)[W]) {
 }
 __device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ bool has(const uint32_t *bits, int i) { return (bits[i >> 5] >> (i & 31) & 1u) != 0; }
-__device__ __forceinline__ void mark(uint32_t *bits, int i) { atomicOr(bits + (i >> 5), 1u << (i & 31)); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(LogitParams p) {
     extern __shared__ uint4 dynamic[];
     __shared__ Smem sm;
     constexpr int W = 16 / (int)sizeof(T);  // elements of a vector
-    constexpr bool kBeside = sizeof(T) == 2;
-    const Stretch shape = stretch_of(p.chunk, sizeof(T));
+    const Share shape = share_of(p.chunk, sizeof(T));
     T *z = reinterpret_cast<T *>(dynamic);
     uint32_t *set = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(dynamic) + shape.elements);
-    uint16_t *before = reinterpret_cast<uint16_t *>(set + shape.words);
     griddep_launch_dependents();
     cluster_arrive();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int t = blockIdx.x / ctas;
-    // this CTA's stretch of the row: elements begin .. end of z, as far behind a vector as in memory
-    const int lo = min(p.vocab, rank * p.chunk), n = min(p.vocab, lo + p.chunk) - lo;
-    const T *row = static_cast<const T *>(p.logits) + t * p.logits_s + lo;
-    const int begin = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T)), end = begin + n;
+    // This CTA's blocks of the row.  Blocks are counted from the 16-byte boundary at or
+    // before it; z[i] is the logit of token(i), which is outside the vocabulary before
+    // the row's first element and behind its last one.
+    const T *row = static_cast<const T *>(p.logits) + t * p.logits_s;
+    const int begin = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T)), turns = 31 - __clz(ctas);
+    const int blocks = (begin + p.vocab + kBlock - 1) / kBlock, n = rank < blocks ? ((blocks - 1 - rank) >> turns) * kBlock + kBlock : 0;
+    auto token = [&](unsigned i) { return (int)((((i / kBlock) << turns) + rank) * kBlock + i % kBlock) - begin; };
+    auto inside = [&](int token) { return (unsigned)token < (unsigned)p.vocab; };
     const float none = __int_as_float(0xff800000);
-    for (int i = tid * W; i < end; i += kThreads * W) {
-        if (i >= begin && i + W <= end) cp_async16(z + i, row + (i - begin), 16);
+    const int v_first = token(tid * W), v_step = (kThreads * W) << turns;  // tokens of a thread's vectors
+    static_assert(kThreads * W % kBlock == 0, "a thread's vectors have one place in their blocks");
+    auto whole = [&](int v) { return (unsigned)v <= (unsigned)(p.vocab - W) && p.vocab >= W; };
+    for (int i = tid * W, v = v_first; i < n; i += kThreads * W, v += v_step) {
+        if (whole(v)) cp_async16(z + i, row + v, 16);
         else
-            for (int e = i; e < i + W; ++e) z[e] = e >= begin && e < end ? row[e - begin] : from_f32<T>(none);
+            for (int e = 0; e < W; ++e) z[i + e] = inside(v + e) ? row[v + e] : from_f32<T>(none);
     }
     // the row's request: the last one that begins at or before it, 32 tried at once
     int b = 0;
@@ -161,14 +167,19 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
         return;
     }
     const uint32_t *allow = gate >= 0 ? reinterpret_cast<const uint32_t *>(p.allow) + (int64_t)gate * p.allow_words : nullptr;
-    float *out = p.out + t * p.out_s + lo - begin;  // out[i] is the place of z[i]
+    float *out = p.out + t * p.out_s;
     // where a token is in z if it is this CTA's to put right, or -1
-    auto place = [&](int token) { return token >= lo && token < lo + n && (!allow || has(allow, token)) ? token - lo + begin : -1; };
+    auto place = [&](int token) {
+        const unsigned j = token + begin, block = j / kBlock;
+        return inside(token) && (int)(block & (ctas - 1)) == rank && (!allow || has(allow, token)) ? (int)((block >> turns) * kBlock + j % kBlock) : -1;
+    };
     const bool punish = rho != 1.0f || alpha != 0.0f || beta != 0.0f, branch = punish && p.mask;
-    const int32_t *counts = punish && p.counts ? p.counts + (int64_t)seq * p.vocab + lo - begin : nullptr;
+    const int32_t *counts = punish && p.counts ? p.counts + (int64_t)seq * p.vocab : nullptr;
     const int32_t *seen = counts ? p.seen + (int64_t)seq * p.vocab : nullptr;
     const int held = counts ? min(p.num_seen[seq], p.vocab) : 0;
     const bool sparse = held > 0 || branch || b1 > b0;
+    if (tid == 0) sm.n_kept = 0, sm.steps = 0, sm.list_at = INT32_MAX, sm.lost = 0;
+    if (warp == 0) sm.drawn[lane] = sm.biased[lane] = 0;
     // the first tokens that the sequence holds, where they are, and their counts on the way
     constexpr int S = 4;
     int held_at[S];
@@ -181,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
     load_held(0);
 #pragma unroll
     for (int u = 0; u < S; ++u)
-        if (held_at[u] >= 0) prefetch(counts + held_at[u]);
+        if (held_at[u] >= 0) prefetch(counts + token(held_at[u]));
+    if (allow && tid * kBlock < n) prefetch(allow + (max(token(tid * kBlock), 0) >> 5));
     if (sparse) {
         if (b0 + tid < b1) prefetch(p.bias_tokens + b0 + tid), prefetch(p.bias_values + b0 + tid);
         for (int i = tid; i < shape.words; i += kThreads) set[i] = 0;
@@ -190,16 +202,16 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
             for (int w = 0; w < p.mask_words; ++w) {
                 const uint32_t bits = (uint32_t)p.mask[(int64_t)t * p.mask_words + w];
                 const int j = 32 * w + lane;
-                int token = -1;
+                int v = -1;
                 if ((bits >> lane & 1u) && j < last - first) {
-                    token = p.drafts[first + j];
-                    if (token < 0 || token >= p.vocab) {
+                    v = p.drafts[first + j];
+                    if (!inside(v)) {
                         if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
-                        token = -1;
+                        v = -1;
                     }
                 }
-                const unsigned m = __ballot_sync(kFullMask, token >= 0);
-                if (token >= 0) sm.branch[k + __popc(m & ((1u << lane) - 1u))] = token;
+                const unsigned m = __ballot_sync(kFullMask, v >= 0);
+                if (v >= 0) sm.branch[k + __popc(m & ((1u << lane) - 1u))] = v;
                 k += __popc(m);
             }
             if (lane == 0) sm.n_branch = k;
@@ -209,128 +221,141 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
     __syncthreads();
     if (allow) {  // what is not allowed, out of the stretch
 #pragma unroll 4
-        for (int i = tid * W; i < end; i += kThreads * W) {
-            const int token = lo + i - begin, from = max(token, 0);  // of the first element, which may be before the stretch
+        for (int i = tid * W, v0 = v_first; i < n; i += kThreads * W, v0 += v_step) {
+            const int from = min(max(v0, 0), p.vocab - 1);  // (the vector may begin before the row)
             uint32_t bits = allow[from >> 5] >> (from & 31);
             if ((from & 31) + W > 32 && (from | 31) + 1 < p.vocab) bits |= allow[(from >> 5) + 1] << (32 - (from & 31));
-            bits <<= from - token;
+            bits <<= max(from - v0, 0);
             Vec<T, W> v = *reinterpret_cast<const Vec<T, W> *>(z + i);
 #pragma unroll
             for (int e = 0; e < W; ++e) v.e[e] = bits >> e & 1u ? v.e[e] : from_f32<T>(none);
             *reinterpret_cast<Vec<T, W> *>(z + i) = v;
         }
     }
-    int done = 0;  // scores that are not the row's own
+    int done = 0;  // tokens in the list, and behind it
     if (sparse) {
+        if (allow) __syncthreads();
+        auto take = [&](int at) {
+            const uint32_t bit = 1u << (at & 31);
+            if (atomicOr(set + (at >> 5), bit) & bit) return;
+            const int r = atomicAdd(&sm.n_kept, 1);
+            if (r < kKept) sm.kept[r] = to_f32(z[at]), sm.place[r] = (uint16_t)at;
+            else out[token(at)] = to_f32(z[at]);
+            z[at] = from_f32<T>(none);
+        };
         const int k = branch ? sm.n_branch : 0;
         for (int i = tid; i < k; i += kThreads)
-            if (const int at = place(sm.branch[i]); at >= 0) mark(set, at);
+            if (const int at = place(sm.branch[i]); at >= 0) {
+                atomicOr(&sm.drawn[at >> 5 & 31], 1u << (at & 31));
+                take(at);
+            }
         bool torn = false;
         for (int i = b0 + tid; i < b1; i += kThreads) {
-            const int token = p.bias_tokens[i];
-            torn |= i > b0 && token < p.bias_tokens[i - 1];
-            if (token < 0 || token >= p.vocab) {
+            const int v = p.bias_tokens[i];
+            torn |= i > b0 && v < p.bias_tokens[i - 1];
+            if (!inside(v)) {
                 if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
-            } else if (const int at = place(token); at >= 0) {
-                mark(set, at);
+            } else if (const int at = place(v); at >= 0) {
+                atomicOr(&sm.biased[at >> 5 & 31], 1u << (at & 31));
+                take(at);
             }
         }
         for (int i0 = 0; i0 < held; i0 += S * kThreads) {
             if (i0 > 0) load_held(i0);
 #pragma unroll
             for (int u = 0; u < S; ++u)
-                if (held_at[u] >= 0) mark(set, held_at[u]);
+                if (held_at[u] >= 0) take(held_at[u]);
         }
         if (__syncthreads_or(torn)) {  // biases out of order; every CTA of the cluster alike
             if (rank == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_VALUE);
             return;
         }
-        for (int w0 = 0; w0 < shape.words; w0 += kThreads) {
-            const int w = w0 + tid;
-            const uint32_t word = w < shape.words ? set[w] : 0;
-            int more, r = done + block_scan_ex(__popc(word), sm.scan, &more);
-            if (w < shape.words) before[w] = (uint16_t)r;
-            for (uint32_t bits = word; bits && r < kKept; bits &= bits - 1, ++r) sm.place[r] = (uint16_t)(32 * w + __ffs(bits) - 1);
-            done += more;
+        done = sm.n_kept;
+        if (done > kKept) {  // bits of those that the list has no room for are left
+            for (int r = tid; r < kKept; r += kThreads) atomicAnd(set + (sm.place[r] >> 5), ~(1u << (sm.place[r] & 31)));
+            __syncthreads();
         }
+    } else if (allow) {
         __syncthreads();
-        auto score = [&](int at, int r) {
-            const int token = lo + at - begin;
-            float x = to_f32(z[at]);
-            if (punish) {
-                const int word = counts ? counts[at] : 0;
-                int more = 0;
-                for (int j = 0; j < k; ++j) more += sm.branch[j] == token;
-                x = penalized(x, word, more, rho, alpha, beta);
-            }
-            if (b1 > b0) {
-                int i = b0;  // the first bias of the token
-                for (int len = b1 - b0; len > 0;) {
-                    const int half = len >> 1;
-                    if (p.bias_tokens[i + half] < token) i += half + 1, len -= half + 1;
-                    else len = half;
-                }
-                for (; i < b1 && p.bias_tokens[i] == token; ++i) x = __fadd_rn(x, p.bias_values[i]);
-            }
-            if constexpr (kBeside) {
-                if (r < kKept) sm.kept[r] = x;
-                else out[at] = x;
-                z[at] = from_f32<T>(none);
-            } else {
-                z[at] = x;
-            }
-        };
-        for (int r = tid; r < min(done, kKept); r += kThreads) score(sm.place[r], r);
-        if (done > kKept)
-            for (int w = tid; w < shape.words; w += kThreads) {
-                int r = before[w];
-                for (uint32_t bits = set[w]; bits; bits &= bits - 1, ++r)
-                    if (r >= kKept) score(32 * w + __ffs(bits) - 1, r);
-            }
     }
-    if (sparse || allow) __syncthreads();
+    // f(score, place) for each of the list, and behind it
+    auto each = [&](auto f) {
+        for (int r = tid; r < min(done, kKept); r += kThreads) f(sm.kept[r], (int)sm.place[r]);
+        if (done > kKept)
+            for (int w = tid; w < shape.words; w += kThreads)
+                for (uint32_t bits = set[w]; bits; bits &= bits - 1) f(out[token(32 * w + __ffs(bits) - 1)], 32 * w + __ffs(bits) - 1);
+    };
+    auto score = [&](float &x, int at, int word) {
+        const int v = token(at);
+        float y = x;
+        if (punish) {
+            int more = 0;
+            if (branch && (sm.drawn[at >> 5 & 31] >> (at & 31) & 1u)) {
+                const int k = sm.n_branch;
+                for (int j = 0; j < k; ++j) more += sm.branch[j] == v;
+            }
+            y = penalized(y, word, more, rho, alpha, beta);
+        }
+        if (b1 > b0 && (sm.biased[at >> 5 & 31] >> (at & 31) & 1u)) {
+            int i = b0;  // the first bias of the token
+            for (int len = b1 - b0; len > 0;) {
+                const int half = len >> 1;
+                if (p.bias_tokens[i + half] < v) i += half + 1, len -= half + 1;
+                else len = half;
+            }
+            for (; i < b1 && p.bias_tokens[i] == v; ++i) y = __fadd_rn(y, p.bias_values[i]);
+        }
+        x = y;
+    };
+    // the counts of the list, on the way during the first pass
+    constexpr int C = (kKept + kThreads - 1) / kThreads;
+    int word[C];
+#pragma unroll
+    for (int u = 0; u < C; ++u) word[u] = counts && tid + u * kThreads < min(done, kKept) ? counts[token(sm.place[tid + u * kThreads])] : 0;
+    auto score_all = [&]() {
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+            if (const int r = tid + u * kThreads; r < min(done, kKept)) score(sm.kept[r], sm.place[r], word[u]);
+        if (done > kKept)
+            for (int w = tid; w < shape.words; w += kThreads)
+                for (uint32_t bits = set[w]; bits; bits &= bits - 1) {
+                    const int at = 32 * w + __ffs(bits) - 1;
+                    score(out[token(at)], at, counts ? counts[token(at)] : 0);
+                }
+    };
     auto vector = [&](int i, float (&x)[W]) {
         const Vec<T, W> v = *reinterpret_cast<const Vec<T, W> *>(z + i);
 #pragma unroll
         for (int e = 0; e < W; ++e) x[e] = to_f32(v.e[e]);
     };
-    // f(score, place) for those beside the stretch
-    auto beside = [&](auto f) {
-        for (int r = tid; kBeside && r < min(done, kKept); r += kThreads) f(sm.kept[r], sm.place[r]);
-        if (kBeside && done > kKept)
-            for (int w = tid; w < shape.words; w += kThreads) {
-                int r = before[w];
-                for (uint32_t bits = set[w]; bits; bits &= bits - 1, ++r)
-                    if (r >= kKept) f(out[32 * w + __ffs(bits) - 1], 32 * w + __ffs(bits) - 1);
-            }
-    };
-    // out = f(score, place), in vectors where those of out are where those of z are
+    // out = f(score, token), in vectors where those of out are where those of z are
     // and no score waits in out
-    const bool wide = reinterpret_cast<uintptr_t>(out) % (4 * W) == 0 && (!kBeside || done <= kKept);
+    const bool wide = reinterpret_cast<uintptr_t>(out - begin) % (4 * W) == 0 && done <= kKept;
     auto write = [&](auto f) {
         if (wide) {
-            for (int i = tid * W; i < end; i += kThreads * W) {
+            for (int i = tid * W, v = v_first; i < n; i += kThreads * W, v += v_step) {
                 float x[W];
                 vector(i, x);
 #pragma unroll
-                for (int e = 0; e < W; ++e) x[e] = f(x[e], i + e);
-                if (i >= begin && i + W <= end) store<W>(out + i, x);
+                for (int e = 0; e < W; ++e) x[e] = f(x[e], v + e);
+                if (whole(v)) store<W>(out + v, x);
                 else
 #pragma unroll
                     for (int e = 0; e < W; ++e)
-                        if (i + e >= begin && i + e < end) out[i + e] = x[e];
+                        if (inside(v + e)) out[v + e] = x[e];
             }
         } else {
 #pragma unroll 4
-            for (int i = begin + tid; i < end; i += kThreads)
-                if (!kBeside || done <= kKept || !has(set, i)) out[i] = f(to_f32(z[i]), i);
+            for (int i = tid; i < n; i += kThreads)
+                if (const int v = token(i); inside(v) && (done <= kKept || !has(set, i))) out[v] = f(to_f32(z[i]), v);
         }
-        if (kBeside && done > 0) {
+        if (done > 0) {
             __syncthreads();
-            beside([&](float x, int at) { out[at] = f(x, at); });
+            each([&](float &x, int at) { out[token(at)] = f(x, token(at)); });
         }
     };
     if (!p.softmax) {
+        score_all();
         write([](float x, int) { return x; });
         return;
     }
@@ -339,22 +364,17 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
     const float heat = greedy ? 1.0f : fminf(1.4426950408889634f / temperature, kLargest);
     Part part = {none, 0.0f, INT32_MAX};
     if (greedy) {
-        for (int i = tid * W; i < end; i += kThreads * W) {
+        for (int i = tid * W, v = v_first; i < n; i += kThreads * W, v += v_step) {
             float x[W];
             vector(i, x);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                if (x[e] > part.top) part.top = x[e], part.at = lo + i + e - begin;
+                if (x[e] > part.top) part.top = x[e], part.at = v + e;
                 if (x[e] != x[e]) part.sum = x[e];
             }
         }
-        beside([&](float x, int at) {
-            const int token = lo + at - begin;
-            if (x > part.top || (x == part.top && token < part.at)) part.top = x, part.at = token;
-            if (x != x) part.sum = x;
-        });
     } else {
-        for (int i = tid * W; i < end; i += kThreads * W) {
+        for (int i = tid * W; i < n; i += kThreads * W) {
             float x[W], s[W];
             vector(i, x);
             float top = x[0];
@@ -373,38 +393,69 @@ __global__ void __launch_bounds__(kThreads, 5) process(LogitParams p) {
                 for (int e = 0; e < o; ++e) s[e] += s[e + o];
             part.sum += s[0];
         }
-        beside([&](float x, int) {
-            if (x > part.top) {
-                part.sum *= ex2((part.top - x) * heat);
-                part.top = x;
-            }
-            part.sum += ex2((x - (part.top == none ? 0.0f : part.top)) * heat);
-        });
     }
+    // Each warp's part, and the list's, to every CTA of the cluster.
+    auto tell = [&](const Part &x, int slot) {
+        if (lane >= ctas) return;
+        const uint32_t to = dsmem_addr(&sm.parts[rank * (kWarps + 1) + slot], lane);
+        dsmem_st_f32(to, x.top);
+        dsmem_st_f32(to + 4, x.sum);
+        dsmem_st_f32(to + 8, __int_as_float(x.at));
+    };
     part = warp_join(part, greedy, heat);
-    if (lane == 0) sm.warp[warp] = part;
-    __syncthreads();
     cluster_wait();  // (all have begun)
-    if (warp == 0) {
-        part = warp_join(lane < kWarps ? sm.warp[lane] : Part{none, 0.0f, INT32_MAX}, greedy, heat);
-        if (lane < ctas) {  // to every CTA of the cluster
-            const uint32_t to = dsmem_addr(&sm.ctas[rank], lane);
-            dsmem_st_f32(to, part.top);
-            dsmem_st_f32(to + 4, part.sum);
-            dsmem_st_f32(to + 8, __int_as_float(part.at));
-        }
+    tell(part, warp);
+    Part list = {none, 0.0f, INT32_MAX};
+    if (done > 0) {
+        float most = none;
+        score_all();
+        each([&](float &x, int) { most = fmaxf(most, x); });
+        most = warp_max(most);
+        if (lane == 0) sm.most[warp] = most;
+        __syncthreads();
+        list.top = warp_max(lane < kWarps ? sm.most[lane] : none);
+        const float about = list.top == none ? 0.0f : list.top;
+        unsigned long long steps = 0;
+        int lost = 0;
+        each([&](float &x, int at) {
+            if (greedy) {
+                if (x == list.top) list.at = min(list.at, token(at));
+                lost |= x != x;
+            } else {
+                const float y = ex2((x - about) * heat);
+                if (y > 0.0f) steps += (unsigned long long)(y * 0x1p40f);
+                lost |= y != y;
+            }
+        });
+        // (whole numbers: in any order)
+        steps = warp_sum(steps);
+        list.at = __reduce_min_sync(kFullMask, list.at);
+        if (lane == 0) atomicAdd(&sm.steps, steps), atomicMin(&sm.list_at, list.at);
+        if (lost) sm.lost = 1;
+        __syncthreads();
+        list.sum = sm.lost ? __int_as_float(0x7fc00000) : (float)sm.steps * 0x1p-40f;
+        list.at = sm.list_at;
     }
+    if (warp == 0) tell(list, kWarps);
     cluster_sync();
-    float top = none, sum = 0.0f;
-    for (int r = 0; r < ctas; ++r) top = fmaxf(top, sm.ctas[r].top);
-    for (int r = 0; r < ctas; ++r) sum += shifted(sm.ctas[r].sum, sm.ctas[r].top, top, heat);
+    // (up to 72 parts, three a lane)
+    Part row_part = {none, 0.0f, INT32_MAX};
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int i = lane + 32 * u;
+        if (i >= ctas * (kWarps + 1)) break;
+        const Part x = sm.parts[i];
+        const float most = fmaxf(row_part.top, x.top);
+        if (x.top == most) row_part.at = row_part.top == most ? min(row_part.at, x.at) : x.at;
+        row_part.sum = shifted(row_part.sum, row_part.top, most, heat) + shifted(x.sum, x.top, most, heat);
+        row_part.top = most;
+    }
+    row_part = warp_join(row_part, greedy, heat);
+    const float top = row_part.top, sum = row_part.sum;
     // a sum that is NaN makes all of the row that; nothing but -infinity makes it 0
     const float share = sum != sum ? sum : top == none ? 0.0f : greedy ? 1.0f : __fdiv_rn(1.0f, sum);
     if (greedy) {
-        int at = INT32_MAX;
-        for (int r = 0; r < ctas; ++r)
-            if (sm.ctas[r].top == top) at = min(at, sm.ctas[r].at);
-        write([&](float, int i) { return (lo + i - begin == at ? 1.0f : 0.0f) * share; });
+        write([&](float, int v) { return (v == row_part.at ? 1.0f : 0.0f) * share; });
     } else {
         // the exponential by halves: their product may be subnormal, they are not
         const float about = top == none ? 0.0f : top, half = 0.5f * heat;
@@ -505,9 +556,14 @@ __global__ void __launch_bounds__(kCountThreads) count_fork(CountParams p, const
 constexpr int kMaxDevices = 64;
 std::atomic<bool> g_ready[kMaxDevices];  // whether the kernels may use all the shared memory they need (twice does no harm)
 
+// Elements of the largest share of a row among ctas CTAs, wherever it begins.
+int chunk_of(int vocab, int ctas, int bytes) {
+    const int blocks = (16 / bytes - 1 + vocab + kBlock - 1) / kBlock;
+    return (blocks + ctas - 1) / ctas * kBlock;
+}
 size_t smem_of(int chunk, int bytes) {
-    const Stretch s = stretch_of(chunk, bytes);
-    return (size_t)s.elements + 6 * (size_t)s.words;
+    const Share s = share_of(chunk, bytes);
+    return (size_t)s.elements + 4 * (size_t)s.words;
 }
 
 cudaError_t prepare() {
@@ -519,7 +575,7 @@ cudaError_t prepare() {
                                                          {reinterpret_cast<const void *>(process<__half>), 2},
                                                          {reinterpret_cast<const void *>(process<float>), 4}};
     for (const auto &f : all) {
-        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxVocab / kMaxCtas, f.bytes))) !=
+        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(chunk_of(kMaxVocab, kMaxCtas, f.bytes), f.bytes))) !=
             cudaSuccess)
             return e;
         if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -533,12 +589,12 @@ template <typename T>
 cudaError_t go(LogitParams p, cudaStream_t stream) {
     const cudaError_t e = prepare();
     if (e != cudaSuccess) return e;
-    // CTAs of a row: stretches of up to 16384 elements (32768 where those would be more
-    // than eight), and more of them while there are not enough rows for the SMs.
+    // CTAs of a row: shares of about 16384 elements (32768 where those would be more than
+    // eight), and more of them while there are not enough rows for the SMs.
     int ctas = 1;
     while (ctas < kMaxCtas && ((int64_t)p.vocab > (int64_t)ctas * 16384 || (p.num_tokens * ctas * 2 <= 152 && p.vocab > ctas * 2048)))
         ctas *= 2;
-    p.chunk = ((p.vocab + ctas - 1) / ctas + 31) & ~31;
+    p.chunk = chunk_of(p.vocab, ctas, (int)sizeof(T));
     return launch_kernel(process<T>, dim3((unsigned)(p.num_tokens * ctas)), kThreads, smem_of(p.chunk, sizeof(T)), stream, ctas, true, p);
 }
 
