@@ -3,11 +3,19 @@
 A small random decoder runs the library's calls as a serving loop would:
 
   csgmv_build_batch_info + csgmv_qkv   the adapters' part of every layer's q, k, v
+  csgmv_add_norm                       a block's output into the residual stream, and
+                                       the norm before the next one
+  csgmv_rotary                         positions of drafted tokens
+  csgmv_kv_extend + csgmv_kv_append    prompts and single tokens, turned by their
+                                       positions, straight into the cache
   csgmv_tree_attention                 prompts (causal) and draft trees (masked)
                                        over the paged cache
   csgmv_build_draft_tree               masks and positions of the drafted tokens
-  csgmv_verify_drafts                  which of them stay, and the token after
-  csgmv_kv_commit                      their keys and values into the cache
+  csgmv_process_logits                 penalties, biases, temperature: the
+                                       distributions that the tokens come from
+  csgmv_verify_drafts                  which drafts stay, and the token after
+  csgmv_kv_commit, csgmv_count_tokens  their keys and values into the cache, the
+                                       tokens into the counts of the penalties
   csgmv_kv_fork / _free / _compact     two continuations of one prompt, requests
                                        that end
 
@@ -55,15 +63,18 @@ class Model:
         self.o = [weight(hq * d, hidden, std=0.5 * (hq * d) ** -0.5) for _ in range(layers)]
         self.lora_a = [weight(adapters, 3 * rank, hidden, std=hidden ** -0.5) for _ in range(layers)]
         self.lora_b = [weight(adapters, n, rank, std=0.5 * rank ** -0.5) for _ in range(layers)]
+        self.rms = B.Norm("rms", eps=1e-6)
+        self.rope = B.Rope(d, device=device)
         self.ranks = torch.tensor([0] + [rank] * (adapters - 1), dtype=torch.int32, device=device)
         self.scalings = torch.ones(adapters, device=device)
 
     @staticmethod
     def norm(x):
+        """What self.rms is, in torch."""
         return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
 
     def rotate(self, x, positions):
-        """Rotary positions; x is (tokens, heads, d)."""
+        """What self.rope is, in torch; x is (tokens, heads, d)."""
         half = self.d // 2
         freq = 10000.0 ** (-torch.arange(half, device=x.device, dtype=torch.float64) / half)
         a = (positions.double()[:, None] * freq)[:, None, :]
@@ -71,33 +82,44 @@ class Model:
         u, v = x[..., :half], x[..., half:]
         return torch.cat([u * c - v * s, u * s + v * c], -1)
 
-    def forward(self, tokens, positions, bi, cache, indptr, mask, slots, k_new, v_new):
-        """Logits of the rows; their keys and values go to k_new / v_new."""
+    def forward(self, tokens, positions, bi, cache, indptr, mask, slots, k_new=None, v_new=None, at=None):
+        """Logits of the rows.  Their keys and values go to k_new / v_new, or, with
+        at (csgmv_kv_extend's slots), straight into the cache's pages: cache then has
+        the lengths that the rows' attention is to see."""
         n = tokens.numel()
         a, b, c, end = self.offsets
-        x = self.emb[tokens].float()
+        block = self.emb[tokens]
+        x = torch.empty((n, self.hidden), device=self.device)
+        h = torch.empty((n, self.hidden), dtype=torch.bfloat16, device=self.device)
+        B.csgmv_add_norm(block, self.rms, h, residual_out=x)
         out = torch.empty((n, self.hq, self.d), dtype=torch.bfloat16, device=self.device)
         lora_ws = torch.empty(B.csgmv_qkv_workspace_bytes(bi, 3), dtype=torch.uint8, device=self.device)
         attn_ws = torch.empty(B.csgmv_tree_attention_workspace_bytes(cache, self.hq), dtype=torch.uint8, device=self.device)
         for i in range(self.layers):
-            h = self.norm(x).to(torch.bfloat16)
             qkv = h @ self.qkv[i]
             B.csgmv_qkv(h, self.lora_a[i], self.lora_b[i], self.offsets, 3, b - a, qkv, bi, workspace=lora_ws)
-            q = self.rotate(qkv[:, a:b].float().view(n, self.hq, self.d), positions).to(torch.bfloat16)
-            k_new[i] = self.rotate(qkv[:, b:c].float().view(n, self.hkv, self.d), positions).to(torch.bfloat16)
-            v_new[i] = qkv[:, c:end].view(n, self.hkv, self.d)
-            B.csgmv_tree_attention(q, k_new[i], v_new[i], cache, i, indptr, out, mask=mask, seq_slots=slots, workspace=attn_ws)
-            x = x + (out.view(n, -1) @ self.o[i]).float()
-        return (self.norm(x).to(torch.bfloat16) @ self.head).float()
+            q, k, v = (qkv[:, lo:hi].view(n, -1, self.d) for lo, hi in ((a, b), (b, c), (c, end)))
+            if at is None:
+                B.csgmv_rotary(self.rope, positions, q, k, k_out=k_new[i])
+                v_new[i] = v
+                k, v = k_new[i], v_new[i]
+            else:
+                B.csgmv_kv_append(cache, i, k, v, at, positions, rope=self.rope, q=q, k_out=k)
+            B.csgmv_tree_attention(q, k, v, cache, i, indptr, out, mask=mask, seq_slots=slots, workspace=attn_ws)
+            B.csgmv_add_norm(out.view(n, -1) @ self.o[i], self.rms, h, residual=x)
+        return h @ self.head
 
     def draft_logits(self, tokens):
         return (self.norm(self.emb[tokens].float()).to(torch.bfloat16) @ self.head).float()
 
 
 class Decoder:
-    """Speculative decoding over a paged cache with `max_seqs` sequences."""
+    """Speculative decoding over a paged cache with `max_seqs` sequences.  The
+    penalties and bias ({token: value}) are every request's; a sequence's given
+    tokens are counted from the last one of its prompt on."""
 
-    def __init__(self, model, max_seqs, max_len, page_size=16, parents=PARENTS, temperature=0.0, seed=0):
+    def __init__(self, model, max_seqs, max_len, page_size=16, parents=PARENTS, temperature=0.0, seed=0, repetition=1.0,
+                 frequency=0.0, presence=0.0, bias=None):
         m = self.m = model
         pages = -(-(max_len + len(parents)) // page_size)
         self.cache = B.KvCache.allocate(m.layers, max_seqs * pages, page_size, m.hkv, m.d, max_seqs, pages, device=m.device)
@@ -109,6 +131,10 @@ class Decoder:
         self.rng = torch.Generator(device=m.device)
         self.rng.manual_seed(seed)
         self.steps = self.kept = 0
+        self.penalties, self.bias = (repetition, frequency, presence), sorted((bias or {}).items())
+        self.counts = None
+        if self.penalties != (1.0, 0.0, 0.0):
+            self.counts = B.TokenCounts(max_seqs, m.vocab, device=m.device)
 
     def ints(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.m.device)
@@ -125,6 +151,18 @@ class Decoder:
         shape = (m.layers, n, m.hkv, m.d)
         return tuple(torch.empty(shape, dtype=torch.bfloat16, device=m.device) for _ in range(2))
 
+    def rules(self, bs):
+        """What a batch's logits go through."""
+        each = lambda v: torch.full((bs,), v, device=self.m.device)
+        kw = {"temperature": each(float(self.temperature))}
+        if self.counts is not None:
+            kw.update(zip(("repetition", "frequency", "presence"), map(each, self.penalties)), counts=self.counts)
+        if self.bias:
+            tokens, values = zip(*self.bias)
+            kw["bias"] = (torch.arange(0, len(tokens) * bs + 1, len(tokens), dtype=torch.int32, device=self.m.device),
+                          self.ints(tokens * bs), torch.tensor(values * bs, device=self.m.device))
+        return B.LogitRules(device=self.m.device, **kw)
+
     def prefill(self, prompts, adapters, slots):
         """All of each prompt but its last token, into the cache."""
         lens = [len(p) - 1 for p in prompts]
@@ -133,20 +171,26 @@ class Decoder:
         at = [0]
         for n in lens:
             at.append(at[-1] + n)
-        tokens = self.ints([t for p in prompts for t in p[:-1]]).long()
-        positions = torch.cat([torch.arange(n, device=self.m.device) for n in lens])
-        k, v = self.new_rows(at[-1])
+        tokens = self.ints([t for p in prompts for t in p[:-1]])
         indptr, slots = self.ints(at), self.ints(slots)
-        self.m.forward(tokens, positions, self.batch(lens, adapters), self.cache, indptr, None, slots, k, v)
-        B.csgmv_kv_commit(self.cache, k, v, None, self.ints(lens), indptr, seq_slots=slots)
+        before = torch.empty_like(self.cache.seq_lens)
+        where, positions = B.csgmv_kv_extend(self.cache, indptr, at[-1], seq_slots=slots, lens_before=before)
+        # the rows see what the cache held before, and one another
+        self.m.forward(tokens.long(), positions, self.batch(lens, adapters), self.cache.with_lens(before), indptr, None, slots, at=where)
+        if self.counts is not None:
+            B.csgmv_count_tokens(self.counts, tokens, indptr, seq_slots=slots, prompt=True)
 
     def fork(self, parents, children):
         B.csgmv_kv_fork(self.cache, self.ints(parents), self.ints(children))
+        if self.counts is not None:
+            B.csgmv_count_fork(self.counts, self.ints(parents), self.ints(children))
 
     def free(self, slots):
         """Ends sequences and closes the holes that they leave in the pool."""
         B.csgmv_kv_free(self.cache, self.ints(slots))
         B.csgmv_kv_compact(self.cache)
+        if self.counts is not None:
+            B.csgmv_count_reset(self.counts, self.ints(slots))
 
     def draft(self, last):
         """Draft tokens (requests, nodes) from the last tokens, and the drafter's
@@ -174,19 +218,24 @@ class Decoder:
         indptr = torch.arange(0, n + 1, width, dtype=torch.int32, device=m.device)
         tree = B.DraftTree(n, width, device=m.device)
         B.csgmv_build_draft_tree(tree, self.ints(self.parents * bs), indptr)
-        positions = self.cache.seq_lens[slots.long()].repeat_interleave(width) + tree.depth
-        k, v = self.new_rows(n)
-        logits = m.forward(tokens.view(-1), positions, self.batch([width] * bs, adapters), self.cache, indptr, tree.mask,
-                           slots, k, v)
-        if self.temperature:
-            probs = torch.softmax(logits / self.temperature, -1)
-            draft_probs = draft_probs.view(n, -1)
+        flat, bi, k = tokens.view(-1).int(), self.batch([width] * bs, adapters), None
+        if width == 1:
+            # plain decoding: the token goes straight into the cache, and is seen from there
+            where, positions = B.csgmv_kv_extend(self.cache, indptr, n, seq_slots=slots)
+            logits = m.forward(tokens.view(-1), positions, bi, self.cache, indptr, torch.zeros_like(tree.mask), slots, at=where)
         else:
-            probs = torch.nn.functional.one_hot(logits.argmax(-1), m.vocab).float()
+            positions = self.cache.seq_lens[slots.long()].repeat_interleave(width) + tree.depth
+            k, v = self.new_rows(n)
+            logits = m.forward(tokens.view(-1), positions, bi, self.cache, indptr, tree.mask, slots, k, v)
+        probs = B.csgmv_process_logits(logits, indptr, self.rules(bs), draft_tokens=flat, mask=tree.mask, seq_slots=slots)
+        if self.temperature:
+            draft_probs = draft_probs.view(n, -1)
         uniforms = torch.rand(n + bs, generator=self.rng, device=m.device)
-        path, count, after = B.csgmv_verify_drafts(probs, tokens.view(-1).int(), indptr, tree, uniforms[:n], uniforms[n:],
-                                                   draft_probs=draft_probs)
-        B.csgmv_kv_commit(self.cache, k, v, path, count, indptr, seq_slots=slots)
+        path, count, after = B.csgmv_verify_drafts(probs, flat, indptr, tree, uniforms[:n], uniforms[n:], draft_probs=draft_probs)
+        if k is not None:
+            B.csgmv_kv_commit(self.cache, k, v, path, count, indptr, seq_slots=slots)
+        if self.counts is not None:
+            B.csgmv_count_tokens(self.counts, flat, indptr, path, count, seq_slots=slots)
         path, count, after, tokens = (t.tolist() for t in (path, count, after, tokens))
         self.steps += bs
         self.kept += sum(count)
