@@ -736,7 +736,9 @@ CSGMV_API int csgmv_rotary(const csgmv_rope *rope, int dtype, int head_dim, cons
  * Requests are left out as by csgmv_kv_commit.  A tree_indptr that decreases or
  * leaves [0, num_tokens] (CSGMV_KV_STATUS_BAD_LENS), or too few free pages
  * (CSGMV_KV_STATUS_CAPACITY): nothing is extended, all slots are -1.  bs <=
- * max_seqs.  No two of the call's buffers overlap one another or the cache's.
+ * max_seqs.  slots holds until a page is moved, shared or given up
+ * (csgmv_kv_compact, _fork, _free of the sequence): bring the contents before.
+ * The call's buffers overlap neither one another nor the cache's.
  */
 CSGMV_API int csgmv_kv_extend(const csgmv_kv_cache *kv, const int32_t *add_lens, const int32_t *tree_indptr,
                               const int32_t *seq_slots, int bs, int64_t num_tokens, int64_t *slots, int32_t *positions,

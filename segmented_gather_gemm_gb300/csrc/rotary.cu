@@ -39,8 +39,9 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
         if (at < 0 || at >= p.num_slots) {
             if (at != -1 && slot0 == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_PAGE);
             mine = false;
+        } else {
+            to = (at >> p.page_shift) * p.page_stride + (at & ((1 << p.page_shift) - 1)) * p.token_stride;
         }
-        to = (at >> p.page_shift) * p.page_stride + (at & ((1 << p.page_shift) - 1)) * p.token_stride;
     }
     for (int i = threadIdx.x; i < s.tokens * s.pairs * W; i += kThreads) {
         const int token = i / (s.pairs * W);
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
     }
 }
 
-// The widest units (16 bytes of elements, or two, or one): W pairs and W elements
-// of what is not turned, all addresses multiples of W elements.
+// The widest units (16 bytes of elements, four, two or one): W pairs and W
+// elements of what is not turned, all addresses multiples of W elements.
 int width_for(const RotaryParams &p, int bytes) {
     uint64_t at = 0;
     int64_t strides = 0;
@@ -125,7 +126,7 @@ int width_for(const RotaryParams &p, int bytes) {
         at |= reinterpret_cast<uintptr_t>(p.k_pages) | reinterpret_cast<uintptr_t>(p.v_pages);
         strides |= p.page_stride | p.head_stride | p.token_stride;
     }
-    for (int w : {16 / bytes, 2}) {
+    for (int w : {16 / bytes, 4, 2}) {
         const int align = w * bytes;
         if (p.rot / 2 % w == 0 && p.d % w == 0 && at % align == 0 && strides * bytes % align == 0) return w;
     }
@@ -158,6 +159,7 @@ cudaError_t pick(const RotaryParams &p, cudaStream_t stream) {
     constexpr int kWide = 16 / (int)sizeof(T);
     const int w = width_for(p, (int)sizeof(T));
     if (w == kWide) return go<T, kWide, APPEND>(p, stream);
+    if (w == 4) return go<T, 4, APPEND>(p, stream);
     return w == 2 ? go<T, 2, APPEND>(p, stream) : go<T, 1, APPEND>(p, stream);
 }
 
