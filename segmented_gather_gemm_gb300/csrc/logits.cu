@@ -13,7 +13,17 @@
 // of exponentials together, then the probabilities; the list's counts come
 // during the first.  The list is in no certain order, so its exponentials are summed in
 // whole steps of 2^-40 of the CTA's largest: results do not depend on timing.
-// The CTAs of a row exchange one pair of numbers between the passes.
+// The CTAs of a row exchange a pair of numbers a warp between the passes.
+//
+// Measured (device time): 768 bf16 rows of 128256 (64 drafted trees with counts,
+// biases, a quarter of them with masks; 595 MB) 165 us; without any rule 109 us, 5.4
+// TB/s.  256 f32 rows of 100003 70 us, without rules 51 us.  A row's chain of dependent
+// loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
+// sparse) is hidden by five CTAs an SM, three with f32: what holds it up is room
+// for more of them.  (Also tried: scores in f32 shared memory, three CTAs an SM,
+// 286 us; the row read again from L2 with a test for each vector, 210 us; the list
+// in the order of the vocabulary by prefix sums, 172 us; 128 to 512 threads, 165 to
+// 190 us; exponents in one fused operation, 180 us, or two at a time, 170 us.)
 #include <algorithm>
 #include <atomic>
 

@@ -7,7 +7,14 @@
 // itself, so no angle loses bits however far its position is, and no table of
 // cosines is read.  A CTA takes the sines and cosines of its tokens once, into
 // shared memory.  A thread owns W neighbouring pairs (two vectors of W elements, or
-// one of 2 W where pairs lie side by side) of one token in some of its heads.
+// one of 2 W where pairs lie side by side) of one token in some of its heads.  One
+// head at a time: more loads under way a thread take registers from the warps that
+// hide them (four heads: 220 us where one takes 117).
+//
+// Measured (device time): 35507 tokens of 32 + 8 heads of 128, bf16 (727 MB) 117 us,
+// 6.2 TB/s; with values into a layer's pages, 35700 tokens in half (880 MB) 142 us;
+// 12 tokens 3.0 us, a launch and two rounds of loads.  What bounds the large ones is
+// HBM (DRAM 75 to 77 % busy by the counters).
 #include "elements.cuh"
 #include "serving.cuh"
 #include "step.h"
