@@ -16,14 +16,15 @@
 // The CTAs of a row exchange a pair of numbers a warp between the passes.
 //
 // Measured (device time): 768 bf16 rows of 128256 (64 drafted trees with counts,
-// biases, a quarter of them with masks; 595 MB) 165 us; without any rule 109 us, 5.4
-// TB/s.  256 f32 rows of 100003 70 us, without rules 51 us.  A row's chain of dependent
+// biases, a quarter of them with masks; 595 MB) 161 us; without any rule 108 us, 5.5
+// TB/s.  256 f32 rows of 100003 69 us, without rules 50 us.  A row's chain of dependent
 // loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
 // sparse) is hidden by five CTAs an SM, three with f32: what holds it up is room
 // for more of them.  (Also tried: scores in f32 shared memory, three CTAs an SM,
 // 286 us; the row read again from L2 with a test for each vector, 210 us; the list
 // in the order of the vocabulary by prefix sums, 172 us; 128 to 512 threads, 165 to
-// 190 us; exponents in one fused operation, 180 us, or two at a time, 170 us.)
+// 190 us; exponents in one fused operation, 180 us, or two at a time, 170 us; one
+// atomic a warp for places in the list, 172 us.)
 #include <algorithm>
 #include <atomic>
 
@@ -142,6 +143,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
         else
             for (int e = 0; e < W; ++e) z[i + e] = inside(v + e) ? row[v + e] : from_f32<T>(none);
     }
+    // (a word of the row's mask a lane: eight at most)
+    const uint32_t mask_word = warp == 0 && p.mask && lane < p.mask_words ? (uint32_t)p.mask[(int64_t)t * p.mask_words + lane] : 0;
     // the row's request: the last one that begins at or before it, 32 tried at once
     int b = 0;
     for (int len = p.bs; len > 1;) {
@@ -199,34 +202,40 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
 #pragma unroll
         for (int u = 0; u < S; ++u) held_at[u] = place(held_at[u]);
     };
+    // the last warp has the first biases, the first one the branch: loads before all that waits
+    const int bias_i = b0 + (tid ^ (kThreads - 32));
+    int bias_v = 0, bias_before = 0;
+    if (bias_i < b1) {
+        bias_v = p.bias_tokens[bias_i];
+        bias_before = bias_i > b0 ? p.bias_tokens[bias_i - 1] : bias_v;
+        prefetch(p.bias_values + bias_i);
+    }
+    if (branch && warp == 0) {
+        int k = 0;
+        for (int w = 0; w < p.mask_words; ++w) {
+            const uint32_t bits = __shfl_sync(kFullMask, mask_word, w);
+            const int j = 32 * w + lane;
+            int v = -1;
+            if ((bits >> lane & 1u) && j < last - first) {
+                v = p.drafts[first + j];
+                if (!inside(v)) {
+                    if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
+                    v = -1;
+                }
+            }
+            const unsigned m = __ballot_sync(kFullMask, v >= 0);
+            if (v >= 0) sm.branch[k + __popc(m & ((1u << lane) - 1u))] = v;
+            k += __popc(m);
+        }
+        if (lane == 0) sm.n_branch = k;
+    }
     load_held(0);
 #pragma unroll
     for (int u = 0; u < S; ++u)
         if (held_at[u] >= 0) prefetch(counts + token(held_at[u]));
     if (allow && tid * kBlock < n) prefetch(allow + (max(token(tid * kBlock), 0) >> 5));
-    if (sparse) {
-        if (b0 + tid < b1) prefetch(p.bias_tokens + b0 + tid), prefetch(p.bias_values + b0 + tid);
+    if (sparse)
         for (int i = tid; i < shape.words; i += kThreads) set[i] = 0;
-        if (branch && warp == 0) {
-            int k = 0;
-            for (int w = 0; w < p.mask_words; ++w) {
-                const uint32_t bits = (uint32_t)p.mask[(int64_t)t * p.mask_words + w];
-                const int j = 32 * w + lane;
-                int v = -1;
-                if ((bits >> lane & 1u) && j < last - first) {
-                    v = p.drafts[first + j];
-                    if (!inside(v)) {
-                        if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
-                        v = -1;
-                    }
-                }
-                const unsigned m = __ballot_sync(kFullMask, v >= 0);
-                if (v >= 0) sm.branch[k + __popc(m & ((1u << lane) - 1u))] = v;
-                k += __popc(m);
-            }
-            if (lane == 0) sm.n_branch = k;
-        }
-    }
     cp_async_wait_all();
     __syncthreads();
     if (allow) {  // what is not allowed, out of the stretch
@@ -260,12 +269,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
                 take(at);
             }
         bool torn = false;
-        for (int i = b0 + tid; i < b1; i += kThreads) {
-            const int v = p.bias_tokens[i];
-            torn |= i > b0 && v < p.bias_tokens[i - 1];
-            if (!inside(v)) {
+        for (int i = bias_i; i < b1; i += kThreads) {
+            if (i > bias_i) bias_v = p.bias_tokens[i], bias_before = p.bias_tokens[i - 1];
+            torn |= bias_v < bias_before;
+            if (!inside(bias_v)) {
                 if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
-            } else if (const int at = place(v); at >= 0) {
+            } else if (const int at = place(bias_v); at >= 0) {
                 atomicOr(&sm.biased[at >> 5 & 31], 1u << (at & 31));
                 take(at);
             }
