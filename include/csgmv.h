@@ -710,7 +710,8 @@ CSGMV_API int csgmv_rope_turns(const double *freq, int n, uint64_t *turns);
  *               output overlaps an input, nor the other output
  *   inverse     1: by the negative angles, times scale: the gradient of the
  *               inputs from that of the outputs
- * Products are f32, rounded once.  1 <= head_dim <= 1024.
+ * Products are f32, rounded once.  1 <= head_dim <= 1024; at most 4096 heads of each;
+ * strides of at most 2^40 elements (as in the calls below and above).
  */
 CSGMV_API int csgmv_rotary(const csgmv_rope *rope, int dtype, int head_dim, const int32_t *positions,
                            int64_t num_tokens, const void *q, int64_t q_token_stride, int64_t q_head_stride,

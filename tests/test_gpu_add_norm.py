@@ -104,6 +104,44 @@ def test_parts_left_out():
     assert B.csgmv_add_norm(x[:0], B.Norm("rms")).shape == (0, D)
 
 
+def test_a_norm_that_is_none_and_broadcast_rows():
+    """kind "none" with an output: the sum, rounded; one row of x or of the residual
+    for all (stride 0)."""
+    g = torch.Generator().manual_seed(3)
+    n, none = 50, ("none", None, None, EPS)
+    for D in (4096, 1001):
+        x, r = draw(g, (1, D), BF).expand(n, D), draw(g, (n, D), F32)
+        after = torch.empty_like(r)
+        out = B.csgmv_add_norm(x, B.Norm("none"), residual=r, residual_out=after, residual_scale=0.5)
+        check(after, out, add_norm(x, r, None, none, none, 0.5), F32)
+        pre, ref = side(g, "layer", D, BF, True)
+        x, r = draw(g, (n, D), BF), draw(g, (1, D), BF).expand(n, D)
+        after = torch.empty((n, D), dtype=BF, device="cuda")
+        out = B.csgmv_add_norm(x, pre, residual=r, residual_out=after)
+        check(after, out, add_norm(x, r, None, none, ref, 1.0), BF)
+
+
+@pytest.mark.parametrize("rtype", [BF, F32])
+@pytest.mark.parametrize("D", [513, 4097])
+@pytest.mark.parametrize("shifts", [(0, 0, 0, 0), (3, 3, 3, 3), (1, 5, 5, 1), (1, 2, 3, 4)])
+def test_rows_that_begin_anywhere(rtype, D, shifts):
+    """Odd widths, each tensor's first row somewhere behind a boundary: alike, alike
+    modulo the four elements of an f32 vector, or each elsewhere."""
+    g = torch.Generator().manual_seed(D + sum(shifts))
+    n, none = 21, ("none", None, None, EPS)
+
+    def rows(shift, dtype):
+        flat = draw(g, (n * D + 8,), dtype)
+        return flat, flat[shift:shift + n * D].view(n, D)
+    (fx, x), (fr, r), (fa, after), (fo, out) = rows(shifts[0], BF), rows(shifts[1], rtype), rows(shifts[2], rtype), rows(shifts[3], BF)
+    was = fa.clone(), fo.clone()
+    pre, ref = side(g, "rms", D, BF, True)
+    B.csgmv_add_norm(x, pre, out, residual=r, residual_out=after)
+    check(after, out, add_norm(x, r, None, none, ref, 1.0), rtype)
+    for flat, old, k in ((fa, was[0], shifts[2]), (fo, was[1], shifts[3])):
+        assert torch.equal(flat[:k], old[:k]) and torch.equal(flat[k + n * D:], old[k + n * D:])
+
+
 def test_rows_of_one_value_and_of_infinities():
     """A centred norm of equal values is its bias; what is not finite stays in its row."""
     D = 1024

@@ -190,6 +190,38 @@ def test_slots_outside_the_cache_are_left_out():
     assert torch.equal(rows(c.k_pages, "HND")[1, most - 1], k[1]) and torch.equal(rows(c.v_pages, "HND")[1, 0], k[4])
 
 
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_slots_past_32_bits_of_elements(layout):
+    """2.2e9 elements a pool: the last slots are where they belong."""
+    c = B.KvCache.allocate(1, 34000, 64, 8, 128, 1, 8, layout=layout)
+    most, g = c.num_pages * c.page_size, torch.Generator().manual_seed(1)
+    k, v = (torch.randn((3, 8, 128), generator=g).to(BF).cuda() for _ in range(2))
+    at = [most - 1, most - 64, 5]
+    B.csgmv_kv_append(c, 0, k, v, ints(at, torch.int64))
+    for i, a in enumerate(at):
+        for pool, new in ((c.k_pages, k), (c.v_pages, v)):
+            page = pool[0, a // 64]
+            assert torch.equal(page[:, a % 64] if layout == "HND" else page[a % 64], new[i])
+
+
+def test_pages_with_gaps_and_heads_broadcast():
+    """Strides of the cache beyond its sizes; one head's values for all heads."""
+    wide = torch.full((2, 6, 3, 20, 72), 7.0, dtype=BF, device="cuda"), torch.full((2, 6, 3, 20, 72), 7.0, dtype=BF, device="cuda")
+    kp, vp = (w[:, :, :, :16, :64] for w in wide)
+    c = B.KvCache(kp, vp, torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                  torch.zeros(6, dtype=torch.int32, device="cuda"))
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.randn((20, 3, 64), generator=g).to(BF).cuda(), torch.randn((20, 1, 64), generator=g).to(BF).cuda().expand(20, 3, 64)
+    slots, pos = B.csgmv_kv_extend(c, ints([0, 17, 20]), 20)
+    rope = B.Rope(64, interleaved=True)
+    B.csgmv_kv_append(c, 1, k, v, slots, pos, rope=rope)
+    close(rows(kp, "HND")[1, slots], *rotary(k, pos, rope.freq, 64, True))
+    assert torch.equal(rows(vp, "HND")[1, slots], v)
+    for w, p in zip(wide, (kp, vp)):
+        p.fill_(7.0)
+        assert bool((w == 7.0).all())
+
+
 def test_keys_turned_in_place():
     """k_out = k: a projection's rows are ready for attention and in the cache."""
     c, g = make([5, 20, 100], d=128, layout="NHD")

@@ -132,7 +132,34 @@ def test_large_vocabularies(dtype, vocab):
     b.check(b.call())
 
 
-@pytest.mark.parametrize("bs", [2, 33, 300])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("vocab,softmax", [(40000, True), (40000, False), (39999, True), (200000, True)])
+def test_more_tokens_held_than_the_list_has_room_for(dtype, vocab, softmax):
+    """Most of a small vocabulary, and a good part of a large one."""
+    b = Batch(vocab, [2, 1, 1], dtype, seed=vocab + softmax, history=60000, biases=2000, masks=vocab != 40000)
+    b.heat[0] = 0.0
+    b.rules.temperature[0] = 0.0
+    b.check(b.call(softmax=softmax), softmax)
+    if dtype is F32:
+        want = [[b.row(i, j, softmax) for j in range(t)] for i, t in enumerate(b.T)]
+        out = b.call(b.logits, softmax=softmax)
+        for i, t in enumerate(b.T):
+            for j in range(t):
+                close(out[b.ptr[i] + j], *want[i][j])
+
+
+def test_results_do_not_depend_on_the_order_of_the_list():
+    """The same counts listed in another order, and many runs: the same bits."""
+    b = Batch(30000, [3, 2], BF, seed=77, history=20000)
+    first = b.call()
+    for k in range(5):
+        for s in b.seqs:
+            n = int(b.counts.num_seen[s])
+            b.counts.seen[s, :n] = b.counts.seen[s, :n][torch.randperm(n, device="cuda")]
+        assert torch.equal(b.call(), first)
+
+
+@pytest.mark.parametrize("bs", [2, 33, 300, 5000])
 def test_many_requests(bs):
     """One row each and some without; enough rows that a CTA has a whole one."""
     b = Batch(640, [i % 4 != 1 for i in range(bs)], F32, seed=bs, branch=False)
@@ -346,6 +373,21 @@ def test_counting():
             refs[s].add(l, prompt)
         same_counts(c, refs)
     assert c.device_status() == 0
+
+
+def test_counting_long_prompts():
+    V, lens, g = 50000, [200000, 0, 3, 70001], torch.Generator().manual_seed(2)
+    tokens = (V * torch.rand(sum(lens), generator=g) ** 3).int()
+    c, p = B.TokenCounts(4, V), indptr(lens)
+    B.csgmv_count_tokens(c, tokens.cuda(), ints(p))
+    B.csgmv_count_tokens(c, tokens.cuda(), ints(p), prompt=True)
+    for s in range(4):
+        want = torch.bincount(tokens[p[s]:p[s + 1]].long(), minlength=V)
+        assert torch.equal(c.counts[s].cpu(), (want + (want > 0) * 2 ** 30).int())
+        n = int(c.num_seen[s])
+        assert torch.equal(c.seen[s, :n].cpu().long().sort().values, want.nonzero()[:, 0])
+    B.csgmv_count_reset(c, ints([0, 1, 2, 3]))
+    assert not bool(c.counts.any()) and not bool(c.num_seen.any())
 
 
 def test_counting_accepted_paths():
