@@ -236,9 +236,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
     if (allow && tid * kBlock < n) prefetch(allow + (max(token(tid * kBlock), 0) >> 5));
     if (sparse)
         for (int i = tid; i < shape.words; i += kThreads) set[i] = 0;
+    bool torn = bias_v < bias_before;
+    for (int i = bias_i + kThreads; i < b1; i += kThreads) torn |= p.bias_tokens[i] < p.bias_tokens[i - 1];
     cp_async_wait_all();
-    __syncthreads();
-    if (allow) {  // what is not allowed, out of the stretch
+    if (__syncthreads_or(torn)) {  // biases out of order; every CTA of the cluster alike
+        if (rank == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_VALUE);
+        return;
+    }
+    if (allow) {  // what is not allowed, out of there
 #pragma unroll 4
         for (int i = tid * W, v0 = v_first; i < n; i += kThreads * W, v0 += v_step) {
             const int from = min(max(v0, 0), p.vocab - 1);  // (the vector may begin before the row)
@@ -268,10 +273,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
                 atomicOr(&sm.drawn[at >> 5 & 31], 1u << (at & 31));
                 take(at);
             }
-        bool torn = false;
         for (int i = bias_i; i < b1; i += kThreads) {
-            if (i > bias_i) bias_v = p.bias_tokens[i], bias_before = p.bias_tokens[i - 1];
-            torn |= bias_v < bias_before;
+            if (i > bias_i) bias_v = p.bias_tokens[i];
             if (!inside(bias_v)) {
                 if (rank == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_TOKEN);
             } else if (const int at = place(bias_v); at >= 0) {
@@ -285,10 +288,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
             for (int u = 0; u < S; ++u)
                 if (held_at[u] >= 0) take(held_at[u]);
         }
-        if (__syncthreads_or(torn)) {  // biases out of order; every CTA of the cluster alike
-            if (rank == 0 && tid == 0) atomicOr(p.status, CSGMV_KV_STATUS_BAD_VALUE);
-            return;
-        }
+        __syncthreads();
         done = sm.n_kept;
         if (done > kKept) {  // bits of those that the list has no room for are left
             for (int r = tid; r < kKept; r += kThreads) atomicAnd(set + (sm.place[r] >> 5), ~(1u << (sm.place[r] & 31)));
@@ -424,21 +424,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
     part = warp_join(part, greedy, heat);
     cluster_wait();  // (all have begun)
     tell(part, warp);
+    // The list's part: by the first warp alone where it has them all, without barriers.
     Part list = {none, 0.0f, INT32_MAX};
-    if (done > 0) {
-        float most = none;
+    const bool many = done > 32;
+    if (many || (done > 0 && warp == 0)) {
         score_all();
+        float most = none;
         each([&](float &x, int) { most = fmaxf(most, x); });
         most = warp_max(most);
-        if (lane == 0) sm.most[warp] = most;
-        __syncthreads();
-        list.top = warp_max(lane < kWarps ? sm.most[lane] : none);
-        const float about = list.top == none ? 0.0f : list.top;
+        if (many) {
+            if (lane == 0) sm.most[warp] = most;
+            __syncthreads();
+            most = warp_max(lane < kWarps ? sm.most[lane] : none);
+        }
+        list.top = most;
+        const float about = most == none ? 0.0f : most;
         unsigned long long steps = 0;
         int lost = 0;
         each([&](float &x, int at) {
             if (greedy) {
-                if (x == list.top) list.at = min(list.at, token(at));
+                if (x == most) list.at = min(list.at, token(at));
                 lost |= x != x;
             } else {
                 const float y = ex2((x - about) * heat);
@@ -449,11 +454,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
         // (whole numbers: in any order)
         steps = warp_sum(steps);
         list.at = __reduce_min_sync(kFullMask, list.at);
-        if (lane == 0) atomicAdd(&sm.steps, steps), atomicMin(&sm.list_at, list.at);
-        if (lost) sm.lost = 1;
-        __syncthreads();
-        list.sum = sm.lost ? __int_as_float(0x7fc00000) : (float)sm.steps * 0x1p-40f;
-        list.at = sm.list_at;
+        lost = __any_sync(kFullMask, lost);
+        if (many) {
+            if (lane == 0) {
+                atomicAdd(&sm.steps, steps), atomicMin(&sm.list_at, list.at);
+                if (lost) sm.lost = 1;
+            }
+            __syncthreads();
+            steps = sm.steps, list.at = sm.list_at, lost = sm.lost;
+        }
+        list.sum = lost ? __int_as_float(0x7fc00000) : (float)steps * 0x1p-40f;
     }
     if (warp == 0) tell(list, kWarps);
     cluster_sync();

@@ -313,6 +313,20 @@ def test_bad_requests_are_left_out():
     run(torn, BAD_VALUE, [3])
 
 
+def test_biases_out_of_order_beside_a_full_list():
+    """More tokens than the list holds, and the last of many biases out of order: the
+    rows stay as they are."""
+    b = Batch(40000, [2, 1], BF, seed=5, history=60000, biases=2000, masks=False)
+    n = int(b.rules.bias[0][2] - b.rules.bias[0][1])
+    assert n > 256  # not all of them are looked at by one round of threads
+    b.rules.bias[1][-1] = 0
+    out = torch.full((3, 40000), 9.0, device="cuda")
+    b.call(out)
+    assert b.rules.device_status() == BAD_VALUE
+    b.check(out, skip=[1])
+    assert bool((out[2] == 9.0).all())
+
+
 def test_bad_rows_and_tokens():
     b = Batch(300, [2, 3], F32, seed=22, masks=True)
     b.rules.allow_index[1], b.rules.allow_index[3] = 99, -2
