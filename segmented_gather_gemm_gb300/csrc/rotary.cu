@@ -7,13 +7,15 @@
 // itself, so no angle loses bits however far its position is, and no table of
 // cosines is read.  A CTA takes the sines and cosines of its tokens once, into
 // shared memory.  A thread owns W neighbouring pairs (two vectors of W elements, or
-// one of 2 W where pairs lie side by side) of one token in some of its heads.  One
+// one of 2 W where pairs lie side by side) of one token in some of its heads.  What is not
+// turned is moved two vectors at a time too, or, in place, not touched.  One
 // head at a time: more loads under way a thread take registers from the warps that
 // hide them (four heads: 220 us where one takes 117).
 //
 // Measured (device time): 35507 tokens of 32 + 8 heads of 128, bf16 (727 MB) 117 us,
 // 6.2 TB/s; with values into a layer's pages, 35700 tokens in half (880 MB) 142 us;
-// 12 tokens 3.0 us, a launch and two rounds of loads.  What bounds the large ones is
+// 12 tokens 3.0 us, a launch and two rounds of loads.  With 32 of the 128 turned 116 us
+// (149 by single vectors of the rest), 53 in place.  What bounds the large ones is
 // HBM (DRAM 75 to 77 % busy by the counters).
 #include "elements.cuh"
 #include "serving.cuh"
@@ -63,10 +65,13 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
     __syncthreads();
     if (!mine) return;
     for (int slot = slot0; slot < s.units * s.lanes; slot += s.slots) {
-        // the thread's unit: its first element and, of pairs apart, how far their second ones are
-        const int lane = slot / s.units, unit = slot - lane * s.units, apart = IL ? W : p.rot / 2;
+        // the thread's unit: its first element, and how far its second vector is (nowhere, so
+        // that it moves one twice, where an odd number of them is not turned)
+        const int lane = slot / s.units, unit = slot - lane * s.units;
         const bool turned = unit < s.pairs;
         const int e = turned ? unit * (IL ? 2 * W : W) : p.rot + (unit - s.pairs) * W;
+        int apart = !turned ? (s.units - s.pairs) * W : IL ? W : p.rot / 2;
+        if (e + apart >= p.d) apart = 0;
         float c[W], z[W];
         if (turned) {
             const int first = (local * s.pairs + unit) * W;
@@ -85,10 +90,10 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
         auto heads = [&](const Heads &x, bool turn, T *page) {
             const T *in = static_cast<const T *>(x.in) + t * x.ts + lane * x.hs + e;
             T *out = x.out ? static_cast<T *>(x.out) + t * x.o_ts + lane * x.o_hs + e : nullptr;
+            if (APPEND && !turned && out == in && !page) return;  // (queries in place, nothing to turn)
             if (APPEND && page) page += to + lane * p.head_stride + e;
             for (int h = lane; h < x.n; h += s.lanes) {
-                Vec<T, W> a = ld_vec<T, W>(in), b;
-                if (turned) b = ld_vec<T, W>(in + apart);
+                Vec<T, W> a = ld_vec<T, W>(in), b = ld_vec<T, W>(in + apart);
                 in += s.lanes * x.hs;
                 if (turn && turned) {
 #pragma unroll
@@ -103,12 +108,12 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
                 }
                 if (out) {
                     st_vec<T, W>(out, a);
-                    if (turned) st_vec<T, W>(out + apart, b);
+                    st_vec<T, W>(out + apart, b);
                     out += s.lanes * x.o_hs;
                 }
                 if (APPEND && page) {
                     st_vec<T, W>(page, a);
-                    if (turned) st_vec<T, W>(page + apart, b);
+                    st_vec<T, W>(page + apart, b);
                     page += s.lanes * p.head_stride;
                 }
             }
@@ -119,8 +124,9 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
     }
 }
 
-// The widest units (16 bytes of elements, four, two or one): W pairs and W
-// elements of what is not turned, all addresses multiples of W elements.
+// The widest units (16 bytes of elements, four, two or one): W pairs or 2 W
+// elements of what is not turned (nobody's where all is turned in place), all
+// addresses multiples of W elements.
 int width_for(const RotaryParams &p, int bytes) {
     uint64_t at = 0;
     int64_t strides = 0;
@@ -135,7 +141,7 @@ int width_for(const RotaryParams &p, int bytes) {
     }
     for (int w : {16 / bytes, 4, 2}) {
         const int align = w * bytes;
-        if (p.rot / 2 % w == 0 && p.d % w == 0 && at % align == 0 && strides * bytes % align == 0) return w;
+        if (p.rot / 2 % w == 0 && p.rest % w == 0 && at % align == 0 && strides * bytes % align == 0) return w;
     }
     return 1;
 }
@@ -144,7 +150,8 @@ template <typename T, int W, bool APPEND>
 cudaError_t go(const RotaryParams &p, cudaStream_t stream) {
     Shape s;
     s.pairs = p.rot / 2 / W;
-    s.units = s.pairs + (p.d - p.rot) / W;
+    s.units = s.pairs + (p.rest / W + 1) / 2;
+    if (s.units == 0) return cudaSuccess;  // all in place, nothing to turn
     const int heads = std::max(1, p.q.n + p.k.n + p.v.n);
     // A warp a token where there are enough of them to fill the GPU (35507 tokens of 40
     // heads of 128: 117 us; twice as many threads a token 123, half as many 128); with

@@ -40,6 +40,7 @@ struct RotaryParams {
     const int32_t *positions;
     float scale, sign;      // sign -1: by the negative angles
     int rot, interleaved, d, dtype;
+    int rest;               // of a head's elements, those that are moved without turning
     int64_t num_tokens;
     Heads q, k;
     // appending to a layer of the cache (v, slots); slots NULL: only turning

@@ -243,6 +243,8 @@ int csgmv_rotary(const csgmv_rope *rope, int dtype, int head_dim, const int32_t 
     p.rot = rope->rotary_dim;
     p.interleaved = rope->interleaved;
     p.d = head_dim;
+    // (outputs that begin where their inputs do are those)
+    p.rest = (num_q_heads == 0 || q_out == q) && (num_k_heads == 0 || k_out == k) ? 0 : head_dim - rope->rotary_dim;
     p.dtype = dtype;
     p.num_tokens = num_tokens;
     return launched(csgmv::launch_rotary(p, st(stream)), "csgmv_rotary");
@@ -337,6 +339,7 @@ int csgmv_kv_append(const csgmv_kv_cache *kv, int layer, const csgmv_rope *rope,
     p.sign = 1.0f;
     p.positions = positions;
     p.d = d;
+    p.rest = d - p.rot;
     p.dtype = kv->dtype;
     p.num_tokens = num_tokens;
     p.slots = slots;

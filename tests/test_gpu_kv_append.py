@@ -237,6 +237,26 @@ def test_keys_turned_in_place():
     assert torch.equal(rows(c.k_pages, "NHD")[1, slots], k) and torch.equal(rows(c.v_pages, "NHD")[1, slots], v)
 
 
+@pytest.mark.parametrize("rot", [None, 0, 32])
+@pytest.mark.parametrize("keys", [False, True])
+def test_queries_partly_turned_in_place(rot, keys):
+    """What of them is not turned keeps its bits; the keys' is written to the cache."""
+    c, g = make([5, 20, 100], d=128, dtype=HF)
+    n, rope = 30, None if rot is None else B.Rope(128, rotary_dim=rot)
+    turn = rot or 0
+    slots, pos = B.csgmv_kv_extend(c, ints([0, 10, 11, 30]), n)
+    q, k, v = (torch.randn((n, h, 128), generator=g).to(HF).cuda() for h in (4, 2, 2))
+    q.view(torch.int16)[..., turn:] = torch.randint(-2 ** 15, 2 ** 15, (n, 4, 128 - turn), generator=g, dtype=torch.int16).cuda()
+    was = q.clone(), k.clone(), v.clone()
+    B.csgmv_kv_append(c, 0, k, v, slots, pos, rope=rope, q=q, k_out=k if keys else None)
+    for x, y in ((was[0], q), (was[1], rows(c.k_pages, "HND")[0, slots])):
+        if turn:
+            close(y[..., :turn], *(t[..., :turn] for t in rotary(x.nan_to_num(), pos, rope.freq, turn, False)))
+        assert torch.equal(y.view(torch.int16)[..., turn:], x.view(torch.int16)[..., turn:])
+    assert torch.equal(k, rows(c.k_pages, "HND")[0, slots] if keys else was[1])
+    assert torch.equal(v, was[2]) and torch.equal(rows(c.v_pages, "HND")[0, slots], v)
+
+
 def test_many_requests_and_empty_ones():
     lens = [i % 37 for i in range(700)]
     c, g = make(lens, ps=8, layers=1, heads=1, d=8, spare=700)

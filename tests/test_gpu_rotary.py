@@ -69,6 +69,34 @@ def test_slices_of_one_projection(n, off, dtype):
     assert torch.equal(wide, was)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(128, 32), (80, 20), (72, 64), (70, 32), (64, 0)])
+def test_parts_of_heads_in_place_and_apart(dtype, interleaved, d, rot):
+    """Queries in place with keys apart, keys in place with queries apart, or
+    queries alone: what is not turned keeps its bits, whatever they are."""
+    g = torch.Generator().manual_seed(d + rot)
+    n, rope = 130, B.Rope(d, rotary_dim=rot, interleaved=interleaved)
+    pos = positions(g, n, 30000)
+    bits = torch.int16 if dtype is BF else torch.int32
+    for q_apart, k_apart in ((False, True), (True, False), (False, None), (False, False)):
+        q, k = draw(g, (n, 6, d), dtype), draw(g, (n, 3, d), dtype)
+        for x in (q, k):
+            x.view(bits)[..., rot:] = torch.randint(-2 ** 15, 2 ** 15, (n, x.shape[1], d - rot), generator=g, dtype=bits).cuda()
+        was = q.clone(), k.clone()
+        qo, ko = torch.empty_like(q) if q_apart else q, torch.empty_like(k) if k_apart else k
+        B.csgmv_rotary(rope, pos, q, None if k_apart is None else k, q_out=qo, k_out=None if k_apart is None else ko)
+        for x, y, turned in ((was[0], qo, True), (was[1], ko, k_apart is not None)):
+            if turned:
+                close(y[..., :rot], *(t[..., :rot] for t in rotary(x.nan_to_num(), pos, rope.freq, rot, interleaved)))
+                assert torch.equal(y.view(bits)[..., rot:], x.view(bits)[..., rot:])
+            else:
+                assert torch.equal(y.view(bits), x.view(bits))
+        for x, y, apart in ((was[0], q, q_apart), (was[1], k, k_apart)):
+            if apart:
+                assert torch.equal(x.view(bits), y.view(bits))
+
+
 def test_heads_outside_the_tokens():
     """(heads, tokens, d) seen as (tokens, heads, d); a head broadcast over many."""
     g = torch.Generator().manual_seed(2)
