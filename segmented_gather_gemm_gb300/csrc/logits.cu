@@ -16,7 +16,7 @@
 // The CTAs of a row exchange a pair of numbers a warp between the passes.
 //
 // Measured (device time): 768 bf16 rows of 128256 (64 drafted trees with counts,
-// biases, a quarter of them with masks; 595 MB) 161 us; without any rule 108 us, 5.5
+// biases, a quarter of them with masks; 595 MB) 158 us; without any rule 108 us, 5.5
 // TB/s.  256 f32 rows of 100003 69 us, without rules 50 us.  A row's chain of dependent
 // loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
 // sparse) is hidden by five CTAs an SM, three with f32: what holds it up is room
@@ -343,9 +343,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(Logi
                 }
     };
     auto vector = [&](int i, float (&x)[W]) {
-        const Vec<T, W> v = *reinterpret_cast<const Vec<T, W> *>(z + i);
-#pragma unroll
-        for (int e = 0; e < W; ++e) x[e] = to_f32(v.e[e]);
+        widen(*reinterpret_cast<const Vec<T, W> *>(z + i), x);
     };
     // out = f(score, token), in vectors where those of out are where those of z are
     // and no score waits in out

@@ -192,3 +192,79 @@ def test_rows_past_32_bits_of_elements():
     assert torch.equal(out[-2], torch.ones(D, dtype=BF, device="cuda"))
     want = torch.where(torch.arange(D, device="cuda") % 2 == 0, -3.0, 1.0).double() / 5 ** 0.5
     close(out[-1], want, 2.0 ** -17)
+
+
+def laid_out(g, n, D, dtype, std=1.0, gap=0, shift=0):
+    """Rows of D in a wider tensor of NaN that begin `shift` behind its boundary."""
+    wide = torch.full((n * (D + gap) + 16,), float("nan"), dtype=dtype, device="cuda")
+    rows = wide[shift:shift + n * (D + gap)].view(n, D + gap)[:, :D]
+    rows.copy_(draw(g, (n, D), dtype, std))
+    return wide, rows
+
+
+# (rows, width, dtype, residual, post, pre, gate, gap, shift): several rows to a CTA, its
+# inputs asked for while the one before is worked on, and the same rows one by one
+MANY = [
+    (2500, 4096, BF, BF, "none", "rms", None, 0, 0),
+    (2501, 4104, HF, HF, "layer", "none", None, 8, 0),
+    (700, 8200, BF, F32, "rms", "layer", None, 0, 0),
+    (615, 16384, HF, HF, "rms", "rms", "column", 0, 0),
+    (1300, 10008, BF, None, "none", "layer", None, 8, 8),
+    (1300, 6144, BF, BF, "none", "rms", None, 0, 0),
+    (5000, 513, BF, F32, "layer", "layer", "token", 0, 0),
+    (2500, 1001, HF, HF, "none", "rms", "column", 0, 3),
+    (900, 4097, BF, BF, "rms", "layer", "token", 0, 0),
+    (900, 4096, BF, BF, "none", "rms", "token", 5, 1),
+    (470, 16371, BF, F32, "none", "rms", "token", 0, 5),
+    (900, 4097, F32, F32, "rms", "rms", "token", 0, 0),
+    (40001, 40, BF, BF, "none", "layer", "column", 0, 0),
+    (9001, 129, HF, F32, "rms", "rms", "token", 0, 0),
+    (9001, 128, BF, BF, "none", "rms", None, 0, 0),
+    (3001, 7, F32, F32, "none", "layer", "token", 0, 0),
+]
+
+
+@pytest.mark.parametrize("n,D,dtype,rtype,post,pre,gate,gap,shift", MANY)
+def test_many_rows(n, D, dtype, rtype, post, pre, gate, gap, shift):
+    """What lies before, between and behind the rows is NaN, and stays; some rows hold
+    one, which stays in its row."""
+    g = torch.Generator().manual_seed(n + D)
+    xw, x = laid_out(g, n, D, dtype, gap=gap, shift=shift)
+    x[5::97, D - 1], x[6::97, 0] = float("nan"), float("inf")
+    rw, r = laid_out(g, n, D, rtype, 3.0, gap=gap, shift=shift) if rtype else (None, None)
+    gw, gt = (None, None) if gate is None else laid_out(g, 1 if gate == "column" else n, D, dtype, gap=gap, shift=shift)
+    pre, pre_ref = side(g, pre, D, dtype, D % 3 == 0)
+    post, post_ref = side(g, post, D, dtype, D % 2 == 1)
+    ow, out = laid_out(g, n, D, dtype, gap=gap, shift=shift)
+    aw, after = laid_out(g, n, D, rtype or dtype, gap=gap, shift=shift)
+    B.csgmv_add_norm(x, pre, out, residual=r, residual_out=after, post_norm=post, gate=gt, residual_scale=0.75)
+    want = add_norm(x, r, gt, post_ref, pre_ref, 0.75)
+    check(after, out, want, rtype or dtype)
+    once = out.clone(), after.clone()
+    for wide, rows in ((ow, out), (aw, after)):
+        rows.fill_(float("nan"))
+        assert bool(torch.isnan(wide).all())
+    # single rows, and rows in place of the inputs
+    for k in (0, 1, n // 2, n - 1):
+        one = slice(k, k + 1)
+        B.csgmv_add_norm(x[one], pre, out[one], residual=None if r is None else r[one], residual_out=after[one], post_norm=post,
+                         gate=gt if gate != "token" else gt[one], residual_scale=0.75)
+        check(after[one], out[one], [(v[one], t[one]) for v, t in want], rtype or dtype)
+    if r is not None:
+        B.csgmv_add_norm(x, pre, x, residual=r, post_norm=post, gate=gt, residual_scale=0.75)
+        assert torch.equal(x.nan_to_num(), once[0].nan_to_num()) and torch.equal(r.nan_to_num(), once[1].nan_to_num())
+
+
+@pytest.mark.parametrize("D", [4096, 4097])
+def test_one_row_of_an_input_for_many(D):
+    """A stride of 0, where several rows come to a CTA one behind the other."""
+    g = torch.Generator().manual_seed(D)
+    n, none = 2600, ("none", None, None, EPS)
+    pre, ref = side(g, "rms", D, BF, False)
+    one, many = draw(g, (D + 3,), BF), draw(g, (n, D), BF)
+    for off in (0, 3) if D % 8 else (0,):
+        row = one[off:off + D].view(1, D).expand(n, D)
+        for x, r in ((row, many), (many, row)):
+            after = torch.empty((n, D), dtype=BF, device="cuda")
+            out = B.csgmv_add_norm(x, pre, residual=r, residual_out=after)
+            check(after, out, add_norm(x, r, None, none, ref, 1.0), BF)
