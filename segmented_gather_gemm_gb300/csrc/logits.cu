@@ -19,7 +19,7 @@
 // biases, a quarter of them with masks; 595 MB) 158 us; without any rule 108 us, 5.5
 // TB/s.  256 f32 rows of 100003 69 us, without rules 50 us.  A row's chain of dependent
 // loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
-// sparse) is hidden by five CTAs an SM, three with f32: what holds it up is room
+// sparse) is hidden by five CTAs an SM, f32 four (long rows three): what holds it up is room
 // for more of them.  (Also tried: scores in f32 shared memory, three CTAs an SM,
 // 286 us; the row read again from L2 with a test for each vector, 210 us; the list
 // in the order of the vocabulary by prefix sums, 172 us; 128 to 512 threads, 165 to
@@ -113,7 +113,7 @@ __device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch
 __device__ __forceinline__ bool has(const uint32_t *bits, int i) { return (bits[i >> 5] >> (i & 31) & 1u) != 0; }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 3) process(LogitParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process(LogitParams p) {
     extern __shared__ uint4 dynamic[];
     __shared__ Smem sm;
     constexpr int W = 16 / (int)sizeof(T);  // elements of a vector
