@@ -56,10 +56,9 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
         const int token = i / (s.pairs * W);
         if (t0 + token >= p.num_tokens) break;
         const uint64_t pos = (uint64_t)(int64_t)p.positions[t0 + token];
-        // modulo a whole turn; the upper half, 2^-32 turns, is more than f32 holds of it
-        const int turn = (int)(pos * p.turns[i - token * (s.pairs * W)] >> 32);
+        const int64_t turn = (int64_t)(pos * p.turns[i - token * (s.pairs * W)]);  // 2^-64 turns, modulo a whole one
         float sn, cs;
-        sincospif((float)turn * 0x1p-31f, &sn, &cs);
+        sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
         cosines[i] = cs * p.scale;
         sines[i] = sn * p.scale * p.sign;
     }
