@@ -132,6 +132,20 @@ def test_far_and_negative_positions():
     close(a[:1], a[1:], tol)
 
 
+def test_small_angles_keep_their_bits():
+    """Of a pair (0, 1) a small angle's sine is left: an angle in f32 and a sine of two
+    units in the last place, 2^-21 of it, however small (2^-64 turns: a radian is
+    2^61.3 of them)."""
+    f = torch.tensor([2.0 ** -k for k in range(2, 34)], dtype=torch.float64)
+    rope = B.Rope(64, freq=f)
+    x = torch.zeros((3, 1, 64), dtype=F32, device="cuda")
+    x[..., 32:] = 1.0
+    pos = torch.tensor([1, -1, 3], dtype=torch.int32, device="cuda")
+    B.csgmv_rotary(rope, pos, x)
+    want = -torch.sin(pos.double().cpu()[:, None] * f)
+    close(x[:, 0, :32], want, 2.0 ** -21 * want.abs() + 2.0 ** -61)
+
+
 def test_the_inverse_is_the_gradient():
     """<g, R x> = <R^T g, x>, and turning there and back is scale^2."""
     g = torch.Generator().manual_seed(6)
