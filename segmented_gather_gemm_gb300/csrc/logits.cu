@@ -17,9 +17,9 @@
 //
 // Measured (device time): 768 bf16 rows of 128256 (64 drafted trees with counts,
 // biases, a quarter of them with masks; 595 MB) 158 us; without any rule 108 us, 5.5
-// TB/s.  256 f32 rows of 100003 69 us, without rules 50 us.  A row's chain of dependent
+// TB/s.  256 f32 rows of 100003 63 us, without rules 45 us.  A row's chain of dependent
 // loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
-// sparse) is hidden by five CTAs an SM, f32 four (long rows three): what holds it up is room
+// sparse) is hidden by five CTAs an SM, f32 four (three above 102400 tokens): what holds it up is room
 // for more of them.  (Also tried: scores in f32 shared memory, three CTAs an SM,
 // 286 us; the row read again from L2 with a test for each vector, 210 us; the list
 // in the order of the vocabulary by prefix sums, 172 us; 128 to 512 threads, 165 to
@@ -37,11 +37,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBranch = 32 * kTreeMaxWords;
 constexpr int kPrompt = 1 << 30;
 constexpr int kMaxVocab = 1 << 18, kMaxCtas = 8;
 constexpr int kBlock = 512;  // elements; blocks of a row go to its CTAs in turn
-constexpr int kKept = 1024;  // scores in a CTA's list; further ones wait in out
+// Scores in a CTA's list; further ones wait in out.  f32 has fewer, and room for a
+// branch only where there is one: that lets a fourth CTA on an SM with rows of 100000 (256
+// of them 45 us, else 51).
+template <typename T>
+constexpr int kKeptOf = sizeof(T) == 2 ? 1024 : 512;
 constexpr float kLargest = 3.402823466e+38f;
 
 // A part of a row: its largest score, and the sum of 2^((z - top) heat), which
@@ -50,10 +53,11 @@ struct Part {
     float top, sum;
     int at;  // temperature 0: the lowest place of top
 };
+template <typename T>
 struct Smem {
-    int branch[kMaxBranch];
-    float kept[kKept];
-    uint16_t place[kKept];
+    int branch[sizeof(T) == 2 ? 32 * kTreeMaxWords : 1];
+    float kept[kKeptOf<T>];
+    uint16_t place[kKeptOf<T>];
     int n_branch, n_kept;
     uint32_t drawn[32], biased[32];  // bits of the branch's and the biases' places modulo 1024
     float most[kWarps];
@@ -61,11 +65,12 @@ struct Smem {
     int list_at, lost;
     Part parts[kMaxCtas * (kWarps + 1)];  // of the row: each CTA's warps, and its list
 };
-// Shared memory of a CTA's blocks of a row: the elements, and a bit for each.
+// Shared memory of a CTA's blocks of a row: the elements, a bit for each, and (f32) the
+// tokens of the row's branch.
 struct Share {
-    int elements, words;  // bytes, and words of bits
+    int elements, words, branch;  // bytes, words of bits, tokens
 };
-__host__ __device__ inline Share share_of(int chunk, int bytes) { return {chunk * bytes, chunk >> 5}; }
+__host__ __device__ inline Share share_of(int chunk, int bytes, int mask_words) { return {chunk * bytes, chunk >> 5, bytes == 2 ? 0 : 32 * mask_words}; }
 
 // 2^x to two units in the last place, what is below 2^-126 as 0.
 __device__ __forceinline__ float ex2(float x) {
@@ -115,11 +120,13 @@ __device__ __forceinline__ bool has(const uint32_t *bits, int i) { return (bits[
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process(LogitParams p) {
     extern __shared__ uint4 dynamic[];
-    __shared__ Smem sm;
+    __shared__ Smem<T> sm;
+    constexpr int kKept = kKeptOf<T>;
     constexpr int W = 16 / (int)sizeof(T);  // elements of a vector
-    const Share shape = share_of(p.chunk, sizeof(T));
+    const Share shape = share_of(p.chunk, sizeof(T), p.mask_words);
     T *z = reinterpret_cast<T *>(dynamic);
     uint32_t *set = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(dynamic) + shape.elements);
+    int *tokens = sizeof(T) == 2 ? sm.branch : reinterpret_cast<int *>(set + shape.words);  // of the branch
     griddep_launch_dependents();
     cluster_arrive();
     griddep_wait();
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process(Logi
                 }
             }
             const unsigned m = __ballot_sync(kFullMask, v >= 0);
-            if (v >= 0) sm.branch[k + __popc(m & ((1u << lane) - 1u))] = v;
+            if (v >= 0) tokens[k + __popc(m & ((1u << lane) - 1u))] = v;
             k += __popc(m);
         }
         if (lane == 0) sm.n_branch = k;
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process(Logi
         };
         const int k = branch ? sm.n_branch : 0;
         for (int i = tid; i < k; i += kThreads)
-            if (const int at = place(sm.branch[i]); at >= 0) {
+            if (const int at = place(tokens[i]); at >= 0) {
                 atomicOr(&sm.drawn[at >> 5 & 31], 1u << (at & 31));
                 take(at);
             }
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process(Logi
             int more = 0;
             if (branch && (sm.drawn[at >> 5 & 31] >> (at & 31) & 1u)) {
                 const int k = sm.n_branch;
-                for (int j = 0; j < k; ++j) more += sm.branch[j] == v;
+                for (int j = 0; j < k; ++j) more += tokens[j] == v;
             }
             y = penalized(y, word, more, rho, alpha, beta);
         }
@@ -588,9 +595,9 @@ int chunk_of(int vocab, int ctas, int bytes) {
     const int blocks = (16 / bytes - 1 + vocab + kBlock - 1) / kBlock;
     return (blocks + ctas - 1) / ctas * kBlock;
 }
-size_t smem_of(int chunk, int bytes) {
-    const Share s = share_of(chunk, bytes);
-    return (size_t)s.elements + 4 * (size_t)s.words;
+size_t smem_of(int chunk, int bytes, int mask_words) {
+    const Share s = share_of(chunk, bytes, mask_words);
+    return (size_t)s.elements + 4 * (size_t)s.words + 4 * (size_t)s.branch;
 }
 
 cudaError_t prepare() {
@@ -602,7 +609,7 @@ cudaError_t prepare() {
                                                          {reinterpret_cast<const void *>(process<__half>), 2},
                                                          {reinterpret_cast<const void *>(process<float>), 4}};
     for (const auto &f : all) {
-        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(chunk_of(kMaxVocab, kMaxCtas, f.bytes), f.bytes))) !=
+        if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(chunk_of(kMaxVocab, kMaxCtas, f.bytes), f.bytes, kTreeMaxWords))) !=
             cudaSuccess)
             return e;
         if ((e = cudaFuncSetAttribute(f.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -622,7 +629,7 @@ cudaError_t go(LogitParams p, cudaStream_t stream) {
     while (ctas < kMaxCtas && ((int64_t)p.vocab > (int64_t)ctas * 16384 || (p.num_tokens * ctas * 2 <= 152 && p.vocab > ctas * 2048)))
         ctas *= 2;
     p.chunk = chunk_of(p.vocab, ctas, (int)sizeof(T));
-    return launch_kernel(process<T>, dim3((unsigned)(p.num_tokens * ctas)), kThreads, smem_of(p.chunk, sizeof(T)), stream, ctas, true, p);
+    return launch_kernel(process<T>, dim3((unsigned)(p.num_tokens * ctas)), kThreads, smem_of(p.chunk, sizeof(T), p.mask_words), stream, ctas, true, p);
 }
 
 }  // namespace
