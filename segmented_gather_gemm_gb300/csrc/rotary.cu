@@ -9,14 +9,15 @@
 // shared memory.  A thread owns W neighbouring pairs (two vectors of W elements, or
 // one of 2 W where pairs lie side by side) of one token in some of its heads.  What is not
 // turned is moved two vectors at a time too, or, in place, not touched.  One
-// head at a time: more loads under way a thread take registers from the warps that
-// hide them (four heads: 220 us where one takes 117).
+// head at a time, its angles from shared memory: more loads under way a thread, or
+// angles in registers, take room from the warps that hide loads (four heads: 220 us
+// where one takes 117, angles in shared memory 113; six CTAs an SM spill: 116).
 //
-// Measured (device time): 35507 tokens of 32 + 8 heads of 128, bf16 (727 MB) 117 us,
-// 6.2 TB/s; with values into a layer's pages, 35700 tokens in half (880 MB) 142 us;
-// 12 tokens 3.0 us, a launch and two rounds of loads.  With 32 of the 128 turned 116 us
+// Measured (device time): 35507 tokens of 32 + 8 heads of 128, bf16 (727 MB) 113 us,
+// 6.4 TB/s; with values into a layer's pages, 35700 tokens in half (880 MB) 136 us;
+// 12 tokens 3.0 us, a launch and two rounds of loads.  With 32 of the 128 turned 113 us
 // (149 by single vectors of the rest), 53 in place.  What bounds the large ones is
-// HBM (DRAM 75 to 77 % busy by the counters).
+// HBM; where a token has few heads (one of each: 2.5 TB/s) its angles.
 #include "elements.cuh"
 #include "serving.cuh"
 #include "step.h"
@@ -33,8 +34,37 @@ struct Shape {
     int units, pairs, lanes, slots, tokens;
 };
 
+// n floats of shared memory, read where they are used each time (in registers from
+// head to head they take room from the warps that hide the loads).
+template <int n>
+__device__ __forceinline__ void shared_floats(float (&x)[n], const float *p) {
+    const uint32_t at = smem_u32(p);
+    if constexpr (n == 4) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at));
+    else if constexpr (n == 2) asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(at));
+    else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[0]) : "r"(at));
+}
+// W pairs: elements i of both vectors, or neighbours in the two laid end to end.
+template <typename T, int W, bool IL>
+__device__ __forceinline__ void turn_pairs(Vec<T, W> &a, Vec<T, W> &b, const float *cosines, const float *sines) {
+    constexpr int G = W < 4 ? W : 4;
+#pragma unroll
+    for (int i0 = 0; i0 < W; i0 += G) {
+        float c[G], z[G];
+        shared_floats(c, cosines + i0), shared_floats(z, sines + i0);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int i = i0 + j;
+            T &u = IL ? (2 * i < W ? a.e[(2 * i) % W] : b.e[(2 * i) % W]) : a.e[i];
+            T &v = IL ? (2 * i + 1 < W ? a.e[(2 * i + 1) % W] : b.e[(2 * i + 1) % W]) : b.e[i];
+            const float uf = to_f32(u), vf = to_f32(v);
+            u = from_f32<T>(uf * c[j] - vf * z[j]);
+            v = from_f32<T>(uf * z[j] + vf * c[j]);
+        }
+    }
+}
+
 template <typename T, int W, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams p, Shape s) {
+__global__ void __launch_bounds__(kThreads, 5) rotary(RotaryParams p, Shape s) {
     extern __shared__ float4 angles4[];
     float *cosines = reinterpret_cast<float *>(angles4), *sines = cosines + s.tokens * s.pairs * W;
     griddep_launch_dependents();
@@ -72,20 +102,7 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
         const int e = turned ? unit * (IL ? 2 * W : W) : p.rot + (unit - s.pairs) * W;
         int apart = !turned ? (s.units - s.pairs) * W : IL ? W : p.rot / 2;
         if (e + apart >= p.d) apart = 0;
-        float c[W], z[W];
-        if (turned) {
-            const int first = (local * s.pairs + unit) * W;
-            if constexpr (W % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < W; i += 4) {
-                    *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(cosines + first + i);
-                    *reinterpret_cast<float4 *>(z + i) = *reinterpret_cast<const float4 *>(sines + first + i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) c[i] = cosines[first + i], z[i] = sines[first + i];
-            }
-        }
+        const int first = turned ? (local * s.pairs + unit) * W : 0;
         // the unit in heads lane, lane + lanes, ... of a tensor, to up to two places
         auto heads = [&](const Heads &x, bool turn, T *page) {
             const T *in = static_cast<const T *>(x.in) + t * x.ts + lane * x.hs + e;
@@ -95,17 +112,7 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 4 : 5) rotary(RotaryParams 
             for (int h = lane; h < x.n; h += s.lanes) {
                 Vec<T, W> a = ld_vec<T, W>(in), b = ld_vec<T, W>(in + apart);
                 in += s.lanes * x.hs;
-                if (turn && turned) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        // pair i: elements i of both, or neighbours in the two vectors laid end to end
-                        T &u = IL ? (2 * i < W ? a.e[(2 * i) % W] : b.e[(2 * i) % W]) : a.e[i];
-                        T &v = IL ? (2 * i + 1 < W ? a.e[(2 * i + 1) % W] : b.e[(2 * i + 1) % W]) : b.e[i];
-                        const float uf = to_f32(u), vf = to_f32(v);
-                        u = from_f32<T>(uf * c[i] - vf * z[i]);
-                        v = from_f32<T>(uf * z[i] + vf * c[i]);
-                    }
-                }
+                if (turn && turned) turn_pairs<T, W, IL>(a, b, cosines + first, sines + first);
                 if (out) {
                     st_vec<T, W>(out, a);
                     st_vec<T, W>(out + apart, b);
