@@ -888,8 +888,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | No
       ("yarn", factor, original[, fast = 32, slow = 1])
                               pairs from the one that makes `fast` turns in the
                               original context to the one that makes `slow` are
-                              blended along their index; the turned part is
-                              multiplied by 0.1 ln(factor) + 1"""
+                              blended along their index (the ramp may end behind
+                              the last pair, at rotary_dim - 1 at most); the turned
+                              part is multiplied by 0.1 ln(factor) + 1"""
     _need(rotary_dim >= 0 and rotary_dim % 2 == 0, f"rotary_dim {rotary_dim} must be even and not negative")
     _need(base > 0, "base must be positive")
     n = rotary_dim // 2
@@ -919,7 +920,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | No
 
     def pair(turns):
         return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
-    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), n - 1)
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
     blend = ((i - lo) / max(hi - lo, 0.001)).clamp(0.0, 1.0)
     return f * (1 - blend) + f / factor * blend, 0.1 * math.log(factor) + 1.0
 
