@@ -697,7 +697,8 @@ typedef struct csgmv_rope {
 } csgmv_rope;
 
 /* turns[i] = round(2^64 * freq[i] / (2 pi)) modulo 2^64 (freq in radians a
- * position, finite).  Host only. */
+ * position, finite), rounded once; 2 pi is the double next to it, which is off by
+ * 2^-54 of it, less than a double's own rounding.  -freq gives -turns.  Host only. */
 CSGMV_API int csgmv_rope_turns(const double *freq, int n, uint64_t *turns);
 
 /*

@@ -200,10 +200,20 @@ int csgmv_rope_turns(const double *freq, int n, uint64_t *turns) {
     if (n > 0 && (!freq || !turns)) return fail(CSGMV_ERR_INVALID_ARG, "freq / turns is NULL");
     for (int i = 0; i < n; ++i)
         if (!std::isfinite(freq[i])) return fail(CSGMV_ERR_INVALID_ARG, "freq[%d] is not finite", i);
+    constexpr double whole = 6.283185307179586476925286766559;
     for (int i = 0; i < n; ++i) {
-        const double turn = freq[i] / 6.283185307179586476925;
-        const double steps = std::nearbyint(std::ldexp(turn - std::floor(turn), 64));
-        turns[i] = steps < 0x1p64 ? (uint64_t)steps : 0;  // (a whole turn is none)
+        // what is left of whole turns, a bit of its quotient at a time: every step is exact
+        double rest = std::fmod(std::fabs(freq[i]), whole);
+        uint64_t steps = 0;
+        auto bit = [&] {
+            rest += rest;
+            const bool one = rest >= whole;
+            if (one) rest -= whole;
+            return one;
+        };
+        for (int k = 0; k < 64; ++k) steps = 2 * steps + bit();
+        steps += bit();  // the nearest one (a whole turn is none)
+        turns[i] = freq[i] < 0 ? 0 - steps : steps;
     }
     return CSGMV_OK;
 }

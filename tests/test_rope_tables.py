@@ -1,6 +1,7 @@
 """Tables of rotary positions against their formulas, written out in Python numbers:
-scaled frequencies.  CPU only: no kernel runs."""
+scaled frequencies, and frequencies as parts of a turn.  CPU only: no kernel runs."""
 import math
+from fractions import Fraction
 
 import pytest
 
@@ -52,3 +53,38 @@ def test_pairs_that_all_turn_fast_are_kept():
     """Where the ramp would begin behind all pairs, none is stretched."""
     for rot, base, original in ((4, 10.0, 1 << 20), (8, 2.0, 1 << 20), (2, 100.0, 1 << 20)):
         assert B.rope_frequencies(rot, base, ("yarn", 4.0, original))[0].tolist() == B.rope_frequencies(rot, base)[0].tolist()
+
+
+def turns(*freq):
+    return [t % 2 ** 64 for t in B.csgmv_rope_turns(list(freq)).tolist()]
+
+
+TURN = Fraction(2 * math.pi)  # the double next to 2 pi, as a whole turn
+# 2 pi to 60 decimal places
+TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+FREQ = [1.0, 0.3, 1e-6, 2.0 ** -40 / 3, 2.0 ** -63, 5e-324, 3.0, 6.283185307179586, 6.283185307179587, 12.566, 1e5 / 3, 2.0 ** 53 + 2,
+        1e300 / 7] + [10000.0 ** (-2 * i / 128) for i in range(64)] + [500000.0 ** (-2 * i / 128) for i in range(64)]
+
+
+def test_turns_are_rounded_once():
+    for f in FREQ:
+        whole = 2 ** 64 * Fraction(f) / TURN
+        want = math.floor(whole + Fraction(1, 2)) % 2 ** 64  # (none of these lies between two)
+        assert turns(f) == [want], f
+
+
+def test_turns_of_negative_frequencies():
+    """They are those of the positive ones, the other way round, to the last bit."""
+    up, down = turns(*FREQ), turns(*[-f for f in FREQ])
+    assert [(a + b) % 2 ** 64 for a, b in zip(up, down)] == [0] * len(FREQ)
+
+
+def test_turns_keep_the_bits_of_a_frequency():
+    """The double that stands for a turn is off by 2^-54 of it, less than a
+    frequency's own rounding: so is every frequency below a turn."""
+    for f in FREQ:
+        if f < 6:
+            exact = 2 ** 64 * Fraction(f) / TWO_PI
+            for way in (1, -1):
+                off = (turns(way * f)[0] - way * exact) % 2 ** 64  # (up to whole turns)
+                assert min(off, 2 ** 64 - off) <= exact / 2 ** 54 + Fraction(1, 2), f
