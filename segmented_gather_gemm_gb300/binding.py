@@ -892,7 +892,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | No
                               the last pair, at rotary_dim - 1 at most); the turned
                               part is multiplied by 0.1 ln(factor) + 1"""
     _need(rotary_dim >= 0 and rotary_dim % 2 == 0, f"rotary_dim {rotary_dim} must be even and not negative")
-    _need(base > 0, "base must be positive")
+    _need(0 < base < math.inf, "base must be positive and finite")
     n = rotary_dim // 2
     i = torch.arange(n, dtype=torch.float64)
     if n == 0:
@@ -902,8 +902,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | No
         return f, 1.0
     kind, more = scaling[0], scaling[1:]
     lengths = {"linear": (1,), "ntk": (1,), "wavelength": (4,), "yarn": (2, 4)}
-    _need(kind in lengths and len(more) in lengths[kind] and all(v > 0 for v in more),
-          f"scaling {scaling!r} is none of those that are known, or not positive")
+    _need(kind in lengths and len(more) in lengths[kind] and all(0 < v < math.inf for v in more),
+          f"scaling {scaling!r} is none of those that are known, or not positive and finite")
     factor = float(more[0])
     if kind == "linear":
         return f / factor, 1.0
@@ -915,8 +915,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: tuple | No
         _need(high > low, "wavelength scaling needs low < high")
         keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
         return f * (keep + (1 - keep) / factor), 1.0
-    _need(base != 1.0, "yarn scaling needs a base other than 1")
     original, (fast, slow) = more[1], more[2:] or (32.0, 1.0)
+    _need(base > 1.0 and fast >= slow, "yarn scaling needs a base above 1 and fast >= slow")
 
     def pair(turns):
         return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))

@@ -88,3 +88,12 @@ def test_turns_keep_the_bits_of_a_frequency():
             for way in (1, -1):
                 off = (turns(way * f)[0] - way * exact) % 2 ** 64  # (up to whole turns)
                 assert min(off, 2 ** 64 - off) <= exact / 2 ** 54 + Fraction(1, 2), f
+
+
+@pytest.mark.parametrize("base,scaling", [
+    (10000.0, ("yarn", 4.0, 8192, 1.0, 32.0)), (0.5, ("yarn", 4.0, 8192)), (1.0, ("yarn", 4.0, 8192)), (10000.0, ("yarn", 4.0, math.inf)),
+    (10000.0, ("yarn", math.nan, 8192)), (10000.0, ("linear", math.inf)), (math.inf, None), (math.nan, None), (0.0, None)])
+def test_scalings_that_are_refused(base, scaling):
+    """What makes no ramp, or one that runs backwards."""
+    with pytest.raises(B.CsgmvError):
+        B.rope_frequencies(64, base, scaling)
