@@ -477,7 +477,7 @@ CSGMV_API int64_t csgmv_kv_scratch_ints(int num_pages, int max_seqs);
  * A request with a bad slot, length or node number, or without room in its
  * row of the page table, is left out; when the free pages do not suffice for
  * the whole batch nothing is appended at all (CSGMV_KV_STATUS_CAPACITY).
- * A sequence may appear once in a batch.  bs <= max_seqs.  The lists may not lie
+ * A sequence may appear once in a batch.  bs <= max_seqs, accept_width <= 2^30.  The lists may not lie
  * in the cache's bookkeeping or scratch (nor csgmv_kv_fork's).
  */
 CSGMV_API int csgmv_kv_commit(const csgmv_kv_cache *kv, const void *k_new, const void *v_new, int64_t new_layer_stride,
@@ -625,7 +625,7 @@ CSGMV_API int csgmv_build_draft_tree(const int32_t *parents, const int32_t *tree
  * path is longer than accept_width (CSGMV_KV_STATUS_CAPACITY), gets accept_len
  * = 0 and next_token = -1; one whose last distribution has no mass (BAD_TOKEN)
  * next_token = -1 only.
- * 1 <= vocab_size <= 2^18.  No output may overlap an input.
+ * 1 <= vocab_size <= 2^18, accept_width <= 2^30.  No output may overlap an input.
  */
 CSGMV_API int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const float *draft_probs,
                                   int64_t draft_stride, const int32_t *draft_tokens, const int32_t *tree_indptr,
@@ -789,7 +789,7 @@ typedef struct csgmv_token_counts {
  * prompt 1: they are the sequence's prompt.  A sequence may come several times,
  * and so may a token.  A request with a bad sequence, length or node is left out;
  * a token outside the vocabulary is (CSGMV_KV_STATUS_BAD_TOKEN).  A sequence may
- * give a token at most 2^30 - 1 times.
+ * give a token at most 2^30 - 1 times.  accept_width <= 2^30.
  */
 CSGMV_API int csgmv_count_tokens(const csgmv_token_counts *counts, const int32_t *tokens, int64_t num_tokens,
                                  const int32_t *tree_indptr, const int32_t *accept_index, int accept_width,
@@ -812,7 +812,8 @@ CSGMV_API int csgmv_count_fork(const csgmv_token_counts *counts, const int32_t *
  *                 temperature >= 0, both finite, none NaN
  *   bias_tokens, bias_values   entries [bias_indptr[b], bias_indptr[b+1]) are
  *                 request b's, in increasing order of their tokens (a token may
- *                 come again: the values are added in turn); bias_total entries in all
+ *                 come again: the values are added in turn); bias_total entries in all, at
+ *                 most 2^30
  *   allow         [num_allow][allow_words]: bit v % 32 of word v / 32 lets token v
  *                 through; allow_words >= vocab_size / 32, rounded up
  *   allow_index   [num_tokens]: the row of allow for each row of logits, or -1
@@ -856,7 +857,7 @@ typedef struct csgmv_logit_rules {
  * with a bad allow_index, is left out: its rows of out stay as they are, and so do
  * those of no request.  A drafted token or a bias outside the vocabulary counts
  * for nothing (CSGMV_KV_STATUS_BAD_TOKEN).
- * 1 <= vocab_size <= 2^18, mask_words <= 8, num_tokens < 2^24.
+ * 1 <= vocab_size <= 2^18, mask_words <= 8, num_tokens < 2^24, bs <= 2^30.
  */
 CSGMV_API int csgmv_process_logits(const void *logits, int dtype, int64_t logits_stride, const int32_t *tree_indptr,
                                    const int32_t *seq_slots, int bs, int64_t num_tokens, int vocab_size,

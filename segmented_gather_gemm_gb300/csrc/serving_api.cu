@@ -22,6 +22,7 @@ int csgmv_kv_commit(const csgmv_kv_cache *kv, const void *k_new, const void *v_n
     if (bs == 0) return CSGMV_OK;
     if (!accept_len || !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "accept_len / tree_indptr is NULL");
     if (accept_index && accept_width <= 0) return fail(CSGMV_ERR_INVALID_ARG, "accept_width must be positive");
+    if (accept_index && accept_width > kMaxList) return fail(CSGMV_ERR_UNSUPPORTED, "accept_width exceeds 2^30");
     if (num_tokens == 0) return CSGMV_OK;
     if ((rc = check_new(k_new, v_new, new_token_stride, new_head_stride))) return rc;
     if (new_layer_stride % 8 || new_layer_stride < 0)
@@ -208,6 +209,7 @@ int csgmv_verify_drafts(const float *target_probs, int64_t target_stride, const 
     if (vocab_size < 1 || vocab_size > (1 << 18))
         return fail(CSGMV_ERR_UNSUPPORTED, "vocab_size %d outside 1..2^18", vocab_size);
     if (accept_width < 1) return fail(CSGMV_ERR_INVALID_ARG, "accept_width must be positive");
+    if (accept_width > kMaxList) return fail(CSGMV_ERR_UNSUPPORTED, "accept_width exceeds 2^30");
     if (bs == 0) return CSGMV_OK;
     if (!tree_indptr || !sample_uniforms || !accept_index || !accept_len || !next_token || !status)
         return fail(CSGMV_ERR_INVALID_ARG, "NULL buffer");

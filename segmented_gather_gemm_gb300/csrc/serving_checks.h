@@ -33,6 +33,9 @@ bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
     return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
+// The longest list that a kernel's 32-bit index walks by steps of a CTA's threads.
+[[maybe_unused]] constexpr int kMaxList = 1 << 30;
+
 struct Dim {
     int64_t extent, stride;
 };

@@ -376,6 +376,7 @@ int csgmv_count_tokens(const csgmv_token_counts *counts, const int32_t *tokens, 
     if (!tokens || !tree_indptr) return fail(CSGMV_ERR_INVALID_ARG, "tokens / tree_indptr is NULL");
     if (accept_index && (accept_width <= 0 || !accept_len))
         return fail(CSGMV_ERR_INVALID_ARG, "accept_index needs a positive accept_width and accept_len");
+    if (accept_index && accept_width > kMaxList) return fail(CSGMV_ERR_UNSUPPORTED, "accept_width exceeds 2^30");
     const size_t b4 = 4 * (size_t)bs;
     const struct { const void *at; size_t bytes; } lists[] = {{tokens, 4 * (size_t)num_tokens},
                                                               {tree_indptr, b4 + 4},
@@ -429,6 +430,7 @@ int csgmv_process_logits(const void *logits, int dtype, int64_t logits_stride, c
     if (!known_type(dtype)) return fail(CSGMV_ERR_INVALID_ARG, "dtype %d must be bf16, f16 or f32", dtype);
     if (bs < 0 || num_tokens < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative bs / num_tokens");
     if (num_tokens >= (1 << 24)) return fail(CSGMV_ERR_UNSUPPORTED, "num_tokens exceeds 2^24 - 1");
+    if (bs > kMaxList) return fail(CSGMV_ERR_UNSUPPORTED, "bs exceeds 2^30");
     if (vocab_size < 1 || vocab_size > (1 << 18))
         return fail(CSGMV_ERR_UNSUPPORTED, "vocab_size %d outside 1..2^18", vocab_size);
     if (!rules || !rules->status || !aligned4(rules->status))
@@ -441,7 +443,7 @@ int csgmv_process_logits(const void *logits, int dtype, int64_t logits_stride, c
         if (counts->vocab_size != vocab_size)
             return fail(CSGMV_ERR_INVALID_ARG, "counts of %d tokens, logits of %d", counts->vocab_size, vocab_size);
     }
-    if (r.bias_total < 0 || r.bias_total > INT32_MAX) return fail(CSGMV_ERR_INVALID_ARG, "bias_total outside [0, 2^31)");
+    if (r.bias_total < 0 || r.bias_total > kMaxList) return fail(CSGMV_ERR_INVALID_ARG, "bias_total outside [0, 2^30]");
     if (r.bias_indptr && r.bias_total > 0 && (!r.bias_tokens || !r.bias_values))
         return fail(CSGMV_ERR_INVALID_ARG, "bias_tokens / bias_values is NULL");
     if (r.num_allow < 0) return fail(CSGMV_ERR_INVALID_ARG, "negative num_allow");
