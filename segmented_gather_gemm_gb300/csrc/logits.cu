@@ -17,10 +17,17 @@
 //
 // Measured (device time): 768 bf16 rows of 128256 (64 drafted trees with counts,
 // biases, a quarter of them with masks; 595 MB) 158 us; without any rule 108 us, 5.5
-// TB/s.  256 f32 rows of 100003 63 us, without rules 45 us.  A row's chain of dependent
-// loads and barriers (30000 clocks for a CTA, 12000 of them to find and score what is
-// sparse) is hidden by five CTAs an SM, f32 four (three above 102400 tokens): what holds it up is room
-// for more of them.  (Also tried: scores in f32 shared memory, three CTAs an SM,
+// TB/s; scores without softmax 93 us.  256 f32 rows of 100003 63 us, without rules 45 us.
+// A row's chain of dependent loads and barriers (27600 clocks for a CTA, 14400 of them to ask
+// for, find and score what is sparse) is hidden by the other CTAs of the SM: what holds
+// it up is room for more of them.  Of 16 bits there are five up to 139000 tokens, four up
+// to 184000, three up to 253000, then two.  Of f32 there are four where a row's share has
+// at most 12800 elements (up to 12800, 25600, 51200 or 102400 tokens in 1, 2, 4 or 8
+// CTAs), three of larger ones (16000, 32000, 65536, 128256), two from 139000, one from
+// 213000 on: 4.9 TB/s of 128256, 3.9 of 151936, 3.1 of 262144.  A sequence that holds more
+// tokens than the lists of a row's CTAs have room for costs passes over all bits: 2400
+// bf16 rows of 32000 (two CTAs) with none 87 us, with 1000 127, 2000 185, 3000 348, 8000
+// 1000; 600 of 128256 (eight) 91, 114, 135, 155 and 296.  (Also tried: scores in f32 shared memory, three CTAs an SM,
 // 286 us; the row read again from L2 with a test for each vector, 210 us; the list
 // in the order of the vocabulary by prefix sums, 172 us; 128 to 512 threads, 165 to
 // 190 us; exponents in one fused operation, 180 us, or two at a time, 170 us; one
@@ -41,8 +48,10 @@ constexpr int kPrompt = 1 << 30;
 constexpr int kMaxVocab = 1 << 18, kMaxCtas = 8;
 constexpr int kBlock = 512;  // elements; blocks of a row go to its CTAs in turn
 // Scores in a CTA's list; further ones wait in out.  f32 has fewer, and room for a
-// branch only where there is one: that lets a fourth CTA on an SM with rows of 100000 (256
-// of them 45 us, else 51).
+// branch only where there is one: then four CTAs are on an SM for shares of up to 12800
+// elements, with as many as 16 bits have for up to 11776 (256 rows of 100003, shares of
+// 12800: 45 us, else 51).  What it costs: 2400 rows of 32000 with 2000 tokens held 406 us,
+// bf16 185.
 template <typename T>
 constexpr int kKeptOf = sizeof(T) == 2 ? 1024 : 512;
 constexpr float kLargest = 3.402823466e+38f;

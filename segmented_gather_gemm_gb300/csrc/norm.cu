@@ -25,7 +25,10 @@
 // bf16 rows of 4096 (600 MB): 115 us, 5.2 TB/s, by their instructions: elements as halves
 // of words and a bias in the multiplication took it there from 3.9.  (Operations on
 // pairs of elements: no faster, and 17 us in place of 16: registers.)  Rows of 14336, a
-// CTA of 896 threads to an SM: 6.0 TB/s, f32 5.3.
+// CTA of 896 threads to an SM: 6.0 TB/s, f32 5.3, two norms 4.8, centred 3.6.  1.4 million rows
+// of 40: 3.8 TB/s, of 64, 128 and 256 5.7 (a vector a tensor under way in a thread, and a CTA
+// ends with its rows).  f32 rows of many elements spill at 64 registers (96 bytes, where they
+// begin anywhere 236), and so do the forms by elements (92 to 156).
 #include <algorithm>
 #include <atomic>
 
@@ -432,11 +435,13 @@ int layout_of(const AddNormParams &p) {
 
 // Whether the next row's inputs come beside a row's work.  That pays where a row has few
 // instructions for its bytes, or so many threads that little else is on the SM, and
-// where a CTA has four rows at least.  TB/s with and without, 600 MB of rows: bf16, one
-// norm, of 2048 5.9 and 6.0, of 4096 6.1 and 5.7, of 8192 6.6 and 5.3, of 14336 6.0 and 4.5; with an
-// f32 residual, of 4096 5.4 and 6.7, of 14336 6.0 and 5.8; two norms, of 4096 5.1 and 5.1, of 14336 4.7 and
-// 4.1, with gates 5.2 and 6.0, 4.8 and 4.4; f32, of 14336 4.6 and 5.3.  (us: 700 and 3000 rows of 4096
-// 5.1 and 4.7, 15.8 and 16.8.)
+// where a CTA has four rows at least.  TB/s with and without, 600 MB of bf16 rows: one norm, of
+// 2048 5.8 and 5.9, of 4096 6.0 and 5.5, of 8192 6.5 and 5.2, of 14336 6.0 and 4.4; with an f32
+// residual, of 4096 5.4 and 6.8, of 14336 6.1 and 6.2; two norms, of 4096 5.4 and 5.2 (centred 4.0
+// and 4.5), of 14336 4.8 and 4.2 (3.6 and 3.5).  f32 rows of 14336 4.6 and 5.3.  (us: 700 and 3000 rows
+// of 4096 5.1 and 4.7, 15.8 and 16.8.)  With a gate a token it pays for some and costs others, and none take
+// it: of 4096 one norm 5.9 and 6.0, two centred 4.5 and 5.2; of 14336 one norm 6.2 and 5.1, two 5.0 and
+// 4.8, centred 4.0 and 4.1, two with an f32 residual 5.2 and 5.5.
 template <typename T, typename R>
 bool ahead(const AddNormParams &p) {
     if (sizeof(T) != 2 || (p.gate && p.g_s)) return false;

@@ -11,7 +11,7 @@
 // turned is moved two vectors at a time too, or, in place, not touched.  One
 // head at a time, its angles from shared memory: more loads under way a thread, or
 // angles in registers, take room from the warps that hide loads (four heads: 220 us
-// where one takes 117, angles in shared memory 113; six CTAs an SM spill: 116).
+// where one took 117, angles in shared memory 113; six CTAs an SM spill: 116).
 //
 // Measured (device time): 35507 tokens of 32 + 8 heads of 128, bf16 (727 MB) 113 us,
 // 6.4 TB/s; with values into a layer's pages, 35700 tokens in half (880 MB) 136 us;
@@ -161,7 +161,7 @@ cudaError_t go(const RotaryParams &p, cudaStream_t stream) {
     if (s.units == 0) return cudaSuccess;  // all in place, nothing to turn
     const int heads = std::max(1, p.q.n + p.k.n + p.v.n);
     // A warp a token where there are enough of them to fill the GPU (35507 tokens of 40
-    // heads of 128: 117 us; twice as many threads a token 123, half as many 128); with
+    // heads of 128: 113 us; twice as many threads a token 113, half as many 116); with
     // fewer, more threads share a token's heads (12 of them: 3.0 us, with a warp each 4).
     const int64_t fill = 152 * 5 * kThreads / (p.num_tokens * s.units);
     s.lanes = (int)std::max<int64_t>(1, std::min<int64_t>({std::max<int64_t>(fill, 32 / s.units), heads, kThreads / s.units}));
